@@ -307,6 +307,113 @@ lr_status lr_attn_decode_noalloc(const lr_cache_desc* desc, int32_t len, const v
                                  const void* z_v, const void* B_k, const void* B_v,
                                  const void* q, void* out, float* lse, void* stream);
 
+/* ---- one latent for keys and values (the other low-rank form: K and V compressed jointly) -----
+ * A shared-latent cache holds, per token, ONE latent c of rank r and one rotary key kr of
+ * dim_rope elements shared by all heads.  KV head h's key is [c B_k,h | kr] (dim_nope +
+ * dim_rope elements) and its value c B_v,h (dim_v elements); query head j reads KV head
+ * j / (Hq/Hkv).  Next to lr_cache (two latents per token) this halves what a token costs at
+ * the same rank and keeps RoPE out of the compressed part.
+ *
+ * Storage is paged: token t of sequence b is row t % 128 of page table[b][t / 128].  The cache
+ * keeps no lengths: every call is told, in device memory, what it reads or writes, so all of
+ * them can be captured in a CUDA graph and replayed with other lengths, slots and pages.
+ * Work on one cache is ordered by the caller (one stream, or events between streams): its
+ * pages and the decode's scratch belong to the cache, so two decodes of ONE cache, graphs
+ * included, must not run at the same time.  Calls run on the device the cache was created on,
+ * whichever is current.
+ *
+ * 8 bits (quant_bits = 8): per group of 32 ranks the smallest power of two 2^e, e >= -100, with
+ * max|c| <= 448 * 2^e, and per element the nearest e4m3 value (ties to even) of c / 2^e.  What
+ * a code stands for is a bf16 value.  A group that holds a NaN or an infinity reads back as
+ * NaN throughout; magnitudes of 1.9375 * 2^127 and more read back as infinity.  kr stays bf16. */
+typedef struct lr_shared_desc {
+  int32_t batch;          /* B sequences, 1..1024                                  */
+  int32_t n_q_heads;      /* Hq, 1..128, a multiple of n_kv_heads                  */
+  int32_t n_kv_heads;     /* Hkv >= 1                                              */
+  int32_t dim_nope;       /* dn: 64 or 128, the key elements rebuilt from the latent */
+  int32_t dim_rope;       /* dr: 32 or 64, the rotary key elements                 */
+  int32_t dim_v;          /* dv: 64 or 128                                         */
+  int32_t rank;           /* r, a multiple of 64, 64..512                          */
+  int32_t capacity;       /* max tokens per sequence, a multiple of 128, <= 2^24   */
+  int32_t n_pages;        /* pages in the pool (0: batch * capacity / 128), <= 2^22 */
+  int32_t quant_bits;     /* 0 = latents in bf16; 8 = e4m3 with group scales       */
+  int32_t dtype;          /* LR_BF16 (LR_F32: LR_ERR_UNSUPPORTED)                  */
+  int32_t max_queries;    /* largest n_tokens of lr_shared_decode, 1..8            */
+  double rope_theta;      /* > 0: lr_shared_append rotates kr (rotate-half, position pos);
+                             0: kr arrives rotated                                 */
+  float softmax_scale;    /* 0 -> 1/sqrt(dim_nope + dim_rope)                      */
+  int32_t reserved[3];    /* must be zero                                          */
+} lr_shared_desc;
+
+typedef struct lr_shared lr_shared;   /* opaque */
+
+/* lr_shared_create — allocate a cache (zeroed pages; page (b * capacity/128 + j) % n_pages for
+ *   span j of sequence b) and copy the bases B_k [r][Hkv * dn], B_v [r][Hkv * dv] (bf16, device).
+ *   Errors as for lr_cache_create.  The decode's scratch is part of the cache: at most
+ *   (148 / k + batch) * Hq * max_queries rows (padded to 16 or 32 k) of r floats, k being the
+ *   blocks of 32 query rows of a sequence.  Blocks until the copies end.
+ * lr_shared_destroy — synchronise the device and free all memory.  NULL is a no-op. */
+lr_status lr_shared_create(const lr_shared_desc* desc, const void* B_k, const void* B_v, void* stream,
+                           lr_shared** out);
+lr_status lr_shared_destroy(lr_shared* cache);
+
+/* lr_shared_set_block_table / _device — the page of every 128-token span, [batch][capacity/128]
+ *   int32, from the host (every entry checked) or, capturable, from device memory (entries
+ *   outside the pool are clamped into it by every kernel).  As lr_cache_set_block_table. */
+lr_status lr_shared_set_block_table(lr_shared* cache, const int32_t* table, void* stream);
+lr_status lr_shared_set_block_table_device(lr_shared* cache, const int32_t* table, void* stream);
+
+/* lr_shared_append — write n tokens: token i goes to position pos[i] of sequence seq[i] ([n]
+ *   int32, device).  c: rows of r elements, c_stride elements apart (a multiple of 8, >= r;
+ *   c 16-byte aligned); kr: rows of dr elements, kr_stride apart (>= dr): both may be columns
+ *   of one wider array.  bf16, device.  A token whose seq or pos is out of range writes nothing
+ *   (a padded batch).  The slots of one call must differ: of two tokens with the same slot the
+ *   stored row is unspecified.
+ * lr_shared_read — read tokens back, packed: row cu[b] + i of c_out [total][r] and kr_out
+ *   [total][dr] (bf16, 16-byte aligned) is token start[b] + i of sequence b, for
+ *   i < cu[b + 1] - cu[b].  cu: [batch + 1] int32, device, ascending; start: [batch] int32,
+ *   device, or NULL for 0.  total (host) bounds the rows: rows at or past it, before cu[0] or
+ *   past cu[batch], and rows of positions outside [0, capacity), are left as they are. */
+lr_status lr_shared_append(lr_shared* cache, const void* c, int64_t c_stride, const void* kr, int64_t kr_stride,
+                           const int32_t* seq, const int32_t* pos, int32_t n, void* stream);
+lr_status lr_shared_read(lr_shared* cache, const int32_t* cu, const int32_t* start, int32_t total, void* c_out,
+                         void* kr_out, void* stream);
+
+/* lr_shared_decode — attention of n_tokens new query tokens per sequence over its stored
+ *   tokens, in rank space (keys and values are not rebuilt).  q [B][n_tokens][Hq][dn + dr]
+ *   (bf16, 16-byte aligned; the rotary part already rotated), row_len [B] int32, device: stored
+ *   tokens of each sequence, the new ones included (clamped to [0, capacity]).  Query token s
+ *   sees tokens t < row_len[b] - (n_tokens - 1 - s).  out [B][n_tokens][Hq][dv] bf16, lse
+ *   [B][n_tokens][Hq] fp32 (natural log) or NULL.  A query that sees no token gets out = 0,
+ *   lse = -inf.  What pages hold behind row_len has no influence.  n_tokens > max_queries:
+ *   LR_ERR_CAPACITY. */
+lr_status lr_shared_decode(lr_shared* cache, const void* q, int32_t n_tokens, const int32_t* row_len, void* out,
+                           float* lse, void* stream);
+
+/* lr_shared_expand — stored tokens as per-head keys and values, for prompts (many queries):
+ *   row cu[b] + i of k [total][Hkv][dn], v [total][Hkv][dv] and kr [total][dr] (bf16, 16-byte
+ *   aligned) is token start[b] + i of sequence b: k_h = c B_k,h, v_h = c B_v,h in fp32,
+ *   rounded once.  cu, start, total as for lr_shared_read.
+ * lr_shared_attn — attention of ragged queries over expanded keys and values: sequence b's
+ *   queries are rows cu_q[b]..cu_q[b+1]-1 of q [total_q][Hq][dn + dr], its keys and values rows
+ *   cu_k[b]..cu_k[b+1]-1 of k, v, kr (as lr_shared_expand writes them; n_seq sequences, 0..1024,
+ *   independent of the cache's batch; cu_*: [n_seq + 1] int32, device, ascending from 0).
+ *   causal = 1: query i of n sees keys j <= i + m - n of its m keys (the queries are the last n
+ *   tokens); 0: all m.  out [total_q][Hq][dv] bf16 (16-byte aligned), lse [total_q][Hq] fp32 or
+ *   NULL; a query that sees no key gets out = 0, lse = -inf; rows past cu_q[n_seq] are left as
+ *   they are.  Partial results over several key ranges join by their lse. */
+lr_status lr_shared_expand(lr_shared* cache, const int32_t* cu, const int32_t* start, int32_t total, void* k, void* v,
+                           void* kr, void* stream);
+lr_status lr_shared_attn(lr_shared* cache, const void* q, const void* k, const void* kr, const void* v,
+                         const int32_t* cu_q, const int32_t* cu_k, int32_t n_seq, int32_t total_q, int32_t total_k,
+                         int32_t causal, void* out, float* lse, void* stream);
+
+/* As lr_cache_set_wait_limit and lr_device_error, for a shared-latent cache's kernels. */
+lr_status lr_shared_set_wait_limit(lr_shared* cache, int64_t ns);
+lr_status lr_shared_device_error(lr_shared* cache, int32_t* code);
+/* sizeof(lr_shared_desc) as compiled (binding check). */
+int32_t lr_shared_desc_size(void);
+
 /* ---- bookkeeping ------------------------------------------------------------ */
 /* Current total length, history length and window length (host-side counters). */
 lr_status lr_cache_get_len(const lr_cache* cache, int32_t* len, int32_t* hist_len,

@@ -12,7 +12,11 @@ lr_cache_truncate, lr_cache_view_get, lr_cache_set_path, lr_cache_plan,
 lr_plan_decode, lr_cache_set_kernel_events, lr_cache_set_trace, lr_device_error, lr_abi_struct_sizes,
 lr_status_string, lr_launch_count, lr_attn_decode_noalloc, lr_cache_set_wait_limit,
 lr_debug_inject_fault, lr_attn_decode_varlen, lr_attn_decode_partial, lr_merge_partials,
-lr_kv_prefill, lr_cache_set_block_table, lr_cache_set_block_table_device, lr_kv_append_rows.
+lr_kv_prefill, lr_cache_set_block_table, lr_cache_set_block_table_device, lr_kv_append_rows;
+for caches with one latent for keys and values: lr_shared_create, lr_shared_destroy,
+lr_shared_set_block_table, lr_shared_set_block_table_device, lr_shared_append, lr_shared_read,
+lr_shared_decode, lr_shared_expand, lr_shared_attn, lr_shared_set_wait_limit,
+lr_shared_device_error, lr_shared_desc_size.
 """
 from __future__ import annotations
 
@@ -50,6 +54,16 @@ class lr_cache_view(ctypes.Structure):
                 ("groups_k", ctypes.c_int32), ("groups_v", ctypes.c_int32),
                 ("capacity", ctypes.c_int32), ("window_slots", ctypes.c_int32),
                 ("int4_blocks", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
+
+
+class lr_shared_desc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("dim_nope", ctypes.c_int32),
+                ("dim_rope", ctypes.c_int32), ("dim_v", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("capacity", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("quant_bits", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("max_queries", ctypes.c_int32), ("rope_theta", ctypes.c_double),
+                ("softmax_scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 3)]
 
 
 class lr_plan(ctypes.Structure):
@@ -97,6 +111,17 @@ def _load() -> ctypes.CDLL:
         "lr_kv_append_rows": [vp, vp, vp, vp, i32, vp],
         "lr_merge_partials": [vp, i32, vp, vp, vp, vp, vp],
         "lr_debug_inject_fault": [i32, ctypes.c_int64],
+        "lr_shared_create": [ctypes.POINTER(lr_shared_desc), vp, vp, vp, ctypes.POINTER(vp)],
+        "lr_shared_destroy": [vp],
+        "lr_shared_set_block_table": [vp, vp, vp],
+        "lr_shared_set_block_table_device": [vp, vp, vp],
+        "lr_shared_append": [vp, vp, ctypes.c_int64, vp, ctypes.c_int64, vp, vp, i32, vp],
+        "lr_shared_read": [vp, vp, vp, i32, vp, vp, vp],
+        "lr_shared_decode": [vp, vp, i32, vp, vp, vp, vp],
+        "lr_shared_expand": [vp, vp, vp, i32, vp, vp, vp, vp],
+        "lr_shared_attn": [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp],
+        "lr_shared_set_wait_limit": [vp, ctypes.c_int64],
+        "lr_shared_device_error": [vp, ctypes.POINTER(i32)],
         "lr_attn_decode_noalloc": [ctypes.POINTER(lr_cache_desc), i32, vp, vp, vp, vp, vp, vp, vp, vp],
     }
     for name, args in sig.items():
@@ -107,6 +132,8 @@ def _load() -> ctypes.CDLL:
     lib.lr_status_string.restype = ctypes.c_char_p
     lib.lr_abi_struct_sizes.argtypes = [ctypes.POINTER(i32)] * 3
     lib.lr_abi_struct_sizes.restype = None
+    lib.lr_shared_desc_size.argtypes = []
+    lib.lr_shared_desc_size.restype = i32
     lib.lr_launch_count.argtypes = []
     lib.lr_launch_count.restype = ctypes.c_int64
     return lib
@@ -371,6 +398,188 @@ def lr_attn_decode_noalloc(desc: lr_cache_desc, length: int, z_k, z_v, B_k, B_v,
                                        _ptr(q, dt, shp, "q"), _ptr(out, dt, shp, "out"),
                                        _ptr(lse, torch.float32, (desc.batch, desc.n_q_heads), "lse", True),
                                        _stream(stream)), "lr_attn_decode_noalloc")
+
+
+# ---------------------------------------------------------------------------
+# one latent for keys and values
+# ---------------------------------------------------------------------------
+
+def make_shared_desc(batch: int, n_q_heads: int, n_kv_heads: int, dim_nope: int, dim_rope: int,
+                     dim_v: int, rank: int, capacity: int, n_pages: int = 0, quant_bits: int = 0,
+                     dtype: int = LR_BF16, max_queries: int = 1, rope_theta: float = 0.0,
+                     softmax_scale: float = 0.0) -> lr_shared_desc:
+    return lr_shared_desc(batch, n_q_heads, n_kv_heads, dim_nope, dim_rope, dim_v, rank, capacity,
+                          n_pages, quant_bits, dtype, max_queries, rope_theta, softmax_scale)
+
+
+class SharedCache:
+    """Handle of one lr_shared (one layer) on one device.  Holds the description for shape checks."""
+
+    def __init__(self, handle: ctypes.c_void_p, desc: lr_shared_desc, device: int):
+        self.handle = handle
+        self.desc = desc
+        self.device = device
+
+    def __del__(self):
+        if getattr(self, "handle", None):
+            try:
+                _lib.lr_shared_destroy(self.handle)
+            except Exception:
+                pass
+            self.handle = None
+
+
+def _shared_ptr(cache: SharedCache, t, dtype, shape, name, allow_none=False):
+    p = _ptr(t, dtype, shape, name, allow_none)
+    if t is not None and t.device.index != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.device}")
+    return p
+
+
+def _shared_stream(cache: SharedCache, stream) -> ctypes.c_void_p:
+    import torch
+    s = torch.cuda.current_stream(cache.device) if stream is None else stream
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def _shared_rows(cache: SharedCache, t, width: int, n: int, name: str):
+    """Pointer and row stride of a [n][width] bf16 tensor whose rows may be spaced."""
+    import torch
+    if not getattr(t, "is_cuda", False) or t.device.index != cache.device:
+        raise ValueError(f"{name} must be a tensor on cuda:{cache.device}")
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (n, width):
+        raise ValueError(f"{name} has dtype {t.dtype} and shape {tuple(t.shape)}, expected bfloat16 {(n, width)}")
+    if t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if n > 1 else width)
+
+
+def lr_shared_create(desc: lr_shared_desc, B_k, B_v, stream=None) -> SharedCache:
+    """B_k: bf16 CUDA tensor [rank][Hkv * dim_nope], B_v: [rank][Hkv * dim_v]."""
+    import torch
+    dt, out = _torch_dtype(desc.dtype), ctypes.c_void_p()
+    bk = _ptr(B_k, dt, (desc.rank, desc.n_kv_heads * desc.dim_nope), "B_k")
+    bv = _ptr(B_v, dt, (desc.rank, desc.n_kv_heads * desc.dim_v), "B_v")
+    if B_v.device != B_k.device:
+        raise ValueError("B_k and B_v must be on one device")
+    with torch.cuda.device(B_k.device):
+        _check(_lib.lr_shared_create(ctypes.byref(desc), bk, bv, _stream(stream), ctypes.byref(out)),
+               "lr_shared_create")
+    return SharedCache(out, desc, B_k.device.index)
+
+
+def lr_shared_destroy(cache: SharedCache) -> None:
+    if cache.handle:
+        _check(_lib.lr_shared_destroy(cache.handle), "lr_shared_destroy")
+        cache.handle = None
+
+
+def lr_shared_set_block_table(cache: SharedCache, table, stream=None) -> None:
+    """table: host array-like of int32, [batch][capacity / 128]."""
+    import numpy as np
+    d = cache.desc
+    t = np.ascontiguousarray(np.asarray(table), dtype=np.int32)
+    if t.shape != (d.batch, d.capacity // 128):
+        raise ValueError(f"table must be [{d.batch}][{d.capacity // 128}], got {t.shape}")
+    _check(_lib.lr_shared_set_block_table(cache.handle, t.ctypes.data_as(ctypes.c_void_p),
+                                          _shared_stream(cache, stream)), "lr_shared_set_block_table")
+
+
+def lr_shared_set_block_table_device(cache: SharedCache, table, stream=None) -> None:
+    """table: int32 CUDA tensor [batch][capacity / 128] (entries are not checked; the kernels
+    clamp them into the pool)."""
+    import torch
+    d = cache.desc
+    _check(_lib.lr_shared_set_block_table_device(
+        cache.handle, _shared_ptr(cache, table, torch.int32, (d.batch, d.capacity // 128), "table"),
+        _shared_stream(cache, stream)), "lr_shared_set_block_table_device")
+
+
+def lr_shared_append(cache: SharedCache, c, kr, seq, pos, stream=None) -> None:
+    """c: bf16 CUDA tensor [n][rank], kr: [n][dim_rope] (rows may be spaced: columns of a wider
+    tensor); seq, pos: int32 CUDA tensors [n], the sequence and position of each token."""
+    import torch
+    n = c.shape[0]
+    cp, cs = _shared_rows(cache, c, cache.desc.rank, n, "c")
+    kp, ks = _shared_rows(cache, kr, cache.desc.dim_rope, n, "kr")
+    _check(_lib.lr_shared_append(cache.handle, cp, cs, kp, ks,
+                                 _shared_ptr(cache, seq, torch.int32, (n,), "seq"),
+                                 _shared_ptr(cache, pos, torch.int32, (n,), "pos"), n,
+                                 _shared_stream(cache, stream)), "lr_shared_append")
+
+
+def lr_shared_read(cache: SharedCache, cu, c_out, kr_out, start=None, stream=None) -> None:
+    """cu: int32 CUDA tensor [batch + 1], first packed row of every sequence; start: [batch] first
+    token of every sequence, or None; c_out: bf16 [total][rank], kr_out: [total][dim_rope]."""
+    import torch
+    d, n = cache.desc, c_out.shape[0]
+    _check(_lib.lr_shared_read(cache.handle, _shared_ptr(cache, cu, torch.int32, (d.batch + 1,), "cu"),
+                               _shared_ptr(cache, start, torch.int32, (d.batch,), "start", True), n,
+                               _shared_ptr(cache, c_out, torch.bfloat16, (n, d.rank), "c_out"),
+                               _shared_ptr(cache, kr_out, torch.bfloat16, (n, d.dim_rope), "kr_out"),
+                               _shared_stream(cache, stream)), "lr_shared_read")
+
+
+def lr_shared_decode(cache: SharedCache, q, row_len, out, lse=None, stream=None) -> None:
+    """q: bf16 CUDA tensor [batch][n_tokens][Hq][dim_nope + dim_rope]; row_len: int32 [batch];
+    out: bf16 [batch][n_tokens][Hq][dim_v]; lse: fp32 [batch][n_tokens][Hq] or None."""
+    import torch
+    d = cache.desc
+    n = q.shape[1] if q.dim() == 4 else -1
+    _check(_lib.lr_shared_decode(
+        cache.handle, _shared_ptr(cache, q, torch.bfloat16, (d.batch, n, d.n_q_heads, d.dim_nope + d.dim_rope), "q"), n,
+        _shared_ptr(cache, row_len, torch.int32, (d.batch,), "row_len"),
+        _shared_ptr(cache, out, torch.bfloat16, (d.batch, n, d.n_q_heads, d.dim_v), "out"),
+        _shared_ptr(cache, lse, torch.float32, (d.batch, n, d.n_q_heads), "lse", True),
+        _shared_stream(cache, stream)), "lr_shared_decode")
+
+
+def lr_shared_expand(cache: SharedCache, cu, k, v, kr, start=None, stream=None) -> None:
+    """cu, start: as for lr_shared_read; k: bf16 CUDA tensor [total][Hkv][dim_nope],
+    v: [total][Hkv][dim_v], kr: [total][dim_rope]."""
+    import torch
+    d, n = cache.desc, k.shape[0]
+    _check(_lib.lr_shared_expand(
+        cache.handle, _shared_ptr(cache, cu, torch.int32, (d.batch + 1,), "cu"),
+        _shared_ptr(cache, start, torch.int32, (d.batch,), "start", True), n,
+        _shared_ptr(cache, k, torch.bfloat16, (n, d.n_kv_heads, d.dim_nope), "k"),
+        _shared_ptr(cache, v, torch.bfloat16, (n, d.n_kv_heads, d.dim_v), "v"),
+        _shared_ptr(cache, kr, torch.bfloat16, (n, d.dim_rope), "kr"),
+        _shared_stream(cache, stream)), "lr_shared_expand")
+
+
+def lr_shared_attn(cache: SharedCache, q, k, kr, v, cu_q, cu_k, out, lse=None, causal: bool = True,
+                   stream=None) -> None:
+    """q: bf16 CUDA tensor [total_q][Hq][dim_nope + dim_rope]; k, kr, v: as lr_shared_expand writes
+    them; cu_q, cu_k: int32 [n_seq + 1]; out: bf16 [total_q][Hq][dim_v]; lse: fp32 [total_q][Hq]
+    or None."""
+    import torch
+    d = cache.desc
+    nq, nk, ns = q.shape[0], k.shape[0], cu_q.shape[0] - 1
+    _check(_lib.lr_shared_attn(
+        cache.handle, _shared_ptr(cache, q, torch.bfloat16, (nq, d.n_q_heads, d.dim_nope + d.dim_rope), "q"),
+        _shared_ptr(cache, k, torch.bfloat16, (nk, d.n_kv_heads, d.dim_nope), "k"),
+        _shared_ptr(cache, kr, torch.bfloat16, (nk, d.dim_rope), "kr"),
+        _shared_ptr(cache, v, torch.bfloat16, (nk, d.n_kv_heads, d.dim_v), "v"),
+        _shared_ptr(cache, cu_q, torch.int32, (ns + 1,), "cu_q"),
+        _shared_ptr(cache, cu_k, torch.int32, (ns + 1,), "cu_k"), ns, nq, nk, int(bool(causal)),
+        _shared_ptr(cache, out, torch.bfloat16, (nq, d.n_q_heads, d.dim_v), "out"),
+        _shared_ptr(cache, lse, torch.float32, (nq, d.n_q_heads), "lse", True),
+        _shared_stream(cache, stream)), "lr_shared_attn")
+
+
+def lr_shared_set_wait_limit(cache: SharedCache, ns: int = 0) -> None:
+    _check(_lib.lr_shared_set_wait_limit(cache.handle, int(ns)), "lr_shared_set_wait_limit")
+
+
+def lr_shared_device_error(cache: SharedCache) -> int:
+    code = ctypes.c_int32()
+    _check(_lib.lr_shared_device_error(cache.handle, ctypes.byref(code)), "lr_shared_device_error")
+    return code.value
+
+
+def lr_shared_desc_size() -> int:
+    return int(_lib.lr_shared_desc_size())
 
 
 def lr_cache_get_len(cache: Cache):

@@ -1,0 +1,114 @@
+// Internal definitions of the shared-latent cache (lr_shared_* in include/lr_kv.h): one latent
+// and one rotary key per token, from which every head's key and value follow.
+#pragma once
+
+#include "lr_internal.cuh"
+
+// Rows of the stored arrays are page * 128 + token % 128, page = table[b][token / 128].
+struct lr_shared {
+  lr_shared_desc desc;
+  int R_max;             // query rows per sequence at max_queries (max_queries * Hq)
+  int pps, n_pages;      // pages per sequence, pages in the pool
+  float scale_log2;      // softmax_scale * log2(e)
+  int num_sms = 148, device = 0;
+  cudaStream_t last_stream = nullptr;
+  unsigned long long wait_ns = 0;
+  std::vector<int32_t> host_table;
+
+  void* c = nullptr;          // [rows][r] bf16, or e4m3 codes
+  uint8_t* scale = nullptr;   // 8 bits: [n_pages][ceil(r/128)][128][4] exponent bytes (shared_scale_index)
+  void* kr = nullptr;         // [rows][dr] bf16
+  int32_t* table = nullptr;   // [B][pps]
+  void* B_k = nullptr;        // [r][Hkv*dn]
+  void* B_v = nullptr;        // [r][Hkv*dv]
+  float2* rope_cs = nullptr;  // [capacity][dr/2] (cos, sin), or null
+  void* qt = nullptr;         // decode: query latents, hi and lo halves (k_shared_decode.cu)
+  float* part_o = nullptr;    // decode: split partials [slots][rows][r]
+  float* part_ml = nullptr;   // decode: [slots][rows][4] = m, l, l of the rounded weights, 0
+  int* dev_err = nullptr;
+};
+
+inline RowMap row_map(const lr_shared* c) {
+  RowMap m;
+  m.table = c->table;
+  m.cap = c->desc.capacity;
+  m.pps = c->pps;
+  m.n_pages = c->n_pages;
+  return m;
+}
+
+// The exponent byte (2^(byte - 127); 255: a group that held a NaN or an infinity) of ranks
+// 32 g .. 32 g + 31 of a stored row.  A page's bytes of 128 ranks are contiguous, so that a
+// tile side's scales are one 512-byte copy.
+__host__ __device__ __forceinline__ long long shared_scale_index(long long row, int r, int g) {
+  return ((((row >> 7) * ((r + 127) >> 7) + (g >> 2)) << 7) + (row & 127)) * 4 + (g & 3);
+}
+
+// 2^(byte - 127) as a float; NaN for 255.  Bytes are 27..247 (shared_quant).
+__device__ __forceinline__ float shared_pow2(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7FC00000u : byte << 23);
+}
+
+// Work of the paged kernels: the 128-token tiles of all sequences in order, cut into equal
+// runs, run x for CTA column x of X.  A run may span several sequences, and a sequence
+// several runs; (x, b) pairs form a staircase, so x + b numbers them without gaps in use.
+struct TileRun {
+  int b, tile, left;   // first sequence, first tile in it, tiles in the run
+};
+__device__ __forceinline__ int shared_len(const int32_t* row_len, int b, int cap) {
+  return min(max(__ldg(row_len + b), 0), cap);
+}
+
+// By one whole warp: the tile total of B sequences (len(b) tokens each) and run x.
+template <typename Len>
+__device__ __forceinline__ TileRun tile_run(Len len, int B, int X, int x, int* chunk_out) {
+  const int lane = threadIdx.x & 31;
+  int total = 0;
+  for (int i = lane; i < B; i += 32) total += (len(i) + 127) >> 7;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int chunk = max(1, (total + X - 1) / X);
+  *chunk_out = chunk;
+  const long long want = (long long)x * chunk;
+  TileRun r{B, 0, 0};
+  if (want >= total) return r;
+  const int begin = (int)want;
+  r.left = min(chunk, total - begin);
+  int run = 0;
+  for (int base = 0; base < B; base += 32) {
+    const int i = base + lane;
+    const int v = i < B ? (len(i) + 127) >> 7 : 0;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, run + inc > begin);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.b = base + src;
+      r.tile = begin - __shfl_sync(0xffffffffu, run + inc - v, src);
+      return r;
+    }
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return r;
+}
+
+// Host side of each operator (checks done by shared_api.cu).
+cudaError_t launch_shared_rope_table(lr_shared* c, cudaStream_t s);
+cudaError_t launch_shared_append(lr_shared* c, const void* z, long long z_stride, const void* kr, long long kr_stride,
+                                 const int32_t* seq, const int32_t* pos, int n, cudaStream_t s);
+cudaError_t launch_shared_read(lr_shared* c, const int32_t* cu, const int32_t* start, int total, void* z, void* kr,
+                               cudaStream_t s);
+cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, const int32_t* row_len, void* out,
+                                 float* lse, cudaStream_t s);
+cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t* start, int total, void* k, void* v,
+                                 void* kr, cudaStream_t s);
+cudaError_t launch_shared_attn(lr_shared* c, const void* q, const void* k, const void* kr, const void* v,
+                               const int32_t* cu_q, const int32_t* cu_k, int nseq, int total_q, int total_k,
+                               int causal, void* out, float* lse, cudaStream_t s);
+// Scratch of the decode, in bytes, for any n_tokens up to max_queries.
+size_t shared_qt_bytes(const lr_shared_desc* d);
+void shared_part_rows(const lr_shared_desc* d, int num_sms, size_t* rows);

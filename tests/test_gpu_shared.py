@@ -1,0 +1,449 @@
+"""Shared-latent caches on the GPU against the fp64 oracle: writing and reading back (bf16 exact,
+8-bit codes exact), the absorbed decode, expansion and ragged attention, at the lengths, page
+boundaries, head layouts and masks where they can go wrong; refusals; streams and graphs.
+
+Tolerances come from the arithmetic (u = 2^-8, half a bf16 step; fp32 half step 2^-24)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import shared as S
+
+pytestmark = pytest.mark.gpu
+
+U, F = 2.0 ** -8, 2.0 ** -24
+
+
+def bf16(x):
+    import torch
+    return torch.tensor(np.asarray(x), dtype=torch.float32).to(torch.bfloat16).cuda()
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def i32(x):
+    import torch
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+class Layer:
+    """A cache filled with seeded tokens through a permuted page table, and its fp64 contents."""
+
+    def __init__(self, lib, lens, hq=4, hkv=4, dn=128, dr=64, dv=128, r=128, bits=0, new=1, cap=None, seed=0,
+                 theta=0.0, spare=2, stale=True, scale=0.0):
+        import torch
+        rng = np.random.default_rng(seed)
+        self.lib, self.lens, B = lib, list(lens), len(lens)
+        self.hq, self.hkv, self.dn, self.dr, self.dv, self.r, self.bits = hq, hkv, dn, dr, dv, r, bits
+        cap = cap or max(128, -(-max(lens) // 128) * 128)
+        self.cap, pps = cap, cap // 128
+        n_pages = B * pps + spare
+        self.desc = lib.make_shared_desc(B, hq, hkv, dn, dr, dv, r, cap, n_pages=n_pages, quant_bits=bits,
+                                         max_queries=new, rope_theta=theta, softmax_scale=scale)
+        self.scale = scale or (dn + dr) ** -0.5
+        sp = np.arange(1, r + 1) ** -0.3
+        self.Bk, self.Bv = bf16(rng.standard_normal((r, hkv * dn)) / r ** 0.5), bf16(
+            rng.standard_normal((r, hkv * dv)) / r ** 0.5)
+        self.cache = lib.lr_shared_create(self.desc, self.Bk, self.Bv)
+        self.table = rng.permutation(n_pages)[:B * pps].reshape(B, pps).astype(np.int32)
+        if stale:                      # every row of the pool first holds non-finite leftovers
+            junk = bf16(np.full((cap, r), np.inf)), bf16(np.full((cap, dr), np.nan))
+            for k in range(0, n_pages, pps):
+                t = (np.arange(B * pps) % n_pages + k) % n_pages
+                lib.lr_shared_set_block_table(self.cache, t.reshape(B, pps).astype(np.int32))
+                lib.lr_shared_append(self.cache, *junk, i32(np.zeros(cap)), i32(np.arange(cap)))
+        lib.lr_shared_set_block_table(self.cache, self.table)
+        n = sum(lens)
+        self.c = bf16(rng.standard_normal((n, r)) * sp * 1.5)
+        self.kr = bf16(rng.standard_normal((n, dr)))
+        seq = np.repeat(np.arange(B), lens)
+        pos = np.concatenate([np.arange(x) for x in lens]) if n else np.zeros(0)
+        if n:
+            lib.lr_shared_append(self.cache, self.c, self.kr, i32(seq), i32(pos))
+        self.cu = np.concatenate([[0], np.cumsum(lens)])
+        c = f64(self.c)
+        self.c64 = S.quantize_e4m3(c) if bits else c
+        self.kr64 = S.rotate(f64(self.kr), pos, theta)
+        self.Bk64, self.Bv64 = f64(self.Bk), f64(self.Bv)
+        self.rng = rng
+        torch.cuda.synchronize()
+
+    def rows(self, b):
+        return slice(self.cu[b], self.cu[b + 1])
+
+    def query(self, n_tok, amp=1.5):
+        return bf16(self.rng.standard_normal((len(self.lens), n_tok, self.hq, self.dn + self.dr)) * amp)
+
+    def decode(self, q, lens=None):
+        import torch
+        B, n = q.shape[:2]
+        out = torch.full((B, n, self.hq, self.dv), 777.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((B, n, self.hq), 777.0, dtype=torch.float32, device="cuda")
+        self.lib.lr_shared_decode(self.cache, q, i32(self.lens if lens is None else lens), out, lse)
+        torch.cuda.synchronize()
+        assert self.lib.lr_shared_device_error(self.cache) == 0
+        return out, lse
+
+    def check_decode(self, q, out, lse, lens=None):
+        """out and lse against the oracle, within what the roundings can add up to.
+
+        Scores: q~ has K = dn fp32 steps, then two bf16 halves (residual u^2 of it), the dot product
+        r + dr fp32 steps: E = scale ((u^2 + (dn + r + dr + 8) F) sum |q~_i c_i|-like terms); log2
+        and exp2 in fp32 add 2^-20 of the score.  Weights: one bf16 rounding (u) in the numerator
+        and in the normaliser.  Rank-space sums: (T + r + 64) F and the split halves u^2 of
+        sum_i (sum_t p |c_ti|) |B_i|.  The output: u of its value."""
+        n_tok = q.shape[1]
+        q64, g = f64(q), self.hq // self.hkv
+        lens = self.lens if lens is None else lens
+        for b, n in enumerate(lens):
+            c, kr = self.c64[self.rows(b)][:n], self.kr64[self.rows(b)][:n]
+            ro, rl, mix = S.attention(q64[b], S.expand(c, self.Bk64, self.hkv), kr, S.expand(c, self.Bv64, self.hkv),
+                                      self.scale)
+            if self.rope_stored:
+                kr_err = U * np.abs(kr)
+            for s in range(n_tok):
+                seen = n - (n_tok - 1 - s)
+                go, gl = f64(out[b, s]), f64(lse[b, s])
+                if seen <= 0:
+                    assert np.all(go == 0) and np.all(np.isneginf(gl)), (b, s)
+                    continue
+                for j in range(self.hq):
+                    h = j // g
+                    Bk, Bv = self.Bk64[:, h * self.dn:(h + 1) * self.dn], self.Bv64[:, h * self.dv:(h + 1) * self.dv]
+                    aq = np.abs(Bk) @ np.abs(q64[b, s, j, :self.dn])
+                    mag = np.abs(c[:seen]) @ aq + np.abs(kr[:seen]) @ np.abs(q64[b, s, j, self.dn:])
+                    E = self.scale * (U * U + (self.dn + self.r + self.dr + 8) * F) * mag.max() + 2.0 ** -20 * (
+                        self.scale * mag.max())
+                    if self.rope_stored:
+                        E += self.scale * (kr_err[:seen] @ np.abs(q64[b, s, j, self.dn:])).max()
+                    assert abs(gl[j] - rl[s, j]) <= E + (seen + 64) * F + 2.0 ** -21 * abs(rl[s, j]), (b, s, j)
+                    w = np.exp(self.scale * (c[:seen] @ (Bk @ q64[b, s, j, :self.dn]) + kr[:seen] @ q64[
+                        b, s, j, self.dn:]) - rl[s, j])
+                    A = (w @ np.abs(c[:seen])) @ np.abs(Bv)
+                    tol = U * np.abs(ro[s, j]) + (2 * U + 2 * E) * mix[s, j] + (U * U + (seen + self.r + 64) * F) * A
+                    err = np.abs(go[j] - ro[s, j])
+                    assert np.all(err <= tol), (b, s, j, (err / tol).max())
+
+    rope_stored = False
+
+
+# ---------------------------------------------------------------------------
+# write and read back
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [0, 8])
+@pytest.mark.parametrize("r,dr", [(64, 32), (192, 64), (512, 64)])
+def test_write_reads_back_what_it_stands_for(lib, bits, r, dr):
+    import torch
+    lens = [1, 127, 128, 129, 300]
+    m = Layer(lib, lens, r=r, dr=dr, bits=bits, theta=1e4)
+    c = torch.full((sum(lens) + 3, r), 5.0, dtype=torch.bfloat16, device="cuda")
+    kr = torch.full((sum(lens) + 3, dr), 5.0, dtype=torch.bfloat16, device="cuda")
+    lib.lr_shared_read(m.cache, i32(m.cu), c, kr)
+    assert np.array_equal(f64(c)[:-3], m.c64)
+    a = np.abs(f64(m.kr))
+    pair = np.concatenate([a[:, :dr // 2] + a[:, dr // 2:]] * 2, axis=1)
+    assert np.all(np.abs(f64(kr)[:-3] - m.kr64) <= U * np.abs(m.kr64) + 4 * F * pair)
+    assert np.all(f64(c)[-3:] == 5) and np.all(f64(kr)[-3:] == 5)   # behind the last sequence: untouched
+
+
+def test_every_code_and_extreme_groups(lib):
+    """All finite e4m3 values at several scales, and groups at the edges of the range."""
+    import torch
+    vals = S.e4m3_values()
+    rows = []
+    for e in (-100, -60, -7, 0, 7, 60, 112):
+        x = np.zeros(256)
+        x[:127], x[128:255] = vals, -vals
+        x = x.reshape(8, 32).copy()
+        x[:, 31] = 448.0                                       # pins every group's scale to 2^e
+        rows.append((x * 2.0 ** e).reshape(-1))
+    rows.append(np.full(256, 2.0 ** -126))                     # below the smallest scale's normal codes
+    top = np.zeros(256)
+    top[::32] = 2.0 ** 127
+    rows.append(top)
+    bad = np.ones(256)
+    bad[[3, 70, 140]] = np.inf, np.nan, -np.inf
+    rows.append(bad)
+    x = bf16(np.array(rows))
+    d = lib.make_shared_desc(1, 1, 1, 64, 32, 64, 256, 128, quant_bits=8)
+    cache = lib.lr_shared_create(d, bf16(np.zeros((256, 64))), bf16(np.zeros((256, 64))))
+    n = len(rows)
+    kr = bf16(np.zeros((n, 32)))
+    lib.lr_shared_append(cache, x, kr, i32(np.zeros(n)), i32(np.arange(n)))
+    c, k = torch.zeros_like(x), torch.zeros_like(kr)
+    lib.lr_shared_read(cache, i32([0, n]), c, k)
+    want = S.quantize_e4m3(f64(x))
+    assert np.array_equal(f64(c)[:7], f64(x)[:7])              # every value is its own code
+    assert np.array_equal(f64(c), want, equal_nan=True)
+
+
+def test_far_positions_rotate_with_exact_angles(lib):
+    import torch
+    d = lib.make_shared_desc(1, 1, 1, 64, 64, 64, 64, 1 << 20, n_pages=3, rope_theta=1e6)
+    cache = lib.lr_shared_create(d, bf16(np.zeros((64, 64))), bf16(np.zeros((64, 64))))
+    pos = np.array([0, 1, 999_999, (1 << 20) - 1])
+    table = np.zeros((1, 8192), np.int32)
+    table[0, 999_999 // 128], table[0, -1] = 1, 2
+    lib.lr_shared_set_block_table(cache, table)
+    kr = bf16(np.random.default_rng(0).standard_normal((4, 64)))
+    lib.lr_shared_append(cache, bf16(np.zeros((4, 64))), kr, i32(np.zeros(4)), i32(pos))
+    want = S.rotate(f64(kr), pos, 1e6)
+    for i, p in enumerate(pos):
+        c, k = torch.zeros((1, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros_like(kr[:1])
+        lib.lr_shared_read(cache, i32([0, 1]), c, k, start=i32([p]))
+        assert np.all(np.abs(f64(k)[0] - want[i]) <= U * np.abs(want[i]) + 1e-6)
+
+
+def test_spaced_rows_padding_and_partial_reads(lib):
+    """Columns of one wider projection output as c and kr; padded tokens write nothing; reads that
+    start inside a page, skip sequences, and run past what may be read."""
+    import torch
+    rng = np.random.default_rng(3)
+    d = lib.make_shared_desc(3, 2, 2, 64, 32, 64, 128, 256)
+    cache = lib.lr_shared_create(d, bf16(np.zeros((128, 128))), bf16(np.zeros((128, 128))))
+    wide = bf16(rng.standard_normal((40, 8 + 128 + 32 + 8)))
+    c, kr = wide[:, 8:136], wide[:, 136:168]
+    seq = np.array([0, 2] * 20)
+    pos = np.arange(40) // 2 + 120                             # crosses a page
+    seq[4], seq[5], pos[6], pos[7] = -1, 3, -1, 256            # padding of each kind
+    lib.lr_shared_append(cache, c, kr, i32(seq), i32(pos))
+    got_c = torch.full((30, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    got_k = torch.full((30, 32), 9.0, dtype=torch.bfloat16, device="cuda")
+    # sequence 0: tokens 120..139; sequence 1: none; sequence 2: tokens 250..259, six of them past the capacity
+    lib.lr_shared_read(cache, i32([2, 22, 22, 32]), got_c, got_k, start=i32([120, 0, 250]))
+    g, k = f64(got_c), f64(got_k)
+    assert np.all(g[:2] == 9) and np.all(k[:2] == 9)
+    for t in range(20):
+        i = 2 * t
+        want = (f64(c)[i], f64(kr)[i]) if i not in (4, 6) else (np.zeros(128), np.zeros(32))
+        assert np.array_equal(g[2 + t], want[0]) and np.array_equal(k[2 + t], want[1]), t
+    assert np.all(g[22:28] == 0) and np.all(g[28:] == 9) and np.all(k[28:] == 9)
+
+
+# ---------------------------------------------------------------------------
+# decode
+# ---------------------------------------------------------------------------
+
+LENS = [0, 1, 2, 127, 128, 129, 300, 517]
+
+
+@pytest.mark.parametrize("bits", [0, 8])
+@pytest.mark.parametrize("hq,hkv,r,dn,dr,dv,new", [
+    (4, 4, 128, 128, 64, 128, 1), (28, 4, 256, 128, 64, 128, 1), (28, 28, 512, 128, 64, 128, 1),
+    (16, 1, 64, 64, 32, 64, 1), (5, 5, 192, 128, 32, 64, 3), (40, 8, 448, 64, 64, 128, 2), (1, 1, 320, 64, 32, 128, 8)])
+def test_decode_matches_the_oracle(lib, bits, hq, hkv, r, dn, dr, dv, new):
+    m = Layer(lib, LENS, hq=hq, hkv=hkv, r=r, dn=dn, dr=dr, dv=dv, bits=bits, new=new)
+    q = m.query(new)
+    m.check_decode(q, *m.decode(q))
+
+
+@pytest.mark.parametrize("bits", [0, 8])
+def test_decode_many_heads_and_uneven_lengths(lib, bits):
+    m = Layer(lib, [1500, 3, 0, 900], hq=128, hkv=128, r=128, bits=bits, new=2, dn=64, dv=64)
+    q = m.query(2)
+    m.check_decode(q, *m.decode(q))
+
+
+def test_decode_long_context_over_many_splits(lib):
+    m = Layer(lib, [20000, 5], hq=6, hkv=3, r=128, bits=8)
+    q = m.query(1)
+    m.check_decode(q, *m.decode(q))
+
+
+def test_decode_of_rotated_keys_and_own_scale(lib):
+    m = Layer(lib, [200, 129], r=128, theta=1e4, scale=0.21)
+    m.rope_stored = True
+    q = m.query(1)
+    m.check_decode(q, *m.decode(q))
+
+
+@pytest.mark.parametrize("amp", [0.0, 30.0])
+def test_decode_equal_and_sharp_weights(lib, amp):
+    m = Layer(lib, [700, 128], hq=16, hkv=16, r=256)
+    q = m.query(1, amp)
+    m.check_decode(q, *m.decode(q))
+
+
+def test_decode_shorter_lengths_and_clamping(lib):
+    """row_len picks a prefix; values outside 0..capacity are clamped."""
+    import torch
+    m = Layer(lib, [300, 384, 10])
+    q = m.query(1)
+    m.check_decode(q, *m.decode(q, [17, 384, 0]), lens=[17, 384, 0])
+    a, b = m.decode(q, [300, 9999, -4]), m.decode(q, [300, 384, 0])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_decode_without_lse_and_twice_the_same(lib):
+    import torch
+    m = Layer(lib, [513, 77, 1000], hq=28, hkv=28, r=512)
+    q = m.query(1)
+    a = m.decode(q)
+    out = torch.zeros_like(a[0])
+    lib.lr_shared_decode(m.cache, q, i32(m.lens), out)
+    assert torch.equal(out, a[0])
+    b = m.decode(q)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_decode_captured_and_replayed_with_other_lengths_and_pages(lib):
+    import torch
+    m = Layer(lib, [260, 300], hq=8, hkv=8, r=128)
+    q = m.query(1)
+    lens = i32([260, 300])
+    out = torch.zeros((2, 1, 8, 128), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((2, 1, 8), dtype=torch.float32, device="cuda")
+    table = i32(m.table)
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lib.lr_shared_decode(m.cache, q, lens, out, lse)      # first launches outside the capture
+    torch.cuda.current_stream().wait_stream(s)
+    with torch.cuda.graph(g):
+        lib.lr_shared_set_block_table_device(m.cache, table)
+        lib.lr_shared_decode(m.cache, q, lens, out, lse)
+    for new in ([260, 300], [1, 129], [0, 256]):
+        lens.copy_(i32(new))
+        g.replay()
+        torch.cuda.synchronize()
+        m.check_decode(q, out, lse, lens=new)
+    # swapped pages: sequence 0 now reads sequence 1's tokens
+    table.copy_(i32(m.table[::-1].copy()))
+    lens.copy_(i32([300, 260]))
+    g.replay()
+    torch.cuda.synchronize()
+    swapped = out.clone()
+    lib.lr_shared_set_block_table(m.cache, m.table)
+    again, _ = m.decode(torch.flip(q, [0]).contiguous(), [260, 300])
+    assert torch.equal(swapped, torch.flip(again, [0]))
+
+
+def test_decode_on_another_stream(lib):
+    import torch
+    m = Layer(lib, [130, 60])
+    q = m.query(1)
+    want = m.decode(q)
+    s = torch.cuda.Stream()
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    lens = i32(m.lens)
+    s.wait_stream(torch.cuda.current_stream())
+    lib.lr_shared_decode(m.cache, q, lens, out, lse, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_bad_device_pages_are_clamped(lib):
+    """Entries outside the pool read some page of it, never memory outside."""
+    import torch
+    m = Layer(lib, [200, 100], stale=False)
+    lib.lr_shared_set_block_table_device(m.cache, i32([[-5, 1 << 30], [7, -(1 << 31)]]))
+    q = m.query(1)
+    out, lse = m.decode(q)
+    assert torch.isfinite(out.float()).all()
+    lib.lr_shared_set_block_table(m.cache, m.table)
+    m.check_decode(q, *m.decode(q))
+
+
+def test_waits_that_give_up_are_reported_and_the_cache_recovers(lib):
+    m = Layer(lib, [500, 129], hq=8, hkv=8, r=256)
+    q = m.query(1)
+    import torch
+    out, lens = torch.zeros((2, 1, 8, 128), dtype=torch.bfloat16, device="cuda"), i32(m.lens)
+    lib.lr_shared_set_wait_limit(m.cache, 4)
+    lib.lr_shared_decode(m.cache, q, lens, out)
+    torch.cuda.synchronize()
+    assert lib.lr_shared_device_error(m.cache) == lib.LR_ERR_TIMEOUT
+    assert lib.lr_shared_device_error(m.cache) == 0
+    lib.lr_shared_set_wait_limit(m.cache, 0)
+    m.check_decode(q, *m.decode(q))
+
+
+# ---------------------------------------------------------------------------
+# refusals
+# ---------------------------------------------------------------------------
+
+def test_refusals(lib):
+    import torch
+    m = Layer(lib, [5, 6], r=128, new=2)
+    q = m.query(2)
+    out = torch.zeros((2, 2, 4, 128), dtype=torch.bfloat16, device="cuda")
+    lens = i32(m.lens)
+    with pytest.raises(ValueError):
+        lib.lr_shared_decode(m.cache, q.float(), lens, out)
+    with pytest.raises(ValueError):
+        lib.lr_shared_decode(m.cache, q, lens.cpu(), out)
+    with pytest.raises(ValueError):
+        lib.lr_shared_decode(m.cache, q, lens, out[:, :1])
+    with pytest.raises(ValueError):
+        lib.lr_shared_append(m.cache, m.c[:, :64], m.kr, i32(np.zeros(11)), i32(np.zeros(11)))
+    with pytest.raises(ValueError):
+        lib.lr_shared_append(m.cache, m.c.T.contiguous().T, m.kr, i32(np.zeros(11)), i32(np.zeros(11)))
+    with pytest.raises(lib.LRError) as e:          # rows 129 elements apart: not 16-byte aligned
+        w = torch.zeros((11, 129), dtype=torch.bfloat16, device="cuda")
+        lib.lr_shared_append(m.cache, w[:, :128], m.kr, i32(np.zeros(11)), i32(np.zeros(11)))
+    assert e.value.status == lib.LR_ERR_INVALID_ARG
+    with pytest.raises(lib.LRError) as e:
+        w = torch.zeros((11, 136), dtype=torch.bfloat16, device="cuda")
+        lib.lr_shared_append(m.cache, w[:, 4:132], m.kr, i32(np.zeros(11)), i32(np.zeros(11)))
+    assert e.value.status == lib.LR_ERR_INVALID_ARG
+    q3 = torch.zeros((2, 3, 4, 192), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(lib.LRError) as e:
+        lib.lr_shared_decode(m.cache, q3, lens, torch.zeros((2, 3, 4, 128), dtype=torch.bfloat16, device="cuda"))
+    assert e.value.status == lib.LR_ERR_CAPACITY
+    with pytest.raises(lib.LRError) as e:
+        lib.lr_shared_set_block_table(m.cache, np.array([[0], [4]]))
+    assert e.value.status == lib.LR_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        lib.lr_shared_set_block_table(m.cache, np.array([[0, 1], [0, 1]]))
+    off = torch.zeros(q.numel() + 1, dtype=torch.bfloat16, device="cuda")[1:].reshape(q.shape)
+    with pytest.raises(lib.LRError) as e:
+        lib.lr_shared_decode(m.cache, off, lens, out)
+    assert e.value.status == lib.LR_ERR_INVALID_ARG
+
+
+def test_nothing_to_do(lib):
+    import torch
+    m = Layer(lib, [5, 6])
+    none = torch.zeros((0, 128), dtype=torch.bfloat16, device="cuda")
+    lib.lr_shared_append(m.cache, none, none[:, :64], i32([]), i32([]))
+    lib.lr_shared_read(m.cache, i32([0, 0, 0]), none, torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda"))
+
+
+def test_failed_allocations_leave_nothing_behind(lib):
+    import torch
+    d = lib.make_shared_desc(2, 4, 4, 128, 64, 128, 128, 256, quant_bits=8, rope_theta=1e4)
+    Bk, Bv = bf16(np.zeros((128, 512))), bf16(np.zeros((128, 512)))
+    lib.lr_shared_destroy(lib.lr_shared_create(d, Bk, Bv))
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    n = 0
+    while True:
+        lib.lr_debug_inject_fault(lib.LR_FAULT_ALLOC, n)
+        try:
+            cache = lib.lr_shared_create(d, Bk, Bv)
+            break
+        except lib.LRError as e:
+            assert e.status == lib.LR_ERR_OOM
+            assert torch.cuda.mem_get_info()[0] == free
+        n += 1
+    lib.lr_debug_inject_fault(lib.LR_FAULT_ALLOC, -1)
+    assert n == 11
+    lib.lr_shared_destroy(cache)
+    assert torch.cuda.mem_get_info()[0] == free
+
+
+def test_failed_launches_are_reported(lib):
+    m = Layer(lib, [130, 60])
+    q = m.query(1)
+    for n in range(3):
+        lib.lr_debug_inject_fault(lib.LR_FAULT_LAUNCH, n)
+        with pytest.raises(lib.LRError) as e:
+            m.decode(q)
+        assert e.value.status == lib.LR_ERR_CUDA
+    lib.lr_debug_inject_fault(lib.LR_FAULT_LAUNCH, -1)
+    m.check_decode(q, *m.decode(q))
