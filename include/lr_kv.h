@@ -391,7 +391,7 @@ lr_status lr_shared_decode(lr_shared* cache, const void* q, int32_t n_tokens, co
                            float* lse, void* stream);
 
 /* lr_shared_expand — stored tokens as per-head keys and values, for prompts (many queries):
- *   row cu[b] + i of k [total][Hkv][dn], v [total][Hkv][dv] and kr [total][dr] (bf16, 16-byte
+ *   row cu[b] + i of k [total][Hkv][dn], v [total][Hkv][dv] (32-byte) and kr [total][dr] (bf16, 16-byte
  *   aligned) is token start[b] + i of sequence b: k_h = c B_k,h, v_h = c B_v,h in fp32,
  *   rounded once.  cu, start, total as for lr_shared_read.
  * lr_shared_attn — attention of ragged queries over expanded keys and values: sequence b's
@@ -399,7 +399,7 @@ lr_status lr_shared_decode(lr_shared* cache, const void* q, int32_t n_tokens, co
  *   cu_k[b]..cu_k[b+1]-1 of k, v, kr (as lr_shared_expand writes them; n_seq sequences, 0..1024,
  *   independent of the cache's batch; cu_*: [n_seq + 1] int32, device, ascending from 0).
  *   causal = 1: query i of n sees keys j <= i + m - n of its m keys (the queries are the last n
- *   tokens); 0: all m.  out [total_q][Hq][dv] bf16 (16-byte aligned), lse [total_q][Hq] fp32 or
+ *   tokens); 0: all m.  out [total_q][Hq][dv] bf16 (32-byte aligned), lse [total_q][Hq] fp32 or
  *   NULL; a query that sees no key gets out = 0, lse = -inf; rows past cu_q[n_seq] are left as
  *   they are.  Partial results over several key ranges join by their lse. */
 lr_status lr_shared_expand(lr_shared* cache, const int32_t* cu, const int32_t* start, int32_t total, void* k, void* v,

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
   pdl_trigger();
   if (warp == 0) {
     int chunk;
-    const TileRun run = tile_run([&](int b) { return shared_len(p.row_len, b, p.cap); }, p.B, p.X, x, &chunk);
+    const TileRun run = tile_run([&](int b) { return (shared_len(p.row_len, b, p.cap) + 127) >> 7; }, p.B, p.X, x, &chunk);
     if (lane == 0) aux->run = run;
   }
   ptx::tc_fence_before();
@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
                            : "memory");
           }
         }
+        __syncwarp();
         if (ex) {
           const float top = reduce_cols<NR, true>(s, lane);
           aux->red[qd][lane] = top;
@@ -754,13 +755,12 @@ __global__ void __launch_bounds__(kOutThreads)
   const int nrow = min(p.RB, p.rows - m0);               // rows m0 .. m0 + nrow - 1
   if (warp == 0) {
     // slots of the rows' sequences, from the same cut into runs as the decode's
-    auto len = [&](int b) { return shared_len(p.row_len, b, p.cap); };
-    int chunk;
-    tile_run(len, p.B, p.X, 0, &chunk);
+    auto tiles = [&](int b) { return (shared_len(p.row_len, b, p.cap) + 127) >> 7; };
+    const int chunk = max(1, (tile_total(tiles, p.B) + p.X - 1) / p.X);
     int run = 0;
     for (int base = 0; base < p.B; base += 32) {
       const int b = base + lane;
-      const int v = b < p.B ? (len(b) + 127) >> 7 : 0;
+      const int v = b < p.B ? tiles(b) : 0;
       int inc = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -987,8 +987,8 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   qp.qt = static_cast<__nv_bfloat16*>(c->qt);
   qp.err = c->dev_err;
   CUtensorMap tw, tq;
-  if (!map2d(&tw, bf, c->B_k, (uint64_t)d.n_kv_heads * d.dim_nope, r, (uint64_t)d.n_kv_heads * d.dim_nope * 2, 64, 128))
-    return cudaErrorInvalidValue;
+  const uint64_t wk = (uint64_t)d.n_kv_heads * d.dim_nope, wv = (uint64_t)d.n_kv_heads * d.dim_v;
+  if (!map2d(&tw, bf, c->B, wk, r, (wk + wv) * 2, 64, 128)) return cudaErrorInvalidValue;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)dq, (cuuint64_t)d.n_q_heads, (cuuint64_t)BS};
     const cuuint64_t st[2] = {(cuuint64_t)dq * 2, (cuuint64_t)d.n_q_heads * dq * 2};
@@ -1076,7 +1076,7 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   o.lse = lse;
   o.err = c->dev_err;
   CUtensorMap tv;
-  if (!map2d(&tv, bf, c->B_v, (uint64_t)d.n_kv_heads * d.dim_v, r, (uint64_t)d.n_kv_heads * d.dim_v * 2, 64, 64))
+  if (!map2d(&tv, bf, static_cast<const __nv_bfloat16*>(c->B) + wk, wv, r, (wk + wv) * 2, 64, 64))
     return cudaErrorInvalidValue;
   e = smem_optin(k_shared_out, optin_o);
   if (e != cudaSuccess) return e;

@@ -1,0 +1,403 @@
+// Stored tokens of a shared-latent cache as per-head keys and values: K = C B_k, V = C B_v,
+// with C the latents read back from their pages, and the rotary keys copied along.
+//
+// One GEMM whose A operand is gathered by page: M = 128 tokens (a page), N = 256 columns of
+// [K | V], K = rank.  The tensor pipe bounds it (2 r flop per 2-byte output element: 512 flop
+// per byte written at r = 512).  A CTA keeps a page's whole latent tile in shared memory
+// (r <= 512: 128 KB) and streams the bases past it (from a copy transposed at creation, so both
+// operands are K-major rows of 64 ranks), so per 128 x 256 output block only the bases cross
+// L2 (64 B per SM and clock at full rate, what a 256 x 256 tile pair would need too).  The
+// (page, column block) units of all sequences are cut into equal consecutive runs, one per SM:
+// a run changes its tile once or twice, and each 64-rank part of the next tile is fetched as
+// soon as the last block has used the old one.  Two TMEM accumulators let the epilogue of one
+// block run under the MMAs of the next; it stores 32 bytes per lane, whole sectors.
+//
+// 8-bit latents are expanded to bf16 (exactly) by eight warps straight from global memory into
+// the swizzled tile, once per tile; the MMAs then run as for bf16.
+#include "shared_internal.cuh"
+#include "tc_common.cuh"
+
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+namespace {
+
+using tc::drain_wait;
+
+constexpr int kSub = 128 * 128;        // 128 tokens x 64 ranks x 2 B
+constexpr int kStage = 2 * kSub;       // 256 columns x 64 ranks x 2 B: two boxes of 128 columns
+constexpr int kStages = 3;
+constexpr int kAuxBytes = 2048;
+
+constexpr int kMaxTiles = 60;          // tiles of one CTA's run
+
+struct ExpArgs {
+  unsigned long long wait_ns;
+  const int32_t* cu; const int32_t* start;
+  RowMap map;
+  int B, cap, total, r, Wk, W, NB;   // columns: [0, Wk) of K, [Wk, W) of V; NB blocks of 256
+  const uint8_t* codes; const uint8_t* scale;
+  __nv_bfloat16* k; __nv_bfloat16* v;
+  int* err;
+};
+
+// One tile of the run: token row i of it is row pool + i of the stored arrays and, for
+// lo <= i < hi, row out + i of the results.
+struct Tile {
+  long long pool, out;
+  int lo, hi;
+};
+
+// Barriers (arrival count; who arrives -> who waits):
+//   a_full[s]   1 + tx / 8   producer (bf16) or expansion warps (8 bits) -> MMA; 64 ranks of the tile
+//   a_empty[s]  1        MMA commit in the tile's last block -> producer / expansion warps
+//   b_full/b_empty[s]    1 + tx / 1   basis stages (64 ranks)
+//   d_full/d_empty[2]    1 / 4        accumulators
+struct Aux {
+  uint64_t a_full[8], a_empty[8], b_full[kStages], b_empty[kStages], d_full[2], d_empty[2], done;
+  unsigned long long wait_ns;
+  uint32_t tmem_base;
+  int abort_flag;
+  int blk0, units;       // first column block, units of this CTA
+  Tile tiles[kMaxTiles];
+};
+static_assert(sizeof(Aux) <= kAuxBytes, "aux block");
+
+__device__ __forceinline__ bool wait_b(uint64_t* bar, uint32_t parity, Aux* aux, int* err) {
+  return tc::wait_b(bar, parity, &aux->abort_flag, err, aux->wait_ns);
+}
+__device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, Aux* aux, int* err) {
+  return __all_sync(0xffffffffu, wait_b(bar, parity, aux, err));
+}
+
+// Positions [lo, hi) of sequence b to expand, inside the cache; position t goes to row t + off.
+struct Span {
+  int lo, hi;
+  long long off;
+};
+__device__ __forceinline__ Span span_at(const ExpArgs& p, int b) {
+  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), st = p.start ? __ldg(p.start + b) : 0;
+  Span s;
+  s.lo = min(max(st, 0), p.cap);
+  s.hi = (int)min(max((long long)st + ((long long)c1 - c0), (long long)s.lo), (long long)p.cap);
+  s.off = (long long)c0 - st;
+  return s;
+}
+__device__ __forceinline__ int span_tiles(const ExpArgs& p, int b) {
+  const Span s = span_at(p, b);
+  return s.hi > s.lo ? ((s.hi + 127) >> 7) - (s.lo >> 7) : 0;
+}
+
+// A role's place in the run: unit u is column block blk of tile k.
+struct Place {
+  int u, k, blk;
+  __device__ __forceinline__ bool fresh() const { return u == 0 || blk == 0; }
+  __device__ __forceinline__ bool last(int units, int NB) const { return u == units - 1 || blk == NB - 1; }
+  __device__ __forceinline__ void next(int NB) {
+    ++u;
+    if (++blk == NB) {
+      blk = 0;
+      ++k;
+    }
+  }
+};
+
+template <bool kQuant>
+__global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
+    k_shared_expand(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_w,
+                    const ExpArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (ptx::smem_u32(smem_raw) & 1023) {
+    if (threadIdx.x == 0) atomicExch(p.err, (int)LR_ERR_UNSUPPORTED);
+    return;
+  }
+  Aux* aux = reinterpret_cast<Aux*>(smem_raw);
+  uint8_t* a_s = smem_raw + kAuxBytes;
+  const int nsub = p.r >> 6;
+  uint8_t* b_s = a_s + nsub * kSub;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 8; ++s) {
+      ptx::mbar_init(&aux->a_full[s], kQuant ? 8 : 1);
+      ptx::mbar_init(&aux->a_empty[s], 1);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&aux->b_full[s], 1);
+      ptx::mbar_init(&aux->b_empty[s], 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      ptx::mbar_init(&aux->d_full[k], 1);
+      ptx::mbar_init(&aux->d_empty[k], 4);
+    }
+    ptx::mbar_init(&aux->done, 1);
+    aux->abort_flag = 0;
+    aux->wait_ns = tc::wait_limit(p.wait_ns);
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tm_c);
+    ptx::prefetch_tmap(&tm_w);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&aux->tmem_base, 512);
+    ptx::tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) {
+    // this CTA's run of units, and its tiles
+    auto tiles = [&](int b) { return span_tiles(p, b); };
+    const int total = tile_total(tiles, p.B);
+    const unsigned G = gridDim.x;
+    const unsigned units = (unsigned)total * (unsigned)p.NB;      // < 2^31 (host)
+    const unsigned chunk = (units + G - 1) / G, first = chunk * (unsigned)blockIdx.x;
+    int n = 0, blk0 = 0;
+    if (first < units) {
+      n = (int)min(chunk, units - first);
+      n = min(n, (kMaxTiles - 1) * p.NB);      // (the host's grid never reaches this)
+      blk0 = (int)(first % (unsigned)p.NB);
+      const int t0 = (int)(first / (unsigned)p.NB), nt = (blk0 + n + p.NB - 1) / p.NB;
+      for (int k = 0; k < nt; ++k) {
+        int b, tile;
+        tile_find(tiles, p.B, t0 + k, &b, &tile);
+        if (lane == 0) {
+          const Span s = span_at(p, b);
+          const int tok = ((s.lo >> 7) + tile) << 7;
+          aux->tiles[k].pool = (long long)p.map.page(b, tok) << 7;
+          aux->tiles[k].out = tok + s.off;
+          // rows inside the span, the results and the cache
+          const long long o = tok + s.off;
+          aux->tiles[k].lo = (int)max((long long)max(s.lo - tok, 0), min(-o, 128ll));
+          aux->tiles[k].hi = (int)min((long long)min(s.hi - tok, 128), max((long long)p.total - o, 0ll));
+        }
+      }
+    }
+    if (lane == 0) {
+      aux->blk0 = blk0;
+      aux->units = n;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = aux->tmem_base;
+  const int units = aux->units;
+  Place w{0, 0, aux->blk0};
+  
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int pos = 0, nt = 0;                  // basis stages and tiles issued
+      int a_boxes = 0;                      // boxes issued of tile nt - 1
+      bool ok = true;
+      for (; ok && w.u < units; w.next(p.NB)) {
+        const int c0 = w.blk * 256, nb = p.W - c0 > 128 ? 2 : 1;
+        const bool fresh = w.fresh();
+        const int row = (int)aux->tiles[w.k].pool;
+        if (fresh) {
+          ++nt;
+          a_boxes = 0;
+        }
+        for (int h = 0; h < nsub; ++h) {
+          if (!kQuant && fresh) {
+            if (nt > 1 && !(ok = wait_b(&aux->a_empty[h], nt & 1, aux, p.err))) break;   // tile nt - 2's use
+            ptx::mbar_arrive_expect_tx(&aux->a_full[h], kSub);
+            ptx::tma_load_2d(a_s + h * kSub, &tm_c, &aux->a_full[h], h * 64, row);
+            ++a_boxes;
+          }
+          const int st = pos % kStages;
+          if (pos >= kStages && !(ok = wait_b(&aux->b_empty[st], (pos / kStages - 1) & 1, aux, p.err))) break;
+          ptx::mbar_arrive_expect_tx(&aux->b_full[st], (uint32_t)(nb * kSub));
+          ptx::tma_load_2d(b_s + st * kStage, &tm_w, &aux->b_full[st], h * 64, c0);   // rows past W read as 0
+          if (nb == 2) ptx::tma_load_2d(b_s + st * kStage + kSub, &tm_w, &aux->b_full[st], h * 64, c0 + 128);
+          ++pos;
+        }
+      }
+      // every copy this thread issued has landed before the CTA can exit
+      for (int k = max(0, pos - kStages); k < pos; ++k) drain_wait(&aux->b_full[k % kStages], (k / kStages) & 1);
+      if (!kQuant)
+        for (int s = 0; s < nsub; ++s) {
+          const int n = s < a_boxes ? nt : nt - 1;      // tiles whose box s was issued
+          if (n > 0) drain_wait(&aux->a_full[s], (n - 1) & 1);
+        }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA issuer (warp-wide)
+    const uint64_t ad0 = ptx::smem_desc(ptx::smem_u32(a_s), 16, 1024, 2);
+    const uint64_t bd0 = ptx::smem_desc(ptx::smem_u32(b_s), 16, 1024, 2);
+    int pos = 0, nt = 0;
+    bool ok = true;
+    for (; ok && w.u < units; w.next(p.NB)) {
+      const uint32_t id = ptx::idesc_f16(1, 0, 0, 128, (uint32_t)min(256, p.W - w.blk * 256));
+      const bool fresh = w.fresh(), last = w.last(units, p.NB);
+      const int u = w.u;
+      if (fresh) ++nt;
+      const uint32_t d = tmem + (uint32_t)(u & 1) * 256;
+      if (u >= 2 && !(ok = wait_w(&aux->d_empty[u & 1], ((u >> 1) - 1) & 1, aux, p.err))) break;
+      for (int h = 0; h < nsub; ++h, ++pos) {
+        const int st = pos % kStages;
+        if (fresh && !(ok = wait_w(&aux->a_full[h], (nt - 1) & 1, aux, p.err))) break;
+        if (!(ok = wait_w(&aux->b_full[st], (pos / kStages) & 1, aux, p.err))) break;
+        ptx::tc_fence_after();
+        const uint64_t ad = ad0 + (uint64_t)((h * kSub) >> 4);
+        const uint64_t bd = bd0 + (uint64_t)((st * kStage) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          ptx::mma_f16_elect(d, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), id, (h | kk) ? 1u : 0u);
+        ptx::mma_commit_elect(&aux->b_empty[st]);
+        if (last) ptx::mma_commit_elect(&aux->a_empty[h]);
+      }
+      if (ok) ptx::mma_commit_elect(&aux->d_full[u & 1]);
+    }
+    ptx::mma_commit_elect(&aux->done);
+    drain_wait(&aux->done, 0);
+    __syncwarp();
+  } else if (warp < 6) {
+    // ------------------------------------------------------------- epilogue: thread = token row
+    const int qd = warp & 3, row = qd * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+    for (; w.u < units; w.next(p.NB)) {
+      const Tile t = aux->tiles[w.k];
+      const bool in = row >= t.lo && row < t.hi;
+      const long long orow = t.out + row;
+      const int c0 = w.blk * 256, n = min(256, p.W - c0), u = w.u;
+      if (!wait_w(&aux->d_full[u & 1], (u >> 1) & 1, aux, p.err)) break;
+      ptx::tc_fence_after();
+      for (int c = 0; c < n; c += 32) {
+        uint32_t v[32];
+        ptx::tmem_ld32(tmem + lane_off + (uint32_t)(u & 1) * 256 + c, v);
+        ptx::tmem_wait_ld();
+        if (c + 32 >= n) {             // all read: the accumulator is free before the last stores
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&aux->d_empty[u & 1]);
+        }
+        // 32 columns lie in K or in V (both widths are multiples of 64)
+        const int col = c0 + c;
+        __nv_bfloat16* dst = col < p.Wk ? p.k + orow * p.Wk + col : p.v + orow * (p.W - p.Wk) + (col - p.Wk);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[16 * q + 2 * e]),
+                                                            __uint_as_float(v[16 * q + 2 * e + 1]));
+            o[e] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          if (in) ptx::st_global_v8(dst + 16 * q, o);
+        }
+        __syncwarp();                  // the next TMEM load wants the whole warp
+      }
+    }
+  } else if (kQuant) {
+    // ------------------------------------------------------------- expansion of codes
+    const int tid = threadIdx.x - 192;
+    int nt = 0;
+    bool ok = true;
+    for (; ok && w.u < units; w.next(p.NB)) {
+      if (!w.fresh()) continue;
+      ++nt;
+      const long long row0 = aux->tiles[w.k].pool;
+      // two 64-rank parts at a time: a thread's 16-byte code runs are in flight together
+      for (int s0 = 0; s0 < nsub; s0 += 2) {
+        const int ns = min(2, nsub - s0);
+        uint4 cd[4];
+        uint32_t eb[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int idx = k * 256 + tid, tok = (idx >> 2) & 127, s = s0 + (idx >> 9), col = idx & 3;
+          if ((idx >> 9) < ns) {
+            const long long row = row0 + tok;
+            cd[k] = __ldg(reinterpret_cast<const uint4*>(p.codes + row * p.r + s * 64) + col);
+            eb[k] = __ldg(p.scale + shared_scale_index(row, p.r, s * 2 + (col >> 1)));
+          }
+        }
+        if (nt > 1)
+          for (int q = 0; q < ns && ok; ++q) ok = wait_w(&aux->a_empty[s0 + q], nt & 1, aux, p.err);
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int idx = k * 256 + tid, tok = (idx >> 2) & 127, s = s0 + (idx >> 9), col = idx & 3;
+          if ((idx >> 9) < ns) {
+            const float sc = shared_pow2(eb[k]);
+            const uint32_t cw[4] = {cd[k].x, cd[k].y, cd[k].z, cd[k].w};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t two = (cw[2 * h + (e >> 1)] >> (16 * (e & 1))) & 0xFFFFu;
+                const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * sc, f.y * sc);
+                o[e] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              const uint32_t a = ptx::smem_u32(a_s + s * kSub + tok * 128) + (((col * 2 + h) ^ (tok & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                           "r"(o[3])
+                           : "memory");
+            }
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+          for (int q = 0; q < ns; ++q) ptx::mbar_arrive(&aux->a_full[s0 + q]);
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+bool map2d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint32_t b0, uint32_t b1) {
+  const cuuint64_t dims[2] = {d0, d1}, st[1] = {d0 * 2};
+  const cuuint32_t box[2] = {b0, b1};
+  return tc::make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, 2, dims, st, box);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t* start, int total, void* k, void* v,
+                                 void* kr, cudaStream_t s) {
+  const lr_shared_desc& d = c->desc;
+  ExpArgs a;
+  a.wait_ns = c->wait_ns;
+  a.cu = cu;
+  a.start = start;
+  a.map = row_map(c);
+  a.B = d.batch;
+  a.cap = d.capacity;
+  a.total = total;
+  a.r = d.rank;
+  a.Wk = d.n_kv_heads * d.dim_nope;
+  a.W = a.Wk + d.n_kv_heads * d.dim_v;
+  a.NB = (a.W + 255) / 256;
+  a.codes = static_cast<const uint8_t*>(c->c);
+  a.scale = c->scale;
+  a.k = static_cast<__nv_bfloat16*>(k);
+  a.v = static_cast<__nv_bfloat16*>(v);
+  a.err = c->dev_err;
+  CUtensorMap tlat, tw;
+  if (!map2d(&tw, c->Bt, a.r, a.W, 64, 128)) return cudaErrorInvalidValue;
+  const bool quant = d.quant_bits != 0;
+  if (quant) tlat = tw;                  // not used: the codes are read by the expansion warps
+  else if (!map2d(&tlat, c->c, a.r, (uint64_t)c->n_pages * 128, 64, 128)) return cudaErrorInvalidValue;
+  // One run per SM, no more runs than units there can be, and no run longer than its tile table
+  // holds (beyond 60 tiles an SM, over a million tokens, the runs queue up).
+  const long long tiles = (long long)total / 128 + 2 * std::min<long long>(d.batch, total);
+  const long long grid = std::max(std::min<long long>(c->num_sms, tiles * a.NB), (tiles + kMaxTiles - 3) / (kMaxTiles - 2));
+  if (tiles * a.NB > 0x7FFFFFFF) return cudaErrorNotSupported;
+  const size_t smem = kAuxBytes + (size_t)(a.r / 64) * kSub + (size_t)kStages * kStage;
+  static std::atomic<uint32_t> optin[2] = {{0}, {0}};
+  cudaError_t e = quant ? smem_optin(k_shared_expand<true>, optin[1]) : smem_optin(k_shared_expand<false>, optin[0]);
+  if (e != cudaSuccess) return e;
+  e = launch_shared_read(c, cu, start, total, nullptr, kr, s);   // the rotary keys
+  if (e != cudaSuccess) return e;
+  return quant ? launch_pdl(k_shared_expand<true>, dim3((unsigned)grid), dim3(448), smem, s, tlat, tw, a)
+               : launch_pdl(k_shared_expand<false>, dim3((unsigned)grid), dim3(192), smem, s, tlat, tw, a);
+}

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_read(const ReadArgs a) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int v = k * 32 + lane;
-    if (v >= nv) continue;
+    if (!a.z || v >= nv) continue;     // a.z null: the rotary keys only
     if (!kQuant) {
       dst[v] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.c) + row * a.r) + v);
       continue;
@@ -179,7 +179,22 @@ __global__ void k_shared_rope(float2* cs, int cap, int half, double log_theta) {
   cs[i] = make_float2((float)cn, (float)sn);
 }
 
+// Bt [W][r] = B [r][W] transposed, in 32 x 32 tiles through shared memory (once, at creation).
+__global__ void k_shared_transpose(const __nv_bfloat16* B, __nv_bfloat16* Bt, int r, int W) {
+  __shared__ __nv_bfloat16 t[32][33];
+  const int x = blockIdx.x * 32, y = blockIdx.y * 32;      // column of W, rank; both multiples of 32
+  for (int j = threadIdx.y; j < 32; j += 8) t[j][threadIdx.x] = B[(size_t)(y + j) * W + x + threadIdx.x];
+  __syncthreads();
+  for (int j = threadIdx.y; j < 32; j += 8) Bt[(size_t)(x + j) * r + y + threadIdx.x] = t[threadIdx.x][j];
+}
+
 }  // namespace
+
+cudaError_t launch_shared_transpose(lr_shared* c, cudaStream_t s) {
+  const int W = c->desc.n_kv_heads * (c->desc.dim_nope + c->desc.dim_v);
+  return launch_serial(k_shared_transpose, dim3(W / 32, c->desc.rank / 32), dim3(32, 8), 0, s,
+                       static_cast<const __nv_bfloat16*>(c->B), static_cast<__nv_bfloat16*>(c->Bt), c->desc.rank, W);
+}
 
 cudaError_t launch_shared_rope_table(lr_shared* c, cudaStream_t s) {
   const int half = c->desc.dim_rope / 2;

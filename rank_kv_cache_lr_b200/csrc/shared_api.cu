@@ -9,6 +9,7 @@
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
 
 // Makes the cache's device current for a call and restores the caller's afterwards.
 struct OnDevice {
@@ -56,7 +57,7 @@ cudaError_t dalloc(T** p, size_t bytes, bool zero) {
 }
 
 void free_all(lr_shared* c) {
-  void* ptrs[] = {c->c, c->scale, c->kr, c->table, c->B_k, c->B_v, c->rope_cs, c->qt, c->part_o, c->part_ml, c->dev_err};
+  void* ptrs[] = {c->c, c->scale, c->kr, c->table, c->B, c->Bt, c->rope_cs, c->qt, c->part_o, c->part_ml, c->dev_err};
   for (void* p : ptrs)
     if (p) cudaFree(p);
 }
@@ -92,14 +93,14 @@ lr_status lr_shared_create(const lr_shared_desc* desc, const void* B_k, const vo
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device);
   const size_t rows = (size_t)c->n_pages * kPageTokens, r = d.rank;
-  const size_t nk = r * d.n_kv_heads * d.dim_nope * 2, nv = r * d.n_kv_heads * d.dim_v * 2;
+  const size_t wk = (size_t)d.n_kv_heads * d.dim_nope * 2, wv = (size_t)d.n_kv_heads * d.dim_v * 2;   // bytes a basis row
   cudaStream_t s = (cudaStream_t)stream;
   if (e == cudaSuccess) e = dalloc(&c->c, rows * r * (d.quant_bits ? 1 : 2), true);
   if (e == cudaSuccess && d.quant_bits) e = dalloc(&c->scale, rows * ((r + 127) / 128) * 4, true);
   if (e == cudaSuccess) e = dalloc(&c->kr, rows * d.dim_rope * 2, true);
   if (e == cudaSuccess) e = dalloc(&c->table, (size_t)d.batch * c->pps * sizeof(int32_t), false);
-  if (e == cudaSuccess) e = dalloc(&c->B_k, nk, false);
-  if (e == cudaSuccess) e = dalloc(&c->B_v, nv, false);
+  if (e == cudaSuccess) e = dalloc(&c->B, r * (wk + wv), false);
+  if (e == cudaSuccess) e = dalloc(&c->Bt, r * (wk + wv), false);
   if (e == cudaSuccess && d.rope_theta > 0.0)
     e = dalloc(&c->rope_cs, (size_t)d.capacity * (d.dim_rope / 2) * sizeof(float2), false);
   if (e == cudaSuccess) e = dalloc(&c->qt, shared_qt_bytes(&d), true);
@@ -119,8 +120,10 @@ lr_status lr_shared_create(const lr_shared_desc* desc, const void* B_k, const vo
   }
   if (e == cudaSuccess)
     e = cudaMemcpy(c->table, c->host_table.data(), c->host_table.size() * sizeof(int32_t), cudaMemcpyHostToDevice);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(c->B_k, B_k, nk, cudaMemcpyDeviceToDevice, s);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(c->B_v, B_v, nv, cudaMemcpyDeviceToDevice, s);
+  if (e == cudaSuccess) e = cudaMemcpy2DAsync(c->B, wk + wv, B_k, wk, wk, r, cudaMemcpyDeviceToDevice, s);
+  if (e == cudaSuccess)
+    e = cudaMemcpy2DAsync(static_cast<char*>(c->B) + wk, wk + wv, B_v, wv, wv, r, cudaMemcpyDeviceToDevice, s);
+  if (e == cudaSuccess) e = launch_shared_transpose(c, s);
   if (e == cudaSuccess && c->rope_cs) e = launch_shared_rope_table(c, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);   // the fills above
@@ -209,7 +212,7 @@ lr_status lr_shared_expand(lr_shared* c, const int32_t* cu, const int32_t* start
                            void* kr, void* stream) {
   if (!c || total < 0) return LR_ERR_INVALID_ARG;
   if (total == 0) return LR_OK;
-  if (!cu || !k || !v || !kr || !aligned16(k) || !aligned16(v) || !aligned16(kr)) return LR_ERR_INVALID_ARG;
+  if (!cu || !k || !v || !kr || !aligned16(kr) || !aligned32(k) || !aligned32(v)) return LR_ERR_INVALID_ARG;
   OnDevice dev(c->device);
   if (!dev.ok) return LR_ERR_CUDA;
   c->last_stream = (cudaStream_t)stream;
@@ -223,7 +226,7 @@ lr_status lr_shared_attn(lr_shared* c, const void* q, const void* k, const void*
   if (n_seq > 1024) return LR_ERR_UNSUPPORTED;
   if (n_seq == 0 || total_q == 0) return LR_OK;
   if (!q || !cu_q || !cu_k || !out || (total_k > 0 && (!k || !kr || !v))) return LR_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(kr) || !aligned16(v) || !aligned16(out)) return LR_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(kr) || !aligned16(v) || !aligned32(out)) return LR_ERR_INVALID_ARG;
   OnDevice dev(c->device);
   if (!dev.ok) return LR_ERR_CUDA;
   c->last_stream = (cudaStream_t)stream;

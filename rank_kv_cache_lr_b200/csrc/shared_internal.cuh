@@ -19,8 +19,8 @@ struct lr_shared {
   uint8_t* scale = nullptr;   // 8 bits: [n_pages][ceil(r/128)][128][4] exponent bytes (shared_scale_index)
   void* kr = nullptr;         // [rows][dr] bf16
   int32_t* table = nullptr;   // [B][pps]
-  void* B_k = nullptr;        // [r][Hkv*dn]
-  void* B_v = nullptr;        // [r][Hkv*dv]
+  void* B = nullptr;          // [r][Hkv*dn | Hkv*dv]: the bases side by side, so that one map covers both
+  void* Bt = nullptr;         // [Hkv*dn | Hkv*dv][r]: B transposed (lr_shared_expand)
   float2* rope_cs = nullptr;  // [capacity][dr/2] (cos, sin), or null
   void* qt = nullptr;         // decode: query latents, hi and lo halves (k_shared_decode.cu)
   float* part_o = nullptr;    // decode: split partials [slots][rows][r]
@@ -59,47 +59,60 @@ __device__ __forceinline__ int shared_len(const int32_t* row_len, int b, int cap
   return min(max(__ldg(row_len + b), 0), cap);
 }
 
-// By one whole warp: the tile total of B sequences (len(b) tokens each) and run x.
-template <typename Len>
-__device__ __forceinline__ TileRun tile_run(Len len, int B, int X, int x, int* chunk_out) {
-  const int lane = threadIdx.x & 31;
+// By one whole warp: the sum of tiles(b) over the sequences.
+template <typename Tiles>
+__device__ __forceinline__ int tile_total(Tiles tiles, int B) {
   int total = 0;
-  for (int i = lane; i < B; i += 32) total += (len(i) + 127) >> 7;
+  for (int i = threadIdx.x & 31; i < B; i += 32) total += tiles(i);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int chunk = max(1, (total + X - 1) / X);
-  *chunk_out = chunk;
-  const long long want = (long long)x * chunk;
-  TileRun r{B, 0, 0};
-  if (want >= total) return r;
-  const int begin = (int)want;
-  r.left = min(chunk, total - begin);
+  return total;
+}
+// By one whole warp: the sequence and its tile that hold tile number `want` (< the total).
+template <typename Tiles>
+__device__ __forceinline__ void tile_find(Tiles tiles, int B, int want, int* b, int* tile) {
+  const int lane = threadIdx.x & 31;
   int run = 0;
   for (int base = 0; base < B; base += 32) {
     const int i = base + lane;
-    const int v = i < B ? (len(i) + 127) >> 7 : 0;
+    const int v = i < B ? tiles(i) : 0;
     int inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += u;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, run + inc > begin);
+    const unsigned hit = __ballot_sync(0xffffffffu, run + inc > want);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      r.b = base + src;
-      r.tile = begin - __shfl_sync(0xffffffffu, run + inc - v, src);
-      return r;
+      *b = base + src;
+      *tile = want - __shfl_sync(0xffffffffu, run + inc - v, src);
+      return;
     }
     run += __shfl_sync(0xffffffffu, inc, 31);
   }
+  *b = B;
+  *tile = 0;
+}
+// By one whole warp: run x of X equal runs of B sequences' tiles, and the runs' length.
+template <typename Tiles>
+__device__ __forceinline__ TileRun tile_run(Tiles tiles, int B, int X, int x, int* chunk_out) {
+  const int total = tile_total(tiles, B);
+  const int chunk = max(1, (total + X - 1) / X);
+  *chunk_out = chunk;
+  TileRun r{B, 0, 0};
+  if ((long long)x * chunk >= total) return r;
+  r.left = min(chunk, total - x * chunk);
+  tile_find(tiles, B, x * chunk, &r.b, &r.tile);
   return r;
 }
 
 // Host side of each operator (checks done by shared_api.cu).
+cudaError_t launch_shared_transpose(lr_shared* c, cudaStream_t s);
 cudaError_t launch_shared_rope_table(lr_shared* c, cudaStream_t s);
 cudaError_t launch_shared_append(lr_shared* c, const void* z, long long z_stride, const void* kr, long long kr_stride,
                                  const int32_t* seq, const int32_t* pos, int n, cudaStream_t s);
+// z null: only the rotary keys are read back
 cudaError_t launch_shared_read(lr_shared* c, const int32_t* cu, const int32_t* start, int total, void* z, void* kr,
                                cudaStream_t s);
 cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, const int32_t* row_len, void* out,

@@ -364,6 +364,264 @@ def test_waits_that_give_up_are_reported_and_the_cache_recovers(lib):
 
 
 # ---------------------------------------------------------------------------
+# expansion
+# ---------------------------------------------------------------------------
+
+def run_expand(m, first, lens, spare=3):
+    """Packed expansion of tokens first[b] .. first[b] + lens[b] - 1, with rows to spare behind."""
+    import torch
+    T = sum(lens) + spare
+    k = torch.full((T, m.hkv, m.dn), 55.0, dtype=torch.bfloat16, device="cuda")
+    v = torch.full((T, m.hkv, m.dv), 55.0, dtype=torch.bfloat16, device="cuda")
+    kr = torch.full((T, m.dr), 55.0, dtype=torch.bfloat16, device="cuda")
+    cu = i32(np.concatenate([[0], np.cumsum(lens)]))
+    m.lib.lr_shared_expand(m.cache, cu, k, v, kr, start=None if first is None else i32(first))
+    assert m.lib.lr_shared_device_error(m.cache) == 0
+    return k, v, kr, cu
+
+
+def check_expand(m, first, lens, k, v, kr):
+    """One rounding to bf16 (u) of an fp32 sum of r products."""
+    idx = np.concatenate([m.cu[b] + f + np.arange(n) for b, (f, n) in enumerate(zip(first, lens))]).astype(int)
+    c, n = m.c64[idx], len(idx)
+    for got, B, w in ((k, m.Bk64, m.hkv * m.dn), (v, m.Bv64, m.hkv * m.dv)):
+        want, mag = c @ B, np.abs(c) @ np.abs(B)
+        err = np.abs(f64(got)[:n].reshape(n, w) - want)
+        assert np.all(err <= U * np.abs(want) + (m.r + 8) * F * mag)
+        assert np.all(f64(got)[n:] == 55)
+    assert np.array_equal(f64(kr)[:n], m.kr64[idx]) and np.all(f64(kr)[n:] == 55)
+
+
+@pytest.mark.parametrize("bits", [0, 8])
+@pytest.mark.parametrize("hkv,r,dn,dr,dv", [(1, 64, 64, 32, 64), (3, 192, 128, 64, 64), (5, 448, 64, 32, 128),
+                                            (28, 512, 128, 64, 128)])
+def test_expand_matches_the_oracle(lib, bits, hkv, r, dn, dr, dv):
+    m = Layer(lib, LENS, hq=hkv, hkv=hkv, r=r, dn=dn, dr=dr, dv=dv, bits=bits)
+    k, v, kr, _ = run_expand(m, None, m.lens)
+    check_expand(m, [0] * len(LENS), m.lens, k, v, kr)
+
+
+@pytest.mark.parametrize("bits", [0, 8])
+def test_expand_parts_that_start_and_end_inside_pages(lib, bits):
+    m = Layer(lib, [300, 257, 129, 600], hq=2, hkv=2, r=128, bits=bits)
+    first, lens = [127, 256, 60, 1], [2, 1, 0, 599]
+    k, v, kr, _ = run_expand(m, first, lens)
+    check_expand(m, first, lens, k, v, kr)
+
+
+def test_expand_many_tiles_per_run(lib):
+    """Runs that cross tiles and sequences: more (page, column block) units than SMs."""
+    m = Layer(lib, [2000, 3000, 1, 4000], hq=10, hkv=10, r=320)
+    k, v, kr, _ = run_expand(m, None, m.lens)
+    check_expand(m, [0] * 4, m.lens, k, v, kr)
+
+
+def test_expand_outside_the_cache_writes_nothing(lib):
+    m = Layer(lib, [128, 128], hq=2, hkv=2, r=64, dn=64, dv=64)
+    k, v, kr, _ = run_expand(m, [-3, 126], [5, 6], spare=0)
+    got = f64(k)
+    assert np.all(got[:3] == 55) and np.all(got[7:] == 55)      # positions -3..-1, and 128..131
+    want = m.c64[[0, 1, 254, 255]] @ m.Bk64
+    assert np.allclose(got[3:7].reshape(4, -1), want, atol=0.02)
+    assert np.array_equal(f64(kr)[3:7], m.kr64[[0, 1, 254, 255]])
+
+
+# ---------------------------------------------------------------------------
+# ragged attention
+# ---------------------------------------------------------------------------
+
+def attn_case(lib, nq, nk, hq=4, hkv=4, dn=128, dr=64, dv=128, seed=0, amp=1.5, behind=5, scale=0.0):
+    """Inputs of ragged attention, with non-finite rows behind the last sequence."""
+    rng = np.random.default_rng(seed)
+    Tq, Tk = sum(nq), sum(nk)
+    q = bf16(rng.standard_normal((Tq + 2, hq, dn + dr)) * amp)
+    k, kr, v = (rng.standard_normal(x) for x in ((Tk + behind, hkv, dn), (Tk + behind, dr), (Tk + behind, hkv, dv)))
+    if behind:
+        k[Tk:], kr[Tk:], v[Tk:] = np.nan, np.inf, np.inf
+    d = lib.make_shared_desc(1, hq, hkv, dn, dr, dv, 64, 128, softmax_scale=scale)
+    cache = lib.lr_shared_create(d, bf16(np.zeros((64, hkv * dn))), bf16(np.zeros((64, hkv * dv))))
+    cu = [i32(np.concatenate([[0], np.cumsum(x)])) for x in (nq, nk)]
+    return cache, q, bf16(k), bf16(kr), bf16(v), cu
+
+
+def run_attn(lib, cache, q, k, kr, v, cu, causal):
+    import torch
+    d = cache.desc
+    out = torch.full((q.shape[0], d.n_q_heads, d.dim_v), 33.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((q.shape[0], d.n_q_heads), 33.0, dtype=torch.float32, device="cuda")
+    lib.lr_shared_attn(cache, q, k, kr, v, cu[0], cu[1], out, lse, causal=causal)
+    assert lib.lr_shared_device_error(cache) == 0
+    return out, lse
+
+
+def check_attn(q, k, kr, v, nq, nk, causal, scale, out, lse):
+    """Scores: dn + dr fp32 steps, log2 / exp2 in fp32 (2^-20 of their size): E.  Weights: one bf16
+    rounding; sums: (m + 64) fp32 steps; the output: u of its value."""
+    q64, k64, kr64, v64, o64, l64 = map(f64, (q, k, kr, v, out, lse))
+    a = b = 0
+    for n, m in zip(nq, nk):
+        Q, K, R, V = q64[a:a + n], k64[b:b + m], kr64[b:b + m], v64[b:b + m]
+        g = Q.shape[1] // K.shape[1]
+        for j in range(Q.shape[1]):
+            key = np.concatenate([K[:, j // g], R], axis=1)
+            s = Q[:, j] @ key.T * scale
+            if causal:
+                s = np.where(np.arange(m) <= np.arange(n)[:, None] + m - n, s, -np.inf)
+            none = ~np.any(np.isfinite(s), axis=1) if m else np.ones(n, bool)
+            assert np.all(o64[a:a + n, j][none] == 0) and np.all(np.isneginf(l64[a:a + n, j][none]))
+            if np.all(none):
+                continue
+            s = s[~none]
+            top = s.max(axis=1, keepdims=True)
+            p = np.exp(s - top)
+            tot = p.sum(axis=1, keepdims=True)
+            rl = (top + np.log(tot))[:, 0]
+            p /= tot
+            ro, mix = p @ V[:, j // g], p @ np.abs(V[:, j // g])
+            mag = (np.abs(Q[:, j][~none]) @ np.abs(key).T).max(axis=1) * scale
+            E = ((key.shape[1] + 8) * F + 2.0 ** -20) * mag
+            assert np.all(np.abs(l64[a:a + n, j][~none] - rl) <= E + (m + 64) * F + 2.0 ** -21 * np.abs(rl)), (n, m, j)
+            tol = U * np.abs(ro) + (U + 2 * E[:, None] + (m + 64) * F) * mix
+            err = np.abs(o64[a:a + n, j][~none] - ro)
+            assert np.all(err <= tol), (n, m, j, (err / tol).max())
+        a, b = a + n, b + m
+    assert np.all(o64[a:] == 33) and np.all(l64[a:] == 33)       # rows behind the last sequence: untouched
+
+
+RAGGED = [([1, 127, 128, 129, 0, 257, 300], [1, 127, 128, 129, 0, 257, 300]),      # prompts
+          ([1, 5, 130, 256, 1], [300, 128, 700, 1000, 129]),                         # chunks of longer contexts
+          ([200, 3, 300, 2], [5, 0, 129, 1])]                                        # fewer keys than queries
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk", RAGGED)
+@pytest.mark.parametrize("hq,hkv,dn,dr,dv", [(4, 4, 128, 64, 128), (6, 2, 64, 32, 64), (3, 3, 128, 32, 64),
+                                             (4, 1, 64, 64, 128)])
+def test_attn_matches_the_oracle(lib, nq, nk, causal, hq, hkv, dn, dr, dv):
+    case = attn_case(lib, nq, nk, hq, hkv, dn, dr, dv)
+    out, lse = run_attn(lib, *case, causal)
+    check_attn(*case[1:5], nq, nk, causal, (dn + dr) ** -0.5, out, lse)
+
+
+@pytest.mark.parametrize("amp", [0.0, 40.0])
+def test_attn_equal_and_sharp_weights(lib, amp):
+    nq = nk = [700, 130]
+    case = attn_case(lib, nq, nk, amp=amp)
+    out, lse = run_attn(lib, *case, True)
+    check_attn(*case[1:5], nq, nk, True, 192 ** -0.5, out, lse)
+
+
+def test_attn_rising_scores_raise_the_maximum_often(lib):
+    """Keys that grow along the sequence: every key tile raises the running maximum, so O is
+    rescaled again and again."""
+    import torch
+    nq, nk = [260], [1500]
+    cache, q, k, kr, v, cu = attn_case(lib, nq, nk, 2, 2, 64, 64, 64, behind=0, scale=1.0)
+    ramp = torch.arange(1500, device="cuda").float() / 10
+    q[:, :, 0], k[:, :, 0] = 1.0, ramp[:, None].to(torch.bfloat16)
+    out, lse = run_attn(lib, cache, q, k, kr, v, cu, True)
+    check_attn(q, k, kr, v, nq, nk, True, 1.0, out, lse)
+
+
+def test_attn_without_keys_or_queries(lib):
+    import torch
+    cache, q, k, kr, v, cu = attn_case(lib, [3, 4], [0, 0], behind=0)
+    out, lse = run_attn(lib, cache, q, k, kr, v, cu, False)
+    assert torch.all(out[:7] == 0) and torch.all(torch.isneginf(lse[:7])) and torch.all(out[7:] == 33)
+    lib.lr_shared_attn(cache, q[:0], k, kr, v, i32([0]), i32([0]), out[:0], lse[:0])
+
+
+def test_attn_joins_over_key_ranges_by_lse(lib):
+    """A chunk against its context in two calls (the context whole, itself causal) equals one call."""
+    import torch
+    n, ctx = 150, 400
+    cache, q, k, kr, v, cu = attn_case(lib, [n], [ctx + n], behind=0)
+    q = q[:n].contiguous()
+    whole, wl = run_attn(lib, cache, q, k, kr, v, cu, True)
+    a, al = run_attn(lib, cache, q, k[:ctx], kr[:ctx], v[:ctx], (cu[0], i32([0, ctx])), False)
+    b, bl = run_attn(lib, cache, q, k[ctx:], kr[ctx:], v[ctx:], (cu[0], i32([0, n])), True)
+    l = torch.logaddexp(al, bl)
+    joined = a.float() * (al - l).exp()[..., None] + b.float() * (bl - l).exp()[..., None]
+    assert torch.allclose(l, wl, atol=1e-5, rtol=1e-5)
+    # each side is within u (|o| + mix) of the truth; |v| <= 6 here
+    assert (joined - whole.float()).abs().max() <= 4 * U * 6
+
+
+def test_attn_captured_and_replayed_with_other_lengths(lib):
+    import torch
+    nq, nk = [100, 300], [300, 301]
+    cache, q, k, kr, v, cu = attn_case(lib, nq, nk)
+    out = torch.zeros((q.shape[0], 4, 128), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((q.shape[0], 4), dtype=torch.float32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lib.lr_shared_attn(cache, q, k, kr, v, cu[0], cu[1], out, lse)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.lr_shared_attn(cache, q, k, kr, v, cu[0], cu[1], out, lse)
+    for nq, nk in (([100, 300], [300, 301]), ([257, 143], [600, 1]), ([0, 1], [5, 600 - 5])):
+        cu[0].copy_(i32(np.concatenate([[0], np.cumsum(nq)])))
+        cu[1].copy_(i32(np.concatenate([[0], np.cumsum(nk)])))
+        out.fill_(33.0), lse.fill_(33.0)
+        g.replay()
+        check_attn(q, k, kr, v, nq, nk, True, 192 ** -0.5, out, lse)
+
+
+# ---------------------------------------------------------------------------
+# as they are used together
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [0, 8])
+def test_prompts_then_steps(lib, bits):
+    """Two prompts written, expanded and attended; then three decode steps, each writing its token
+    first.  Every result against full attention over what the cache stands for."""
+    import torch
+    H, r, dn, dr, dv, theta = 6, 192, 128, 64, 128, 1e4
+    scale, lens, steps = (dn + dr) ** -0.5, [200, 126], 3
+    rng = np.random.default_rng(5)
+    T = [n + steps for n in lens]
+    c = [bf16(rng.standard_normal((n, r))) for n in T]
+    kr = [bf16(rng.standard_normal((n, dr))) for n in T]
+    q = [bf16(rng.standard_normal((n, H, dn + dr))) for n in T]
+    Bk, Bv = bf16(rng.standard_normal((r, H * dn)) / r ** 0.5), bf16(rng.standard_normal((r, H * dv)) / r ** 0.5)
+    d = lib.make_shared_desc(2, H, H, dn, dr, dv, r, 256, quant_bits=bits, rope_theta=theta)
+    cache = lib.lr_shared_create(d, Bk, Bv)
+    lib.lr_shared_set_block_table(cache, np.array([[3, 0], [1, 2]]))
+    lib.lr_shared_append(cache, torch.cat([x[:n] for x, n in zip(c, lens)]),
+                         torch.cat([x[:n] for x, n in zip(kr, lens)]),
+                         i32(np.repeat([0, 1], lens)), i32(np.concatenate([np.arange(n) for n in lens])))
+    cu = i32([0, lens[0], sum(lens)])
+    k = torch.zeros((sum(lens), H, dn), dtype=torch.bfloat16, device="cuda")
+    v, kx = torch.zeros_like(k), torch.zeros((sum(lens), dr), dtype=torch.bfloat16, device="cuda")
+    lib.lr_shared_expand(cache, cu, k, v, kx)
+    qp = torch.cat([x[:n] for x, n in zip(q, lens)])
+    out, lse = torch.zeros((sum(lens), H, dv), dtype=torch.bfloat16, device="cuda"), torch.zeros(
+        (sum(lens), H), dtype=torch.float32, device="cuda")
+    lib.lr_shared_attn(cache, qp, k, kx, v, cu, cu, out, lse)
+    got = [[f64(out[:lens[0]])], [f64(out[lens[0]:])]]
+    for s in range(steps):
+        pos = [n + s for n in lens]
+        lib.lr_shared_append(cache, torch.stack([x[p] for x, p in zip(c, pos)]),
+                             torch.stack([x[p] for x, p in zip(kr, pos)]), i32([0, 1]), i32(pos))
+        o = torch.zeros((2, 1, H, dv), dtype=torch.bfloat16, device="cuda")
+        lib.lr_shared_decode(cache, torch.stack([x[p:p + 1] for x, p in zip(q, pos)]), i32([p + 1 for p in pos]), o)
+        for b in range(2):
+            got[b].append(f64(o[b]))
+    for b, n in enumerate(T):
+        z = f64(c[b])
+        z = S.quantize_e4m3(z) if bits else z
+        ref, _, mix = S.attention(f64(q[b]), S.expand(z, f64(Bk), H), S.rotate(f64(kr[b]), np.arange(n), theta),
+                                  S.expand(z, f64(Bv), H), scale)
+        # stored rotary keys and expanded keys are rounded to bf16: scores move by at most
+        # u scale sum |q| |k|, which here stays below 0.2; values by u
+        err = np.abs(np.concatenate(got[b]) - ref)
+        assert np.sqrt((err ** 2).mean()) <= 2 * U * np.sqrt((mix ** 2).mean())
+        assert err.max() <= 0.25 * mix.max()
+
+
+# ---------------------------------------------------------------------------
 # refusals
 # ---------------------------------------------------------------------------
 
