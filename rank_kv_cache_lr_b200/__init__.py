@@ -416,9 +416,14 @@ class SharedCache:
     """Handle of one lr_shared (one layer) on one device.  Holds the description for shape checks."""
 
     def __init__(self, handle: ctypes.c_void_p, desc: lr_shared_desc, device: int):
+        import torch
         self.handle = handle
         self.desc = desc
         self.device = device
+        self.f32, self.bf16, self.i32 = torch.float32, torch.bfloat16, torch.int32
+        # the current stream's handle, without building a Stream object where torch offers that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.current_stream = (lambda: raw(device)) if raw else (lambda: torch.cuda.current_stream(device).cuda_stream)
 
     def __del__(self):
         if getattr(self, "handle", None):
@@ -430,28 +435,28 @@ class SharedCache:
 
 
 def _shared_ptr(cache: SharedCache, t, dtype, shape, name, allow_none=False):
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == cache.device \
+            and t.is_contiguous():
+        return t.data_ptr()
     p = _ptr(t, dtype, shape, name, allow_none)
     if t is not None and t.device.index != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.device}")
     return p
 
 
-def _shared_stream(cache: SharedCache, stream) -> ctypes.c_void_p:
-    import torch
-    s = torch.cuda.current_stream(cache.device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _shared_stream(cache: SharedCache, stream):
+    return cache.current_stream() if stream is None else stream.cuda_stream
 
 
 def _shared_rows(cache: SharedCache, t, width: int, n: int, name: str):
     """Pointer and row stride of a [n][width] bf16 tensor whose rows may be spaced."""
-    import torch
-    if not getattr(t, "is_cuda", False) or t.device.index != cache.device:
+    if not getattr(t, "is_cuda", False) or t.get_device() != cache.device:
         raise ValueError(f"{name} must be a tensor on cuda:{cache.device}")
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (n, width):
+    if t.dtype is not cache.bf16 or t.shape != (n, width):
         raise ValueError(f"{name} has dtype {t.dtype} and shape {tuple(t.shape)}, expected bfloat16 {(n, width)}")
     if t.stride(1) != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if n > 1 else width)
+    return t.data_ptr(), (t.stride(0) if n > 1 else width)
 
 
 def lr_shared_create(desc: lr_shared_desc, B_k, B_v, stream=None) -> SharedCache:
@@ -488,63 +493,58 @@ def lr_shared_set_block_table(cache: SharedCache, table, stream=None) -> None:
 def lr_shared_set_block_table_device(cache: SharedCache, table, stream=None) -> None:
     """table: int32 CUDA tensor [batch][capacity / 128] (entries are not checked; the kernels
     clamp them into the pool)."""
-    import torch
     d = cache.desc
     _check(_lib.lr_shared_set_block_table_device(
-        cache.handle, _shared_ptr(cache, table, torch.int32, (d.batch, d.capacity // 128), "table"),
+        cache.handle, _shared_ptr(cache, table, cache.i32, (d.batch, d.capacity // 128), "table"),
         _shared_stream(cache, stream)), "lr_shared_set_block_table_device")
 
 
 def lr_shared_append(cache: SharedCache, c, kr, seq, pos, stream=None) -> None:
     """c: bf16 CUDA tensor [n][rank], kr: [n][dim_rope] (rows may be spaced: columns of a wider
     tensor); seq, pos: int32 CUDA tensors [n], the sequence and position of each token."""
-    import torch
     n = c.shape[0]
     cp, cs = _shared_rows(cache, c, cache.desc.rank, n, "c")
     kp, ks = _shared_rows(cache, kr, cache.desc.dim_rope, n, "kr")
     _check(_lib.lr_shared_append(cache.handle, cp, cs, kp, ks,
-                                 _shared_ptr(cache, seq, torch.int32, (n,), "seq"),
-                                 _shared_ptr(cache, pos, torch.int32, (n,), "pos"), n,
+                                 _shared_ptr(cache, seq, cache.i32, (n,), "seq"),
+                                 _shared_ptr(cache, pos, cache.i32, (n,), "pos"), n,
                                  _shared_stream(cache, stream)), "lr_shared_append")
 
 
 def lr_shared_read(cache: SharedCache, cu, c_out, kr_out, start=None, stream=None) -> None:
     """cu: int32 CUDA tensor [batch + 1], first packed row of every sequence; start: [batch] first
     token of every sequence, or None; c_out: bf16 [total][rank], kr_out: [total][dim_rope]."""
-    import torch
     d, n = cache.desc, c_out.shape[0]
-    _check(_lib.lr_shared_read(cache.handle, _shared_ptr(cache, cu, torch.int32, (d.batch + 1,), "cu"),
-                               _shared_ptr(cache, start, torch.int32, (d.batch,), "start", True), n,
-                               _shared_ptr(cache, c_out, torch.bfloat16, (n, d.rank), "c_out"),
-                               _shared_ptr(cache, kr_out, torch.bfloat16, (n, d.dim_rope), "kr_out"),
+    _check(_lib.lr_shared_read(cache.handle, _shared_ptr(cache, cu, cache.i32, (d.batch + 1,), "cu"),
+                               _shared_ptr(cache, start, cache.i32, (d.batch,), "start", True), n,
+                               _shared_ptr(cache, c_out, cache.bf16, (n, d.rank), "c_out"),
+                               _shared_ptr(cache, kr_out, cache.bf16, (n, d.dim_rope), "kr_out"),
                                _shared_stream(cache, stream)), "lr_shared_read")
 
 
 def lr_shared_decode(cache: SharedCache, q, row_len, out, lse=None, stream=None) -> None:
     """q: bf16 CUDA tensor [batch][n_tokens][Hq][dim_nope + dim_rope]; row_len: int32 [batch];
     out: bf16 [batch][n_tokens][Hq][dim_v]; lse: fp32 [batch][n_tokens][Hq] or None."""
-    import torch
     d = cache.desc
     n = q.shape[1] if q.dim() == 4 else -1
     _check(_lib.lr_shared_decode(
-        cache.handle, _shared_ptr(cache, q, torch.bfloat16, (d.batch, n, d.n_q_heads, d.dim_nope + d.dim_rope), "q"), n,
-        _shared_ptr(cache, row_len, torch.int32, (d.batch,), "row_len"),
-        _shared_ptr(cache, out, torch.bfloat16, (d.batch, n, d.n_q_heads, d.dim_v), "out"),
-        _shared_ptr(cache, lse, torch.float32, (d.batch, n, d.n_q_heads), "lse", True),
+        cache.handle, _shared_ptr(cache, q, cache.bf16, (d.batch, n, d.n_q_heads, d.dim_nope + d.dim_rope), "q"), n,
+        _shared_ptr(cache, row_len, cache.i32, (d.batch,), "row_len"),
+        _shared_ptr(cache, out, cache.bf16, (d.batch, n, d.n_q_heads, d.dim_v), "out"),
+        _shared_ptr(cache, lse, cache.f32, (d.batch, n, d.n_q_heads), "lse", True),
         _shared_stream(cache, stream)), "lr_shared_decode")
 
 
 def lr_shared_expand(cache: SharedCache, cu, k, v, kr, start=None, stream=None) -> None:
     """cu, start: as for lr_shared_read; k: bf16 CUDA tensor [total][Hkv][dim_nope],
     v: [total][Hkv][dim_v], kr: [total][dim_rope]."""
-    import torch
     d, n = cache.desc, k.shape[0]
     _check(_lib.lr_shared_expand(
-        cache.handle, _shared_ptr(cache, cu, torch.int32, (d.batch + 1,), "cu"),
-        _shared_ptr(cache, start, torch.int32, (d.batch,), "start", True), n,
-        _shared_ptr(cache, k, torch.bfloat16, (n, d.n_kv_heads, d.dim_nope), "k"),
-        _shared_ptr(cache, v, torch.bfloat16, (n, d.n_kv_heads, d.dim_v), "v"),
-        _shared_ptr(cache, kr, torch.bfloat16, (n, d.dim_rope), "kr"),
+        cache.handle, _shared_ptr(cache, cu, cache.i32, (d.batch + 1,), "cu"),
+        _shared_ptr(cache, start, cache.i32, (d.batch,), "start", True), n,
+        _shared_ptr(cache, k, cache.bf16, (n, d.n_kv_heads, d.dim_nope), "k"),
+        _shared_ptr(cache, v, cache.bf16, (n, d.n_kv_heads, d.dim_v), "v"),
+        _shared_ptr(cache, kr, cache.bf16, (n, d.dim_rope), "kr"),
         _shared_stream(cache, stream)), "lr_shared_expand")
 
 
@@ -553,18 +553,17 @@ def lr_shared_attn(cache: SharedCache, q, k, kr, v, cu_q, cu_k, out, lse=None, c
     """q: bf16 CUDA tensor [total_q][Hq][dim_nope + dim_rope]; k, kr, v: as lr_shared_expand writes
     them; cu_q, cu_k: int32 [n_seq + 1]; out: bf16 [total_q][Hq][dim_v]; lse: fp32 [total_q][Hq]
     or None."""
-    import torch
     d = cache.desc
     nq, nk, ns = q.shape[0], k.shape[0], cu_q.shape[0] - 1
     _check(_lib.lr_shared_attn(
-        cache.handle, _shared_ptr(cache, q, torch.bfloat16, (nq, d.n_q_heads, d.dim_nope + d.dim_rope), "q"),
-        _shared_ptr(cache, k, torch.bfloat16, (nk, d.n_kv_heads, d.dim_nope), "k"),
-        _shared_ptr(cache, kr, torch.bfloat16, (nk, d.dim_rope), "kr"),
-        _shared_ptr(cache, v, torch.bfloat16, (nk, d.n_kv_heads, d.dim_v), "v"),
-        _shared_ptr(cache, cu_q, torch.int32, (ns + 1,), "cu_q"),
-        _shared_ptr(cache, cu_k, torch.int32, (ns + 1,), "cu_k"), ns, nq, nk, int(bool(causal)),
-        _shared_ptr(cache, out, torch.bfloat16, (nq, d.n_q_heads, d.dim_v), "out"),
-        _shared_ptr(cache, lse, torch.float32, (nq, d.n_q_heads), "lse", True),
+        cache.handle, _shared_ptr(cache, q, cache.bf16, (nq, d.n_q_heads, d.dim_nope + d.dim_rope), "q"),
+        _shared_ptr(cache, k, cache.bf16, (nk, d.n_kv_heads, d.dim_nope), "k"),
+        _shared_ptr(cache, kr, cache.bf16, (nk, d.dim_rope), "kr"),
+        _shared_ptr(cache, v, cache.bf16, (nk, d.n_kv_heads, d.dim_v), "v"),
+        _shared_ptr(cache, cu_q, cache.i32, (ns + 1,), "cu_q"),
+        _shared_ptr(cache, cu_k, cache.i32, (ns + 1,), "cu_k"), ns, nq, nk, int(bool(causal)),
+        _shared_ptr(cache, out, cache.bf16, (nq, d.n_q_heads, d.dim_v), "out"),
+        _shared_ptr(cache, lse, cache.f32, (nq, d.n_q_heads), "lse", True),
         _shared_stream(cache, stream)), "lr_shared_attn")
 
 

@@ -14,9 +14,9 @@
 // Roundings: q~ enters GEMM1 as two bf16 halves, hi and lo = q~ - hi, stacked on N (the
 // A operand's shared-memory reads set the pace for N <= 64, so the second half is nearly
 // free) and added in fp32: the scores, and so lse, carry ~16 bits of q~.  The rotary query is
-// bf16 as given.  p enters GEMM2 as one bf16 (2^-9 relative, at random over the tokens, below
-// the output's own rounding); the output is normalised by the sum of those ROUNDED weights
-// and lse comes from the sum of the unrounded ones, so equal weights carry no common bias.
+// bf16 as given.  p enters GEMM2 as one bf16 (2^-8 relative at most, at random over the tokens,
+// below the output's own rounding); its sum, for lse and the normaliser, is of the unrounded
+// weights in fp32.
 //
 // Work: the 128-token tiles of all sequences, in order, are cut into equal runs on the device
 // (tile_run), one run per CTA column, so ragged batches stay balanced and a captured graph
@@ -48,6 +48,7 @@ struct DecArgs {
   RowMap map;
   int B, cap, r, nch, Hq, n_tok, R, HB, X, nslot;
   float scale_log2;
+  const uint8_t* codes;
   const uint8_t* scale;
   float* part_o;
   float* part_ml;
@@ -62,11 +63,11 @@ struct DecArgs {
 //   rope_empty      1        MMA commit of GEMM1 -> producer
 //   q_full/q_empty  1 + tx / 1   per sequence of the run
 //   s_full[2]       1        MMA commit of GEMM1 -> softmax warps
-//   s_empty[2]      4        softmax warps (scores read) -> MMA issuer
-//   p_full          4        softmax warps -> MMA issuer
+//   s_empty[2]      NR / 2   softmax warps (scores read) -> MMA issuer
+//   p_full          NR / 2   softmax warps -> MMA issuer
 //   p_empty         1        MMA commit of GEMM2 -> softmax warps
 //   o_full          1        MMA commit, last tile of a sequence -> softmax warps
-//   o_empty         4        softmax warps (O~ read) -> MMA issuer
+//   o_empty         NR / 2   softmax warps (O~ read) -> MMA issuer
 //   done            1        final commit: every MMA complete before TMEM is freed
 struct Aux {
   uint64_t raw_full[kMaxSlots], slot_full[kMaxSlots], slot_empty[kMaxSlots];
@@ -75,9 +76,7 @@ struct Aux {
   int abort_flag;
   unsigned long long wait_ns;
   TileRun run;
-  float red[4][32];
-  float m_s[32];
-  float alpha_s[32];
+  float red[4][4][8];          // [column group][lane quarter][column]
   int off_s[32];               // row j sees tokens t < len + off_s[j]
 };
 static_assert(sizeof(Aux) <= kAuxBytes, "aux block");
@@ -114,51 +113,83 @@ __device__ __forceinline__ bool next_seg(TileRun* run, const DecArgs& p, Seg* s)
   return false;
 }
 
-template <int NR>
-__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[NR]) {
-  if constexpr (NR == 32) ptx::tmem_ld32(taddr, r);
-  else ptx::tmem_ld16(taddr, r);
-}
-
-// Butterfly reduction over a warp: on return lane l (l < NR) holds op over all lanes of v[l].
-template <int NR, bool kMax>
-__device__ __forceinline__ float reduce_cols(float (&v)[NR], int lane) {
-  if constexpr (NR == 32) {
-    return tc::warp_reduce_scatter32<kMax>(v, lane);
-  } else {
+// Butterfly reduction of 8 columns over a warp: lane l holds op over all lanes of v[l % 8].
+template <bool kMax>
+__device__ __forceinline__ float reduce_cols(float (&v)[8], int lane) {
 #pragma unroll
-    for (int w = 8; w >= 1; w >>= 1) {
-      const bool up = (lane & w) != 0;
+  for (int w = 4; w >= 1; w >>= 1) {
+    const bool up = (lane & w) != 0;
 #pragma unroll
-      for (int k = 0; k < w; ++k) {
-        const float keep = up ? v[k + w] : v[k];
-        const float send = up ? v[k] : v[k + w];
-        const float got = __shfl_xor_sync(0xffffffffu, send, w);
-        v[k] = kMax ? fmaxf(keep, got) : keep + got;
-      }
+    for (int k = 0; k < w; ++k) {
+      const float keep = up ? v[k + w] : v[k];
+      const float send = up ? v[k] : v[k + w];
+      const float got = __shfl_xor_sync(0xffffffffu, send, w);
+      v[k] = kMax ? fmaxf(keep, got) : keep + got;
     }
-    const float o = __shfl_xor_sync(0xffffffffu, v[0], 16);
-    return kMax ? fmaxf(v[0], o) : v[0] + o;
   }
+  float r = v[0];
+#pragma unroll
+  for (int o = 8; o <= 16; o <<= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, r, o);
+    r = kMax ? fmaxf(r, got) : r + got;
+  }
+  return r;
 }
 
-// Four e4m3 codes (one word) as bf16, times 2^e (both factors exact).  A code's sign, exponent
-// and mantissa bits placed in a bf16 stand for its value times 2^-120 (subnormals included).
-__device__ __forceinline__ uint2 expand4(uint32_t w, __nv_bfloat162 up, __nv_bfloat162 sc) {
-  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);   // byte << 8 per half
-  const uint32_t x = (a & 0x80008000u) | ((a & 0x7F007F00u) >> 4);
-  const uint32_t y = (b & 0x80008000u) | ((b & 0x7F007F00u) >> 4);
-  const __nv_bfloat162 fx = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), up), sc);
-  const __nv_bfloat162 fy = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), up), sc);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&fx), *reinterpret_cast<const uint32_t*>(&fy));
+// Two e4m3 codes as bf16 before their scale: a code's sign, exponent and mantissa bits placed in
+// a bf16 stand for its value times 2^-120 (subnormals included).  sel picks bytes (i, j) as
+// halves with the sign replicated above each (selector bit 3).
+template <uint32_t kSel>
+__device__ __forceinline__ __nv_bfloat162 place2(uint32_t w) {
+  uint32_t a;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(a) : "r"(w), "n"(kSel));
+  a = (a << 4) & 0x87F087F0u;
+  return *reinterpret_cast<const __nv_bfloat162*>(&a);
 }
+// Sixteen codes of one token (their words in the order in which they are stored), times 2^e, to
+// two 16-byte columns of a swizzled row: w.x, w.y to address a0 and w.z, w.w to a1.  e <= 7
+// (exponent byte at most 134): 2^(120 + e) is a bf16, so one exact product; kTwo: two products.
+template <bool kTwo>
+__device__ __forceinline__ void expand16(const uint4& w, uint32_t eb, uint32_t a0, uint32_t a1) {
+  // 2^e = 2^(b1 - 127) 2^(b2 - 127) with 120 folded into the first; byte 255 (a group that held a
+  // NaN or an infinity) is NaN
+  const uint32_t b1 = kTwo ? min(eb + 120u, 254u) : eb + 120u;
+  const uint32_t h1 = kTwo && eb == 255u ? 0x7FC07FC0u : b1 * 0x00800080u;
+  const uint32_t h2 = (eb + 247u - b1) * 0x00800080u;
+  const __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162*>(&h1);
+  const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&h2);
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    __nv_bfloat162 x = __hmul2(place2<0x9180>(in[k]), s1), y = __hmul2(place2<0xB3A2>(in[k]), s1);
+    if (kTwo) {
+      x = __hmul2(x, s2);
+      y = __hmul2(y, s2);
+    }
+    o[2 * k] = *reinterpret_cast<const uint32_t*>(&x);
+    o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+               : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+               : "memory");
+}
+// A warp-uniform value, known as such to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Shared memory: [aux][q~: r/64 blocks of (2 NR rows hi | lo) x 128 B][q_rope: NR rows x 128 B]
 // [P: 128 tokens x NR][slots][rotary tile][8 bits: scales per slot].
-// Warps: 0 TMA producer, 1 MMA issuer, 2..5 softmax and epilogue (thread = token row = TMEM
-// lane; in the epilogue rank row), 6..13 (8 bits) expand codes to bf16.
+// Warps: 0 TMA producer, 1 MMA issuer, then NR / 2 softmax warps (thread = token row = TMEM lane
+// of one group of 8 query rows; four warps a group; in the epilogue thread = rank row), then
+// (8 bits) 8 warps that expand codes to bf16.  One warp per lane quarter for all 32 columns had
+// taken ~4 us a tile: a single warp per scheduler cannot hide its own latencies.
 template <int NR, bool kQuant>
-__global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
+constexpr int dec_threads() {
+  return 64 + NR * 16 + (kQuant ? 256 : 0);
+}
+template <int NR, bool kQuant>
+__global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     k_shared_decode(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
                     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_kr,
                     const DecArgs p) {
@@ -193,12 +224,12 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
     ptx::mbar_init(&aux->q_empty, 1);
     for (int k = 0; k < 2; ++k) {
       ptx::mbar_init(&aux->s_full[k], 1);
-      ptx::mbar_init(&aux->s_empty[k], 4);
+      ptx::mbar_init(&aux->s_empty[k], NR / 2);
     }
-    ptx::mbar_init(&aux->p_full, 4);
+    ptx::mbar_init(&aux->p_full, NR / 2);
     ptx::mbar_init(&aux->p_empty, 1);
     ptx::mbar_init(&aux->o_full, 1);
-    ptx::mbar_init(&aux->o_empty, 4);
+    ptx::mbar_init(&aux->o_empty, NR / 2);
     ptx::mbar_init(&aux->done, 1);
     aux->abort_flag = 0;
     aux->wait_ns = tc::wait_limit(p.wait_ns);
@@ -242,17 +273,21 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
           ptx::tma_load_2d(q_s + s * kQSub, &tm_q, &aux->q_full, s * 64, (sg.b * p.HB + hb) * 2 * NR);
         ptx::tma_load_3d(qr_s, &tm_qr, &aux->q_full, 0, hb * NR, sg.b);
         ++nseg;
+        int next_page = p.map.page(sg.b, sg.t0 * 128);
         for (int i = 0; i < sg.nt && ok; ++i, ++gt) {
-          const int page = p.map.page(sg.b, (sg.t0 + i) * 128);
+          const int page = next_page;
+          // the table is read one tile ahead, so that its latency is not between two copies
+          if (i + 1 < sg.nt) next_page = p.map.page(sg.b, (sg.t0 + i + 1) * 128);
           for (int c = 0; c < p.nch; ++c) {
             const int slot = pos % p.nslot, round = pos / p.nslot;
             if (round > 0 && !(ok = wait_b(&aux->slot_empty[slot], (round - 1) & 1, aux, p.err))) break;
             uint8_t* dst = ring + slot * kSlot;
             if (kQuant) {
               // codes into the upper half of their slot, where the expansion reads them before
-              // it writes (box columns past the rank read as 0)
-              ptx::mbar_arrive_expect_tx(&aux->raw_full[slot], kSub + kScaleBytes);
-              ptx::tma_load_2d(dst + kSub, &tm_c, &aux->raw_full[slot], c * 128, page * 128);
+              // it writes
+              const uint32_t bytes = c * 128 + 64 < p.r ? kSub : kSub / 2;
+              ptx::mbar_arrive_expect_tx(&aux->raw_full[slot], bytes + kScaleBytes);
+              ptx::bulk_load(dst + kSub, p.codes + (long long)page * 128 * p.r + c * kSub, bytes, &aux->raw_full[slot]);
               ptx::bulk_load(sc_s + slot * kScaleBytes, p.scale + ((long long)page * p.nch + c) * kScaleBytes,
                              kScaleBytes, &aux->raw_full[slot]);
             } else {
@@ -280,6 +315,8 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
     const uint32_t id1 = ptx::idesc_f16(1, 0, 0, 128, 2 * NR);   // GEMM1: K-major x K-major (hi | lo)
     const uint32_t idr = ptx::idesc_f16(1, 0, 0, 128, NR);       //        rotary part, into the hi columns
     const uint32_t id2 = ptx::idesc_f16(1, 1, 1, 128, NR);       // GEMM2: MN-major x MN-major
+    // Operands go through `uniform`: the compiler then keeps them in uniform registers, and an
+    // MMA issues every ~40 cycles (the pace of an operand read from shared memory) and not ~115.
     const uint64_t kd0 = ptx::smem_desc(ptx::smem_u32(ring), 16, 1024, 2);
     const uint64_t vd0 = ptx::smem_desc(ptx::smem_u32(ring), kSub, 1024, 2);
     const uint64_t qd0 = ptx::smem_desc(ptx::smem_u32(q_s), 16, 1024, 2);
@@ -303,19 +340,22 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
           const int sb = gt & 1;
           if (gt >= 2 && !(ok = wait_w(&aux->s_empty[sb], ((gt - 2) >> 1) & 1, aux, p.err))) break;
           ptx::tc_fence_after();
-          const uint32_t d_s = tmem + kSCol + 64 * sb;
+          const uint32_t d_s = uniform(tmem + kSCol + 64 * sb);
           for (int c = 0; c < p.nch; ++c) {
             const int pos = gt * p.nch + c, slot = pos % p.nslot;
             if (!(ok = wait_w(&aux->slot_full[slot], (pos / p.nslot) & 1, aux, p.err))) break;
             ptx::tc_fence_after();
-            const uint64_t a0 = kd0 + (uint64_t)((slot * kSlot) >> 4);
-            const uint64_t b0 = qd0 + (uint64_t)((c * 2 * kQSub) >> 4);
-            const int nk = min(8, (p.r - c * 128) >> 4);
+            const uint64_t a0 = kd0 + uniform((slot * kSlot) >> 4);
+            const uint64_t b0 = qd0 + uniform((c * 2 * kQSub) >> 4);
+            const uint32_t first = uniform(c ? 1u : 0u);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint64_t ad = a0 + (uint64_t)((kk >> 2) * (kSub >> 4) + (kk & 3) * 2);
-              const uint64_t bd = b0 + (uint64_t)((kk >> 2) * (kQSub >> 4) + (kk & 3) * 2);
-              if (kk < nk) ptx::mma_f16_elect(d_s, ad, bd, id1, (c | kk) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              ptx::mma_f16_elect(d_s, a0 + (uint64_t)(kk * 2), b0 + (uint64_t)(kk * 2), id1, kk ? 1u : first);
+            if (c * 128 + 64 < p.r) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                ptx::mma_f16_elect(d_s, a0 + (uint64_t)((kSub >> 4) + kk * 2), b0 + (uint64_t)((kQSub >> 4) + kk * 2),
+                                   id1, 1u);
             }
           }
           if (!ok || !(ok = wait_w(&aux->rope_full, gt & 1, aux, p.err))) break;
@@ -330,13 +370,14 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
           if (!(ok = wait_w(&aux->p_full, gt & 1, aux, p.err))) break;
           if (i == 0 && nseg > 0 && !(ok = wait_w(&aux->o_empty, (nseg - 1) & 1, aux, p.err))) break;
           ptx::tc_fence_after();
+          const uint32_t first = uniform(i ? 1u : 0u);
           for (int c = 0; c < p.nch; ++c) {
             const int slot = (gt * p.nch + c) % p.nslot;
-            const uint64_t a0 = vd0 + (uint64_t)((slot * kSlot) >> 4);
+            const uint64_t a0 = vd0 + uniform((slot * kSlot) >> 4);
+            const uint32_t d_o = uniform(tmem + kOCol + c * NR);
 #pragma unroll
             for (int kt = 0; kt < 8; ++kt)
-              ptx::mma_f16_elect(tmem + kOCol + c * NR, a0 + (uint64_t)(kt * 128), pd0 + (uint64_t)(kt * 16), id2,
-                                 (i | kt) ? 1u : 0u);
+              ptx::mma_f16_elect(d_o, a0 + (uint64_t)(kt * 128), pd0 + (uint64_t)(kt * 16), id2, kt ? 1u : first);
             ptx::mma_commit_elect(&aux->slot_empty[slot]);
           }
           ptx::mma_commit_elect(&aux->p_empty);
@@ -349,127 +390,108 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
     ptx::mma_commit_elect(&aux->done);
     drain_wait(&aux->done, 0);
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < 2 + NR / 2) {
     // ------------------------------------------------------------- softmax / epilogue
-    const int qd = warp & 3;
+    const int qd = warp & 3, g = (warp - 2) >> 2;        // lane quarter, column group
     const int row = qd * 32 + lane;
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+    const int bar = 1 + g;                               // the group's four warps
     int gt = 0, nseg = 0;
     bool ok = true;
     while (ok && next_seg(&run, p, &sg)) {
-      float l[NR], lr[NR];                 // sums of the weights and of the rounded weights
+      float m[8], l[8];                                  // in units of log2; alike in the whole group
 #pragma unroll
-      for (int j = 0; j < NR; ++j) l[j] = lr[j] = 0.f;
-      if (qd == 0) aux->m_s[lane] = kNoMax;
-      ptx::named_bar_sync(1, 128);
+      for (int j = 0; j < 8; ++j) {
+        m[j] = kNoMax;
+        l[j] = 0.f;
+      }
       for (int i = 0; i < sg.nt; ++i, ++gt) {
         const int k2 = gt & 1;
         const int t = (sg.t0 + i) * 128 + row;
-        const uint32_t s_col = tmem + lane_off + kSCol + 64 * k2;
-        ok = ptx::named_bar_and(1, 128, wait_b(&aux->s_full[k2], (gt >> 1) & 1, aux, p.err));
-        if (!ok) break;
+        const uint32_t s_col = tmem + lane_off + kSCol + 64 * k2 + 8 * g;
+        // after an abort every wait returns at once: the group's warps finish the sequence in step
+        // (their barriers stay matched) and leave at the verdict below
+        (void)wait_w(&aux->s_full[k2], (gt >> 1) & 1, aux, p.err);
         ptx::tc_fence_after();
         // a tile every row sees whole needs no masks; otherwise row j sees t < len + off_s[j]
         const bool edge = (sg.t0 + i) * 128 + 128 > sg.len - (p.n_tok - 1);
-        float s[NR];
-        auto load_s = [&]() {
+        float s[8];
+        {
+          uint32_t a[8], b[8];
+          ptx::tmem_ld8(s_col, a);
+          ptx::tmem_ld8(s_col + NR, b);
+          ptx::tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < NR / 16; ++h) {
-            uint32_t a[16], b[16];
-            ptx::tmem_ld16(s_col + 16 * h, a);
-            ptx::tmem_ld16(s_col + NR + 16 * h, b);
-            ptx::tmem_wait_ld();
+          for (int j = 0; j < 8; ++j) s[j] = (__uint_as_float(a[j]) + __uint_as_float(b[j])) * p.scale_log2;
+        }
+        if (edge) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              s[16 * h + j] = (__uint_as_float(a[j]) + __uint_as_float(b[j])) * p.scale_log2;
-          }
-          if (edge) {
-#pragma unroll
-            for (int j = 0; j < NR; ++j) s[j] = t < sg.len + aux->off_s[j] ? s[j] : -INFINITY;
-          }
-        };
-        load_s();
+          for (int j = 0; j < 8; ++j) s[j] = t < sg.len + aux->off_s[8 * g + j] ? s[j] : -INFINITY;
+        }
         bool ex = false;
 #pragma unroll
-        for (int j = 0; j < NR; ++j) ex |= s[j] > aux->m_s[j] + kLazy;
-        ex = ptx::named_bar_or(1, 128, ex);
+        for (int j = 0; j < 8; ++j) ex |= s[j] > m[j] + kLazy;
+        ex = ptx::named_bar_or(bar, 128, ex);
         if (gt > 0) {   // the value mix before has completed: P may be rewritten, O~ rescaled
-          ok = ptx::named_bar_and(1, 128, wait_b(&aux->p_empty, (gt - 1) & 1, aux, p.err));
-          if (!ok) break;
+          (void)wait_w(&aux->p_empty, (gt - 1) & 1, aux, p.err);
           ptx::tc_fence_after();
         }
         if (!kQuant && t >= sg.len) {
           // rows behind the sequence hold whatever the page held: 0 weight times a stale
-          // infinity would still be NaN, so their values become 0
-          for (int c = 0; c < p.nch; ++c) {
-            const uint32_t base = ptx::smem_u32(ring + ((gt * p.nch + c) % p.nslot) * kSlot + row * 128);
+          // infinity would still be NaN, so their values become 0 (the groups share the boxes)
+          for (int c = g; c < 2 * p.nch; c += NR / 8) {
+            const uint32_t base =
+                ptx::smem_u32(ring + ((gt * p.nch + (c >> 1)) % p.nslot) * kSlot + (c & 1) * kSub + row * 128);
 #pragma unroll
-            for (int v = 0; v < 16; ++v)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + (v >> 3) * kSub + (v & 7) * 16),
-                           "r"(0)
-                           : "memory");
+            for (int v = 0; v < 8; ++v)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + v * 16), "r"(0) : "memory");
           }
         }
         __syncwarp();
         if (ex) {
-          const float top = reduce_cols<NR, true>(s, lane);
-          aux->red[qd][lane] = top;
-          load_s();
-          ptx::named_bar_sync(1, 128);
-          if (qd == 0 && lane < NR) {
-            const float mt =
-                fmaxf(fmaxf(aux->red[0][lane], aux->red[1][lane]), fmaxf(aux->red[2][lane], aux->red[3][lane]));
-            const float mo = aux->m_s[lane];
-            const float mn = fmaxf(mo, mt);
-            aux->alpha_s[lane] = exp2f(mo - mn);
-            aux->m_s[lane] = mn;
-          }
-          ptx::named_bar_sync(1, 128);
+          float top[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top[j] = s[j];
+          const float mt = reduce_cols<true>(top, lane);
+          if (lane < 8) aux->red[g][qd][lane] = mt;   // read by all before the next tile's vote
+          ptx::named_bar_sync(bar, 128);
+          float a[8];
           bool need_o = false;
 #pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            const float a = aux->alpha_s[j];
-            l[j] *= a;
-            lr[j] *= a;
-            need_o |= a < 1.f;
+          for (int j = 0; j < 8; ++j) {
+            const float mn = fmaxf(m[j], fmaxf(fmaxf(aux->red[g][0][j], aux->red[g][1][j]),
+                                               fmaxf(aux->red[g][2][j], aux->red[g][3][j])));
+            a[j] = ptx::ex2_approx(m[j] - mn);
+            m[j] = mn;
+            l[j] *= a[j];
+            need_o |= a[j] < 1.f;
           }
           if (need_o && i > 0) {
             for (int c = 0; c < p.nch; ++c) {
-              uint32_t v2[16];
+              uint32_t v[8];
+              const uint32_t col = tmem + lane_off + kOCol + c * NR + 8 * g;
+              ptx::tmem_ld8(col, v);
+              ptx::tmem_wait_ld();
 #pragma unroll
-              for (int h = 0; h < NR / 16; ++h) {
-                const uint32_t col = tmem + lane_off + kOCol + c * NR + 16 * h;
-                ptx::tmem_ld16(col, v2);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  v2[j] = __float_as_uint(__uint_as_float(v2[j]) * aux->alpha_s[16 * h + j]);
-                ptx::tmem_st16(col, v2);
-              }
+              for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * a[j]);
+              ptx::tmem_st8(col, v);
             }
             ptx::tmem_wait_st();
           }
         }
-        const uint32_t prow = ptx::smem_u32(p_s + row * 16);
+        uint32_t hw[4];
 #pragma unroll
-        for (int hg = 0; hg < NR / 8; ++hg) {
-          uint32_t hw[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = hg * 8 + 2 * e;
-            const float p0 = exp2f(s[j] - aux->m_s[j]);
-            const float p1 = exp2f(s[j + 1] - aux->m_s[j + 1]);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-            l[j] += p0;
-            l[j + 1] += p1;
-            lr[j] += __low2float(h);
-            lr[j + 1] += __high2float(h);
-            hw[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + hg * 2048), "r"(hw[0]), "r"(hw[1]),
-                       "r"(hw[2]), "r"(hw[3])
-                       : "memory");
+        for (int e = 0; e < 4; ++e) {
+          const float p0 = ptx::ex2_approx(s[2 * e] - m[2 * e]);
+          const float p1 = ptx::ex2_approx(s[2 * e + 1] - m[2 * e + 1]);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+          l[2 * e] += p0;
+          l[2 * e + 1] += p1;
+          hw[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(ptx::smem_u32(p_s + g * 2048 + row * 16)),
+                     "r"(hw[0]), "r"(hw[1]), "r"(hw[2]), "r"(hw[3])
+                     : "memory");
         // every lane makes its own stores visible to the tensor core, then one arrival per warp
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
@@ -479,46 +501,40 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
           ptx::mbar_arrive(&aux->p_full);
         }
       }
-      if (!ok) break;
-      ok = ptx::named_bar_and(1, 128, wait_b(&aux->o_full, nseg & 1, aux, p.err));
+      ok = ptx::named_bar_and(bar, 128, wait_b(&aux->o_full, nseg & 1, aux, p.err));
       if (!ok) break;
       ptx::tc_fence_after();
-      const size_t base = ((size_t)(x + sg.b) * p.HB + hb) * NR;
-      const float lt = reduce_cols<NR, false>(l, lane);
-      const float lrt = reduce_cols<NR, false>(lr, lane);
-      aux->red[qd][lane] = lt;
-      ptx::named_bar_sync(1, 128);
-      float l4 = 0.f;
-      if (qd == 0) l4 = (aux->red[0][lane] + aux->red[1][lane]) + (aux->red[2][lane] + aux->red[3][lane]);
-      ptx::named_bar_sync(1, 128);
-      aux->red[qd][lane] = lrt;
-      ptx::named_bar_sync(1, 128);
-      if (qd == 0 && lane < NR) {
-        const float r4 = (aux->red[0][lane] + aux->red[1][lane]) + (aux->red[2][lane] + aux->red[3][lane]);
-        reinterpret_cast<float4*>(p.part_ml)[base + lane] = make_float4(aux->m_s[lane], l4, r4, 0.f);
+      const size_t base = ((size_t)(x + sg.b) * p.HB + hb) * NR + 8 * g;
+      const float lt = reduce_cols<false>(l, lane);
+      if (lane < 8) aux->red[g][qd][lane] = lt;
+      ptx::named_bar_sync(bar, 128);
+      if (qd == 0 && lane < 8) {
+        float mj = m[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) mj = lane == j ? m[j] : mj;
+        const float l4 = (aux->red[g][0][lane] + aux->red[g][1][lane]) + (aux->red[g][2][lane] + aux->red[g][3][lane]);
+        reinterpret_cast<float2*>(p.part_ml)[base + lane] = make_float2(mj, l4);
       }
       for (int c = 0; c < p.nch; ++c) {
-        uint32_t o[NR];
-        tmem_ld_n<NR>(tmem + lane_off + kOCol + c * NR, o);
+        uint32_t o[8];
+        ptx::tmem_ld8(tmem + lane_off + kOCol + c * NR + 8 * g, o);
         ptx::tmem_wait_ld();
         const int e = c * 128 + row;
         if (e < p.r) {
 #pragma unroll
-          for (int j = 0; j < NR; ++j)
-            if (hb * NR + j < p.R) p.part_o[(base + j) * p.r + e] = __uint_as_float(o[j]);
+          for (int j = 0; j < 8; ++j)
+            if (hb * NR + 8 * g + j < p.R) p.part_o[(base + j) * p.r + e] = __uint_as_float(o[j]);
         }
+        __syncwarp();
       }
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&aux->o_empty);
-      ptx::named_bar_sync(1, 128);       // red and m_s are free for the next sequence
       ++nseg;
     }
   } else if (kQuant) {
     // ------------------------------------------------------------- expansion of codes
-    const int tid = threadIdx.x - 192;   // 0..255
-    const __nv_bfloat16 one = __ushort_as_bfloat16((unsigned short)(247 << 7));   // 2^120
-    const __nv_bfloat162 up = __halves2bfloat162(one, one);
+    const int tid = threadIdx.x - (64 + NR * 16);   // 0..255
     int pos = 0;
     bool ok = true;
     while (ok && next_seg(&run, p, &sg)) {
@@ -526,44 +542,52 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
         const int valid = sg.len - (sg.t0 + i) * 128;      // token rows of this tile (may exceed 128)
         for (int c = 0; c < p.nch; ++c, ++pos) {
           const int slot = pos % p.nslot;
-          ok = ptx::named_bar_and(2, 256, wait_b(&aux->raw_full[slot], (pos / p.nslot) & 1, aux, p.err));
-          if (!ok) break;
+          if (!(ok = wait_w(&aux->raw_full[slot], (pos / p.nslot) & 1, aux, p.err))) break;
           uint8_t* dst = ring + slot * kSlot;
           const uint8_t* sc = sc_s + slot * kScaleBytes;
+          // 16 codes a thread and step: 8 (a last chunk of 64 ranks: 4) threads per token row
+          const bool full = c * 128 + 64 < p.r;
+          const int sh = full ? 3 : 2, steps = full ? 4 : 2;
+          const int col = tid & ((1 << sh) - 1), tok0 = tid >> sh, dtok = 256 >> sh;
           uint4 w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = reinterpret_cast<const uint4*>(dst + kSub)[k * 256 + tid];
-          ptx::named_bar_sync(2, 256);                     // every code is in registers
-          const int col = tid & 7;                         // 16 ranks: 16 col .. 16 col + 15
+          uint32_t eb[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int tok = k * 32 + (tid >> 3);
-            const uint32_t eb = sc[tok * 4 + (col >> 1)];
-            const __nv_bfloat16 s1 = __ushort_as_bfloat16((unsigned short)(eb == 255u ? 0x7FC0u : eb << 7));
-            const __nv_bfloat162 s2 = __halves2bfloat162(s1, s1);
-            uint2 o[4];
-            o[0] = expand4(w[k].x, up, s2);
-            o[1] = expand4(w[k].y, up, s2);
-            o[2] = expand4(w[k].z, up, s2);
-            o[3] = expand4(w[k].w, up, s2);
-            if (tok >= valid) {                            // rows behind the sequence, as above
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = make_uint2(0u, 0u);
+            eb[k] = 127u;
+            if (k < steps) {
+              w[k] = reinterpret_cast<const uint4*>(dst + kSub)[k * 256 + tid];
+              eb[k] = sc[(k * dtok + tok0) * 4 + (col >> 1)];
             }
-            // 128-byte swizzle: 16-byte column v of row tok sits at v ^ (tok % 8); the lanes of
-            // the second box take their two columns in the other order, so that the eight
-            // lanes of a row store to eight different columns
-            const uint32_t base = ptx::smem_u32(dst + (col >> 2) * kSub + tok * 128);
-            const int first = col >> 2;
+          }
+          // A whole chunk's codes of a token lie where its second box row goes, and a warp holds
+          // whole tokens: once its lanes have read, it may write.
+          __syncwarp();
+          // 128-byte swizzle: 16-byte column v of row tok sits at v ^ (tok % 8), and tok % 8 is
+          // the same in every step; the lanes of the second box take their two columns in the
+          // other order, so that the eight lanes of a row store to eight different columns
+          const bool swap = col >= 4;
+          const uint32_t base = ptx::smem_u32(dst + (col >> 2) * kSub + tok0 * 128);
+          const uint32_t a0 = base + ((((col & 3) * 2 + swap) ^ (tok0 & 7)) << 4);
+          const uint32_t a1 = base + ((((col & 3) * 2 + !swap) ^ (tok0 & 7)) << 4);
+          const bool two = __any_sync(0xffffffffu, max(max(eb[0], eb[1]), max(eb[2], eb[3])) > 134u);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int pick = h ^ first;
-              const uint32_t a = base + ((((col & 3) * 2 + pick) ^ (tok & 7)) << 4);
-              const uint2 lo = pick ? o[2] : o[0], hi = pick ? o[3] : o[1];
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(lo.x), "r"(lo.y), "r"(hi.x),
-                           "r"(hi.y)
-                           : "memory");
+          for (int k = 0; k < 4; ++k)
+            if (k < steps) {
+              const uint32_t off = k * dtok * 128;
+              uint4 x = w[k];
+              if (swap) x = make_uint4(w[k].z, w[k].w, w[k].x, w[k].y);
+              if (two) expand16<true>(x, eb[k], a0 + off, a1 + off);
+              else expand16<false>(x, eb[k], a0 + off, a1 + off);
             }
+          if (valid < 128) {                               // rows behind the sequence, as above
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < steps && k * dtok + tok0 >= valid) {
+                const uint32_t off = k * dtok * 128;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a0 + off), "r"(0) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a1 + off), "r"(0) : "memory");
+              }
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
@@ -706,7 +730,7 @@ struct OutArgs {
   float* lse;
   int* err;
 };
-constexpr int kOutThreads = 256;
+constexpr int kOutThreads = 512;
 constexpr int kMaxRuns = 160;          // slots one sequence can have: the CTA columns (<= SMs)
 struct OutAux {
   uint64_t w_full, done;
@@ -715,6 +739,7 @@ struct OutAux {
   int first[16], count[16], row[16];   // per row: first slot, slots, row of its sequence
   float inv[16];
   float w[16][kMaxRuns];
+  float4 part[kOutThreads];            // sums over subsets of a row's slots
 };
 
 __global__ void __launch_bounds__(kOutThreads)
@@ -788,29 +813,25 @@ __global__ void __launch_bounds__(kOutThreads)
   const size_t srow = (size_t)p.HB * p.NR;               // rows per slot
   for (int k = warp; k < nrow; k += kOutThreads / 32) {  // weights: a warp per row
     const int n = aux->count[k];
-    const float4* ml = reinterpret_cast<const float4*>(p.part_ml) + (size_t)aux->first[k] * srow + aux->row[k];
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + (size_t)aux->first[k] * srow + aux->row[k];
     float m = -INFINITY;
     for (int s = lane; s < n; s += 32) {
-      const float4 v = ml[s * srow];
+      const float2 v = ml[s * srow];
       if (v.y > 0.f || !(v.y == v.y)) m = fmaxf(m, v.x);  // a part that saw no token has no say
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, lr = 0.f;
+    float l = 0.f;
     for (int s = lane; s < n; s += 32) {
-      const float4 v = ml[s * srow];
+      const float2 v = ml[s * srow];
       const float w = v.y == 0.f ? 0.f : exp2f(v.x - m);
       aux->w[k][s] = w;
       l += w * v.y;
-      lr += w * v.z;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, o);
-      lr += __shfl_xor_sync(0xffffffffu, lr, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      aux->inv[k] = l == 0.f ? 0.f : 1.f / lr;
+      aux->inv[k] = l == 0.f ? 0.f : 1.f / l;
       if (p.lse) {
         const int bs = (m0 + k) / p.g;
         p.lse[(size_t)(bs / p.n_tok) * p.n_tok * p.Hq + aux->row[k]] =
@@ -819,51 +840,66 @@ __global__ void __launch_bounds__(kOutThreads)
     }
   }
   __syncthreads();
-  const int r4 = p.r >> 2;
-  for (int u = threadIdx.x; u < 16 * r4; u += kOutThreads) {
-    const int k = u / r4, e = (u % r4) * 4;
+  // A part of r/4 threads (4 ranks each) sums a row's slots; with fewer rows than parts, several
+  // parts share a row, each with every sub-th slot.  The rows of o_s past nrow stay as they are:
+  // they only reach accumulator columns that nobody reads.
+  const int r4 = p.r >> 2, parts = kOutThreads / r4;
+  const int part = (int)threadIdx.x / r4, e = ((int)threadIdx.x % r4) * 4;
+  const int subs = max(1, parts / nrow);
+  const int sub = subs > 1 ? part / nrow : 0;
+  for (int k0 = 0; k0 < nrow; k0 += parts) {
+    const int k = subs > 1 ? part % nrow : k0 + part;
+    const bool in = part < parts && k < nrow && sub < subs;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (k < nrow) {
+    if (in) {
       const int n = aux->count[k];
       const float* src = p.part_o + ((size_t)aux->first[k] * srow + aux->row[k]) * p.r + e;
       const float* w = aux->w[k];
-      int s = 0;
-      for (; s + 4 <= n; s += 4) {
-        float4 v[4];
+      const size_t step = srow * p.r;
+      for (int s = sub; s < n; s += 8 * subs) {
+        float4 v[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const float4*>(src + (s + q) * srow * p.r);
+        for (int q = 0; q < 8; ++q)
+          if (s + q * subs < n) v[q] = *reinterpret_cast<const float4*>(src + (s + q * subs) * step);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float f = w[s + q];
-          acc.x += f * v[q].x;
-          acc.y += f * v[q].y;
-          acc.z += f * v[q].z;
-          acc.w += f * v[q].w;
+        for (int q = 0; q < 8; ++q)
+          if (s + q * subs < n) {
+            const float f = w[s + q * subs];
+            acc.x += f * v[q].x;
+            acc.y += f * v[q].y;
+            acc.z += f * v[q].z;
+            acc.w += f * v[q].w;
+          }
+      }
+    }
+    if (subs > 1) {
+      aux->part[threadIdx.x] = acc;
+      __syncthreads();
+      if (in && sub == 0)
+        for (int q = 1; q < subs; ++q) {
+          const float4 v = aux->part[threadIdx.x + q * nrow * r4];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
         }
-      }
-      for (; s < n; ++s) {
-        const float4 v = *reinterpret_cast<const float4*>(src + s * srow * p.r);
-        const float f = w[s];
-        acc.x += f * v.x;
-        acc.y += f * v.y;
-        acc.z += f * v.z;
-        acc.w += f * v.w;
-      }
+    }
+    if (in && sub == 0) {
       const float inv = aux->inv[k];
       acc.x *= inv;
       acc.y *= inv;
       acc.z *= inv;
       acc.w *= inv;
+      const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x, acc.y), h1 = __floats2bfloat162_rn(acc.z, acc.w);
+      const __nv_bfloat162 l0 = __floats2bfloat162_rn(acc.x - __low2float(h0), acc.y - __high2float(h0));
+      const __nv_bfloat162 l1 = __floats2bfloat162_rn(acc.z - __low2float(h1), acc.w - __high2float(h1));
+      // K-major, 128-byte swizzle: row k (hi) and 16 + k (lo; 16 % 8 = 0, the same swizzle)
+      uint8_t* d = o_s + (e >> 6) * 4096 + k * 128 + ((((e & 63) >> 3) ^ (k & 7)) << 4) + (e & 4) * 2;
+      *reinterpret_cast<uint2*>(d) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+      *reinterpret_cast<uint2*>(d + 16 * 128) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&l0), *reinterpret_cast<const uint32_t*>(&l1));
     }
-    const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x, acc.y), h1 = __floats2bfloat162_rn(acc.z, acc.w);
-    const __nv_bfloat162 l0 = __floats2bfloat162_rn(acc.x - __low2float(h0), acc.y - __high2float(h0));
-    const __nv_bfloat162 l1 = __floats2bfloat162_rn(acc.z - __low2float(h1), acc.w - __high2float(h1));
-    // K-major, 128-byte swizzle: row k (hi) and 16 + k (lo; 16 % 8 = 0, the same swizzle)
-    uint8_t* d = o_s + (e >> 6) * 4096 + k * 128 + ((((e & 63) >> 3) ^ (k & 7)) << 4) + (e & 4) * 2;
-    *reinterpret_cast<uint2*>(d) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-    *reinterpret_cast<uint2*>(d + 16 * 128) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&l0), *reinterpret_cast<const uint32_t*>(&l1));
   }
   ptx::fence_proxy_async_smem();
   __syncthreads();
@@ -932,12 +968,12 @@ bool map2d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, uint64_t d
 }
 
 template <int NR, bool kQuant>
-cudaError_t launch_dec(const CUtensorMap* tm, const DecArgs& a, size_t smem, cudaStream_t s) {
+cudaError_t launch_dec(const lr_shared* c, const CUtensorMap& tqr, const DecArgs& a, size_t smem, cudaStream_t s) {
   static std::atomic<uint32_t> optin{0};
   cudaError_t e = smem_optin(k_shared_decode<NR, kQuant>, optin);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_shared_decode<NR, kQuant>, dim3(a.X, a.HB), dim3(kQuant ? 448 : 192), smem, s, tm[0], tm[1],
-                    tm[2], tm[3], a);
+  return launch_pdl(k_shared_decode<NR, kQuant>, dim3(a.X, a.HB), dim3(dec_threads<NR, kQuant>()), smem, s,
+                    c->tm_qt[NR / 32], tqr, c->tm_c, c->tm_kr, a);
 }
 
 }  // namespace
@@ -960,6 +996,23 @@ void shared_part_rows(const lr_shared_desc* d, int num_sms, size_t* rows) {
   }
 }
 
+cudaError_t shared_decode_maps(lr_shared* c) {
+  const lr_shared_desc& d = c->desc;
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t r = d.rank, rows = (uint64_t)c->n_pages * 128;
+  const uint64_t wk = (uint64_t)d.n_kv_heads * d.dim_nope, wv = (uint64_t)d.n_kv_heads * d.dim_v;
+  const uint64_t qrows = shared_qt_bytes(&d) / (r * 2);
+  bool ok = map2d(&c->tm_w, bf, c->B, wk, r, (wk + wv) * 2, 64, 128) &&
+            map2d(&c->tm_v, bf, static_cast<const __nv_bfloat16*>(c->B) + wk, wv, r, (wk + wv) * 2, 64, 64) &&
+            map2d(&c->tm_kr, bf, c->kr, d.dim_rope, rows, (uint64_t)d.dim_rope * 2, 64, 128) &&
+            map2d(&c->tm_qt[0], bf, c->qt, r, qrows, r * 2, 64, 32) &&
+            map2d(&c->tm_qt[1], bf, c->qt, r, qrows, r * 2, 64, 64);
+  // (8 bits: the codes are copied without a map; any valid one stands in)
+  if (ok && d.quant_bits) c->tm_c = c->tm_kr;
+  else if (ok) ok = map2d(&c->tm_c, bf, c->c, r, rows, r * 2, 64, 128);
+  return ok ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, const int32_t* row_len, void* out,
                                  float* lse, cudaStream_t s) {
   const lr_shared_desc& d = c->desc;
@@ -968,7 +1021,6 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   const int g = d.n_q_heads / d.n_kv_heads, r = d.rank, dq = d.dim_nope + d.dim_rope;
   const int BS = d.batch * n_tokens;
   const bool quant = d.quant_bits != 0;
-  const uint64_t rows = (uint64_t)c->n_pages * 128;
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
   // query projection
@@ -986,9 +1038,7 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   qp.ncols = (qp.nb * g + 15) / 16 * 16;
   qp.qt = static_cast<__nv_bfloat16*>(c->qt);
   qp.err = c->dev_err;
-  CUtensorMap tw, tq;
-  const uint64_t wk = (uint64_t)d.n_kv_heads * d.dim_nope, wv = (uint64_t)d.n_kv_heads * d.dim_v;
-  if (!map2d(&tw, bf, c->B, wk, r, (wk + wv) * 2, 64, 128)) return cudaErrorInvalidValue;
+  CUtensorMap tq, tqr;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)dq, (cuuint64_t)d.n_q_heads, (cuuint64_t)BS};
     const cuuint64_t st[2] = {(cuuint64_t)dq * 2, (cuuint64_t)d.n_q_heads * dq * 2};
@@ -1000,7 +1050,7 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   if (e != cudaSuccess) return e;
   const size_t smem_q = (size_t)(d.dim_nope / 64) * (kSub + qp.ncols * 128) + sizeof(QpAux);
   e = launch_pdl(k_shared_qproj, dim3((r + 127) / 128, d.n_kv_heads, (BS + qp.nb - 1) / qp.nb), dim3(128), smem_q, s,
-                 tw, tq, qp);
+                 c->tm_w, tq, qp);
   if (e != cudaSuccess) return e;
 
   // attention over the stored rows
@@ -1018,6 +1068,7 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   a.HB = HB;
   a.X = X;
   a.scale_log2 = c->scale_log2;
+  a.codes = static_cast<const uint8_t*>(c->c);
   a.scale = c->scale;
   a.part_o = c->part_o;
   a.part_ml = c->part_ml;
@@ -1025,31 +1076,18 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   a.nslot = 0;
   while (a.nslot < kMaxSlots && decode_smem(r, NR, a.nslot + 1, quant) <= (size_t)kSmemLimit) ++a.nslot;
   if (a.nslot < a.nch) return cudaErrorNotSupported;     // a tile's latents stay until its value mix
-  CUtensorMap tm[4];
-  if (!map2d(&tm[0], bf, c->qt, r, (uint64_t)d.batch * HB * 2 * NR, (uint64_t)r * 2, 64, 2 * NR))
-    return cudaErrorInvalidValue;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)d.dim_rope, (cuuint64_t)R, (cuuint64_t)d.batch};
     const cuuint64_t st[2] = {(cuuint64_t)dq * 2, (cuuint64_t)R * dq * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)NR, 1};
-    if (!tc::make_map(&tm[1], bf, static_cast<const __nv_bfloat16*>(q) + d.dim_nope, 3, dims, st, box))
+    if (!tc::make_map(&tqr, bf, static_cast<const __nv_bfloat16*>(q) + d.dim_nope, 3, dims, st, box))
       return cudaErrorInvalidValue;
   }
-  if (quant) {
-    // plain rows of 128 codes (no swizzle: the expansion warps read them)
-    const cuuint64_t dims[2] = {(cuuint64_t)r, (cuuint64_t)rows}, st[1] = {(cuuint64_t)r};
-    const cuuint32_t box[2] = {128, 128};
-    if (!tc::make_map(&tm[2], CU_TENSOR_MAP_DATA_TYPE_UINT8, c->c, 2, dims, st, box, CU_TENSOR_MAP_SWIZZLE_NONE))
-      return cudaErrorInvalidValue;
-  } else if (!map2d(&tm[2], bf, c->c, r, rows, (uint64_t)r * 2, 64, 128)) {
-    return cudaErrorInvalidValue;
-  }
-  if (!map2d(&tm[3], bf, c->kr, d.dim_rope, rows, (uint64_t)d.dim_rope * 2, 64, 128)) return cudaErrorInvalidValue;
   const size_t smem = decode_smem(r, NR, a.nslot, quant);
   if (NR == 16)
-    e = quant ? launch_dec<16, true>(tm, a, smem, s) : launch_dec<16, false>(tm, a, smem, s);
+    e = quant ? launch_dec<16, true>(c, tqr, a, smem, s) : launch_dec<16, false>(c, tqr, a, smem, s);
   else
-    e = quant ? launch_dec<32, true>(tm, a, smem, s) : launch_dec<32, false>(tm, a, smem, s);
+    e = quant ? launch_dec<32, true>(c, tqr, a, smem, s) : launch_dec<32, false>(c, tqr, a, smem, s);
   if (e != cudaSuccess) return e;
 
   // join and output projection
@@ -1062,9 +1100,9 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   o.dv = d.dim_v;
   o.g = g;
   o.rows = BS * g;
-  // few rows a block while the grid does not fill the SMs; each block reads B_v,h once more
+  // the fewest rows a block whose grid still is one wave (each block reads B_v,h once more)
   o.RB = 16;
-  while (o.RB > 2 && (o.rows + o.RB - 1) / o.RB * d.n_kv_heads < c->num_sms) o.RB /= 2;
+  while (o.RB > 1 && (o.rows + o.RB / 2 - 1) / (o.RB / 2) * d.n_kv_heads <= c->num_sms) o.RB /= 2;
   o.n_tok = n_tokens;
   o.Hq = d.n_q_heads;
   o.HB = HB;
@@ -1075,11 +1113,9 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   o.out = static_cast<__nv_bfloat16*>(out);
   o.lse = lse;
   o.err = c->dev_err;
-  CUtensorMap tv;
-  if (!map2d(&tv, bf, static_cast<const __nv_bfloat16*>(c->B) + wk, wv, r, (wk + wv) * 2, 64, 64))
-    return cudaErrorInvalidValue;
   e = smem_optin(k_shared_out, optin_o);
   if (e != cudaSuccess) return e;
   const size_t smem_o = (size_t)(r / 64) * 4096 + (size_t)2 * r * 128 + sizeof(OutAux);
-  return launch_pdl(k_shared_out, dim3((o.rows + o.RB - 1) / o.RB, d.n_kv_heads), dim3(kOutThreads), smem_o, s, tv, o);
+  return launch_pdl(k_shared_out, dim3((o.rows + o.RB - 1) / o.RB, d.n_kv_heads), dim3(kOutThreads), smem_o, s, c->tm_v,
+                    o);
 }

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
           const int idx = k * 256 + tid, tok = (idx >> 2) & 127, s = s0 + (idx >> 9), col = idx & 3;
           if ((idx >> 9) < ns) {
             const long long row = row0 + tok;
-            cd[k] = __ldg(reinterpret_cast<const uint4*>(p.codes + row * p.r + s * 64) + col);
+            cd[k] = __ldg(reinterpret_cast<const uint4*>(p.codes + shared_code_index(row, p.r, s * 64 + col * 16)));
             eb[k] = __ldg(p.scale + shared_scale_index(row, p.r, s * 2 + (col >> 1)));
           }
         }
@@ -362,6 +362,12 @@ bool map2d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint32_t b
 
 }  // namespace
 
+cudaError_t shared_expand_maps(lr_shared* c) {
+  const lr_shared_desc& d = c->desc;
+  const uint64_t W = (uint64_t)d.n_kv_heads * (d.dim_nope + d.dim_v);
+  return map2d(&c->tm_bt, c->Bt, d.rank, W, 64, 128) ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t* start, int total, void* k, void* v,
                                  void* kr, cudaStream_t s) {
   const lr_shared_desc& d = c->desc;
@@ -382,11 +388,7 @@ cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t*
   a.k = static_cast<__nv_bfloat16*>(k);
   a.v = static_cast<__nv_bfloat16*>(v);
   a.err = c->dev_err;
-  CUtensorMap tlat, tw;
-  if (!map2d(&tw, c->Bt, a.r, a.W, 64, 128)) return cudaErrorInvalidValue;
   const bool quant = d.quant_bits != 0;
-  if (quant) tlat = tw;                  // not used: the codes are read by the expansion warps
-  else if (!map2d(&tlat, c->c, a.r, (uint64_t)c->n_pages * 128, 64, 128)) return cudaErrorInvalidValue;
   // One run per SM, no more runs than units there can be, and no run longer than its tile table
   // holds (beyond 60 tiles an SM, over a million tokens, the runs queue up).
   const long long tiles = (long long)total / 128 + 2 * std::min<long long>(d.batch, total);
@@ -398,6 +400,6 @@ cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t*
   if (e != cudaSuccess) return e;
   e = launch_shared_read(c, cu, start, total, nullptr, kr, s);   // the rotary keys
   if (e != cudaSuccess) return e;
-  return quant ? launch_pdl(k_shared_expand<true>, dim3((unsigned)grid), dim3(448), smem, s, tlat, tw, a)
-               : launch_pdl(k_shared_expand<false>, dim3((unsigned)grid), dim3(192), smem, s, tlat, tw, a);
+  return quant ? launch_pdl(k_shared_expand<true>, dim3((unsigned)grid), dim3(448), smem, s, c->tm_c, c->tm_bt, a)
+               : launch_pdl(k_shared_expand<false>, dim3((unsigned)grid), dim3(192), smem, s, c->tm_c, c->tm_bt, a);
 }

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_append(const AppendArgs 
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
         o[h] = lo | (hi << 16);
       }
-      reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.c) + row * a.r)[v] = make_uint2(o[0], o[1]);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.c) + shared_code_index(row, a.r, v * 8)) = make_uint2(o[0], o[1]);
       if ((lane & 3) == 0) a.scale[shared_scale_index(row, a.r, v >> 2)] = (uint8_t)eb;
     }
   }
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_read(const ReadArgs a) {
       dst[v] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.c) + row * a.r) + v);
       continue;
     }
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.c) + row * a.r) + v);
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.c) + shared_code_index(row, a.r, v * 8)));
     const float sc = shared_pow2(__ldg(a.scale + shared_scale_index(row, a.r, v >> 2)));
     uint32_t o[4];
 #pragma unroll

@@ -107,7 +107,7 @@ lr_status lr_shared_create(const lr_shared_desc* desc, const void* B_k, const vo
   size_t prows = 0;
   shared_part_rows(&d, c->num_sms, &prows);
   if (e == cudaSuccess) e = dalloc(&c->part_o, prows * r * sizeof(float), false);
-  if (e == cudaSuccess) e = dalloc(&c->part_ml, prows * 4 * sizeof(float), false);
+  if (e == cudaSuccess) e = dalloc(&c->part_ml, prows * 2 * sizeof(float), false);
   if (e == cudaSuccess) e = dalloc(&c->dev_err, sizeof(int), true);
   if (e == cudaSuccess) {
     // span j of sequence b in page (b * pps + j) % n_pages until a table is set
@@ -123,6 +123,8 @@ lr_status lr_shared_create(const lr_shared_desc* desc, const void* B_k, const vo
   if (e == cudaSuccess) e = cudaMemcpy2DAsync(c->B, wk + wv, B_k, wk, wk, r, cudaMemcpyDeviceToDevice, s);
   if (e == cudaSuccess)
     e = cudaMemcpy2DAsync(static_cast<char*>(c->B) + wk, wk + wv, B_v, wv, wv, r, cudaMemcpyDeviceToDevice, s);
+  if (e == cudaSuccess) e = shared_decode_maps(c);
+  if (e == cudaSuccess) e = shared_expand_maps(c);
   if (e == cudaSuccess) e = launch_shared_transpose(c, s);
   if (e == cudaSuccess && c->rope_cs) e = launch_shared_rope_table(c, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);

@@ -4,6 +4,8 @@
 
 #include "lr_internal.cuh"
 
+#include <cuda.h>
+
 // Rows of the stored arrays are page * 128 + token % 128, page = table[b][token / 128].
 struct lr_shared {
   lr_shared_desc desc;
@@ -16,6 +18,7 @@ struct lr_shared {
   std::vector<int32_t> host_table;
 
   void* c = nullptr;          // [rows][r] bf16, or e4m3 codes
+                              // (8 bits: shared_code_index)
   uint8_t* scale = nullptr;   // 8 bits: [n_pages][ceil(r/128)][128][4] exponent bytes (shared_scale_index)
   void* kr = nullptr;         // [rows][dr] bf16
   int32_t* table = nullptr;   // [B][pps]
@@ -24,8 +27,14 @@ struct lr_shared {
   float2* rope_cs = nullptr;  // [capacity][dr/2] (cos, sin), or null
   void* qt = nullptr;         // decode: query latents, hi and lo halves (k_shared_decode.cu)
   float* part_o = nullptr;    // decode: split partials [slots][rows][r]
-  float* part_ml = nullptr;   // decode: [slots][rows][4] = m, l, l of the rounded weights, 0
+  float* part_ml = nullptr;   // decode: [slots][rows][2] = m (log2), l
   int* dev_err = nullptr;
+
+  // tensor maps of the cache's own storage, made once
+  CUtensorMap tm_c, tm_kr;    // latents (bf16 caches) and rotary keys by stored row
+  CUtensorMap tm_w, tm_v;     // B_k: 128 ranks x 64 columns; B_v: 64 ranks x 64 columns
+  CUtensorMap tm_bt;          // Bt: 128 columns x 64 ranks
+  CUtensorMap tm_qt[2];       // query latents, hi | lo blocks of 2 x 16 and 2 x 32 rows
 };
 
 inline RowMap row_map(const lr_shared* c) {
@@ -35,6 +44,15 @@ inline RowMap row_map(const lr_shared* c) {
   m.pps = c->pps;
   m.n_pages = c->n_pages;
   return m;
+}
+
+// The code of rank i of a stored row: a page holds its 128-rank chunks one after another, each
+// [128 tokens][128 codes] (a last chunk of 64 ranks: [128][64]), so that a tile's chunk is one
+// contiguous copy of 16 (8) KB.  (Boxes of 128 bytes from 512-byte rows took 1.0 us each with
+// four in flight, 16 GB/s an SM.)
+__host__ __device__ __forceinline__ long long shared_code_index(long long row, int r, int i) {
+  const int c = i >> 7, left = r - (c << 7), w = left < 128 ? left : 128;
+  return (row >> 7) * (128ll * r) + ((long long)c << 14) + (row & 127) * w + (i & 127);
 }
 
 // The exponent byte (2^(byte - 127); 255: a group that held a NaN or an infinity) of ranks
@@ -122,6 +140,9 @@ cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t*
 cudaError_t launch_shared_attn(lr_shared* c, const void* q, const void* k, const void* kr, const void* v,
                                const int32_t* cu_q, const int32_t* cu_k, int nseq, int total_q, int total_k,
                                int causal, void* out, float* lse, cudaStream_t s);
+// tensor maps of the cache's storage (host only)
+cudaError_t shared_decode_maps(lr_shared* c);
+cudaError_t shared_expand_maps(lr_shared* c);
 // Scratch of the decode, in bytes, for any n_tokens up to max_queries.
 size_t shared_qt_bytes(const lr_shared_desc* d);
 void shared_part_rows(const lr_shared_desc* d, int num_sms, size_t* rows);
