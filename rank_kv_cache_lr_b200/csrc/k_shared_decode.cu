@@ -22,38 +22,14 @@
 // (tile_run), one run per CTA column, so ragged batches stay balanced and a captured graph
 // serves any lengths.  A run's part of one sequence is one partial (m, l, o~), joined by
 // k_shared_out.
-#include "shared_internal.cuh"
-#include "tc_common.cuh"
+#include "shared_decode.cuh"
 
 #include <algorithm>
 
 namespace {
 
-using tc::drain_wait;
-using tc::kLazy;
-using tc::kSmemLimit;
-
-constexpr int kSub = 128 * 128;        // 128 tokens x 64 ranks x 2 B (one TMA box)
-constexpr int kSlot = 2 * kSub;        // 128 tokens x 128 ranks
-constexpr int kScaleBytes = 512;       // 8 bits: exponent bytes of 128 tokens x 4 groups
-constexpr int kAuxBytes = 2048;
-constexpr int kMaxSlots = 6;
 constexpr int kSCol = 0;               // TMEM: S of tile t in columns [64 (t % 2), + 2 NR)
 constexpr int kOCol = 128;             // TMEM: O~ of 128-rank chunk c in columns [128 + c NR, + NR)
-constexpr float kNoMax = -1e30f;       // running max before any visible token (finite: no inf - inf)
-
-struct DecArgs {
-  unsigned long long wait_ns;
-  const int32_t* row_len;
-  RowMap map;
-  int B, cap, r, nch, Hq, n_tok, R, HB, X, nslot;
-  float scale_log2;
-  const uint8_t* codes;
-  const uint8_t* scale;
-  float* part_o;
-  float* part_ml;
-  int* err;
-};
 
 // Barriers (arrival count; who arrives -> who waits); phase k is waited with parity k & 1.
 //   raw_full[s]     1 + tx   8 bits: producer's codes and scales -> expansion warps
@@ -87,96 +63,6 @@ __device__ __forceinline__ bool wait_b(uint64_t* bar, uint32_t parity, Aux* aux,
 __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, Aux* aux, int* err) {
   return __all_sync(0xffffffffu, wait_b(bar, parity, aux, err));
 }
-
-// The next sequence part of a run: false at its end.  Every role walks its own copy.
-struct Seg {
-  int b, t0, nt, len;
-};
-__device__ __forceinline__ bool next_seg(TileRun* run, const DecArgs& p, Seg* s) {
-  while (run->left > 0 && run->b < p.B) {
-    const int len = shared_len(p.row_len, run->b, p.cap);
-    const int nt = ((len + 127) >> 7) - run->tile;
-    if (nt <= 0) {
-      ++run->b;
-      run->tile = 0;
-      continue;
-    }
-    s->b = run->b;
-    s->t0 = run->tile;
-    s->nt = min(nt, run->left);
-    s->len = len;
-    run->left -= s->nt;
-    ++run->b;
-    run->tile = 0;
-    return true;
-  }
-  return false;
-}
-
-// Butterfly reduction of 8 columns over a warp: lane l holds op over all lanes of v[l % 8].
-template <bool kMax>
-__device__ __forceinline__ float reduce_cols(float (&v)[8], int lane) {
-#pragma unroll
-  for (int w = 4; w >= 1; w >>= 1) {
-    const bool up = (lane & w) != 0;
-#pragma unroll
-    for (int k = 0; k < w; ++k) {
-      const float keep = up ? v[k + w] : v[k];
-      const float send = up ? v[k] : v[k + w];
-      const float got = __shfl_xor_sync(0xffffffffu, send, w);
-      v[k] = kMax ? fmaxf(keep, got) : keep + got;
-    }
-  }
-  float r = v[0];
-#pragma unroll
-  for (int o = 8; o <= 16; o <<= 1) {
-    const float got = __shfl_xor_sync(0xffffffffu, r, o);
-    r = kMax ? fmaxf(r, got) : r + got;
-  }
-  return r;
-}
-
-// Two e4m3 codes as bf16 before their scale: a code's sign, exponent and mantissa bits placed in
-// a bf16 stand for its value times 2^-120 (subnormals included).  sel picks bytes (i, j) as
-// halves with the sign replicated above each (selector bit 3).
-template <uint32_t kSel>
-__device__ __forceinline__ __nv_bfloat162 place2(uint32_t w) {
-  uint32_t a;
-  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(a) : "r"(w), "n"(kSel));
-  a = (a << 4) & 0x87F087F0u;
-  return *reinterpret_cast<const __nv_bfloat162*>(&a);
-}
-// Sixteen codes of one token (their words in the order in which they are stored), times 2^e, to
-// two 16-byte columns of a swizzled row: w.x, w.y to address a0 and w.z, w.w to a1.  e <= 7
-// (exponent byte at most 134): 2^(120 + e) is a bf16, so one exact product; kTwo: two products.
-template <bool kTwo>
-__device__ __forceinline__ void expand16(const uint4& w, uint32_t eb, uint32_t a0, uint32_t a1) {
-  // 2^e = 2^(b1 - 127) 2^(b2 - 127) with 120 folded into the first; byte 255 (a group that held a
-  // NaN or an infinity) is NaN
-  const uint32_t b1 = kTwo ? min(eb + 120u, 254u) : eb + 120u;
-  const uint32_t h1 = kTwo && eb == 255u ? 0x7FC07FC0u : b1 * 0x00800080u;
-  const uint32_t h2 = (eb + 247u - b1) * 0x00800080u;
-  const __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162*>(&h1);
-  const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&h2);
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    __nv_bfloat162 x = __hmul2(place2<0x9180>(in[k]), s1), y = __hmul2(place2<0xB3A2>(in[k]), s1);
-    if (kTwo) {
-      x = __hmul2(x, s2);
-      y = __hmul2(y, s2);
-    }
-    o[2 * k] = *reinterpret_cast<const uint32_t*>(&x);
-    o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&y);
-  }
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-               : "memory");
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-               : "memory");
-}
-// A warp-uniform value, known as such to the compiler.
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Shared memory: [aux][q~: r/64 blocks of (2 NR rows hi | lo) x 128 B][q_rope: NR rows x 128 B]
 // [P: 128 tokens x NR][slots][rotary tile][8 bits: scales per slot].
@@ -545,50 +431,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
           if (!(ok = wait_w(&aux->raw_full[slot], (pos / p.nslot) & 1, aux, p.err))) break;
           uint8_t* dst = ring + slot * kSlot;
           const uint8_t* sc = sc_s + slot * kScaleBytes;
-          // 16 codes a thread and step: 8 (a last chunk of 64 ranks: 4) threads per token row
-          const bool full = c * 128 + 64 < p.r;
-          const int sh = full ? 3 : 2, steps = full ? 4 : 2;
-          const int col = tid & ((1 << sh) - 1), tok0 = tid >> sh, dtok = 256 >> sh;
-          uint4 w[4];
-          uint32_t eb[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            eb[k] = 127u;
-            if (k < steps) {
-              w[k] = reinterpret_cast<const uint4*>(dst + kSub)[k * 256 + tid];
-              eb[k] = sc[(k * dtok + tok0) * 4 + (col >> 1)];
-            }
-          }
-          // A whole chunk's codes of a token lie where its second box row goes, and a warp holds
-          // whole tokens: once its lanes have read, it may write.
-          __syncwarp();
-          // 128-byte swizzle: 16-byte column v of row tok sits at v ^ (tok % 8), and tok % 8 is
-          // the same in every step; the lanes of the second box take their two columns in the
-          // other order, so that the eight lanes of a row store to eight different columns
-          const bool swap = col >= 4;
-          const uint32_t base = ptx::smem_u32(dst + (col >> 2) * kSub + tok0 * 128);
-          const uint32_t a0 = base + ((((col & 3) * 2 + swap) ^ (tok0 & 7)) << 4);
-          const uint32_t a1 = base + ((((col & 3) * 2 + !swap) ^ (tok0 & 7)) << 4);
-          const bool two = __any_sync(0xffffffffu, max(max(eb[0], eb[1]), max(eb[2], eb[3])) > 134u);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps) {
-              const uint32_t off = k * dtok * 128;
-              uint4 x = w[k];
-              if (swap) x = make_uint4(w[k].z, w[k].w, w[k].x, w[k].y);
-              if (two) expand16<true>(x, eb[k], a0 + off, a1 + off);
-              else expand16<false>(x, eb[k], a0 + off, a1 + off);
-            }
-          if (valid < 128) {                               // rows behind the sequence, as above
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < steps && k * dtok + tok0 >= valid) {
-                const uint32_t off = k * dtok * 128;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a0 + off), "r"(0) : "memory");
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a1 + off), "r"(0) : "memory");
-              }
-          }
+          expand_chunk(dst, sc, tid, c * 128 + 64 < p.r, valid);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&aux->slot_full[slot]);
@@ -951,8 +794,20 @@ __global__ void __launch_bounds__(kOutThreads)
 // host side
 // ---------------------------------------------------------------------------
 
-// Query rows per block: 16 when a sequence has no more, else 32.
-int rows_per_block(int R) { return R <= 16 ? 16 : 32; }
+// How R query rows per sequence are cut: NR per block, HB blocks, X runs of tiles.  A block of
+// 16 rows when a sequence has no more, else 32; pairs of CTAs (r > 256) also have blocks of 64.
+struct Cut {
+  int NR, HB, X;
+};
+Cut cut_of(const lr_shared_desc& d, int n_tokens, int num_sms) {
+  const int R = n_tokens * d.n_q_heads;
+  const bool pair = d.rank > 256;
+  Cut c;
+  c.NR = R <= 16 ? 16 : (pair && R > 32 ? 64 : 32);
+  c.HB = (R + c.NR - 1) / c.NR;
+  c.X = std::max(1, std::min(num_sms, kMaxRuns) / (pair ? 2 : 1) / c.HB);
+  return c;
+}
 
 size_t decode_smem(int r, int NR, int nslot, bool quant) {
   const size_t head = (size_t)(r / 64) * 2 * NR * 128 + (size_t)NR * 128 + 128 * NR * 2;
@@ -981,8 +836,8 @@ cudaError_t launch_dec(const lr_shared* c, const CUtensorMap& tqr, const DecArgs
 size_t shared_qt_bytes(const lr_shared_desc* d) {
   size_t most = 0;
   for (int n = 1; n <= d->max_queries; ++n) {
-    const int R = n * d->n_q_heads, NR = rows_per_block(R);
-    most = std::max(most, (size_t)((R + NR - 1) / NR) * 2 * NR);
+    const Cut c = cut_of(*d, n, 148);
+    most = std::max(most, (size_t)c.HB * 2 * c.NR);
   }
   return most * d->batch * d->rank * 2;
 }
@@ -990,9 +845,8 @@ size_t shared_qt_bytes(const lr_shared_desc* d) {
 void shared_part_rows(const lr_shared_desc* d, int num_sms, size_t* rows) {
   *rows = 0;
   for (int n = 1; n <= d->max_queries; ++n) {
-    const int R = n * d->n_q_heads, NR = rows_per_block(R), HB = (R + NR - 1) / NR;
-    const int X = std::max(1, std::min(num_sms, kMaxRuns) / HB);
-    *rows = std::max(*rows, (size_t)(X + d->batch) * HB * NR);
+    const Cut c = cut_of(*d, n, num_sms);
+    *rows = std::max(*rows, (size_t)(c.X + d->batch) * c.HB * c.NR);
   }
 }
 
@@ -1006,7 +860,8 @@ cudaError_t shared_decode_maps(lr_shared* c) {
             map2d(&c->tm_v, bf, static_cast<const __nv_bfloat16*>(c->B) + wk, wv, r, (wk + wv) * 2, 64, 64) &&
             map2d(&c->tm_kr, bf, c->kr, d.dim_rope, rows, (uint64_t)d.dim_rope * 2, 64, 128) &&
             map2d(&c->tm_qt[0], bf, c->qt, r, qrows, r * 2, 64, 32) &&
-            map2d(&c->tm_qt[1], bf, c->qt, r, qrows, r * 2, 64, 64);
+            map2d(&c->tm_qt[1], bf, c->qt, r, qrows, r * 2, 64, 64) &&
+            map2d(&c->tm_qt[2], bf, c->qt, r, qrows, r * 2, 64, 128);
   // (8 bits: the codes are copied without a map; any valid one stands in)
   if (ok && d.quant_bits) c->tm_c = c->tm_kr;
   else if (ok) ok = map2d(&c->tm_c, bf, c->c, r, rows, r * 2, 64, 128);
@@ -1016,8 +871,8 @@ cudaError_t shared_decode_maps(lr_shared* c) {
 cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, const int32_t* row_len, void* out,
                                  float* lse, cudaStream_t s) {
   const lr_shared_desc& d = c->desc;
-  const int R = n_tokens * d.n_q_heads, NR = rows_per_block(R), HB = (R + NR - 1) / NR;
-  const int X = std::max(1, std::min(c->num_sms, kMaxRuns) / HB);
+  const Cut cut = cut_of(d, n_tokens, c->num_sms);
+  const int R = n_tokens * d.n_q_heads, NR = cut.NR, HB = cut.HB, X = cut.X;
   const int g = d.n_q_heads / d.n_kv_heads, r = d.rank, dq = d.dim_nope + d.dim_rope;
   const int BS = d.batch * n_tokens;
   const bool quant = d.quant_bits != 0;
@@ -1054,28 +909,6 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   if (e != cudaSuccess) return e;
 
   // attention over the stored rows
-  DecArgs a;
-  a.wait_ns = c->wait_ns;
-  a.row_len = row_len;
-  a.map = row_map(c);
-  a.B = d.batch;
-  a.cap = d.capacity;
-  a.r = r;
-  a.nch = (r + 127) / 128;
-  a.Hq = d.n_q_heads;
-  a.n_tok = n_tokens;
-  a.R = R;
-  a.HB = HB;
-  a.X = X;
-  a.scale_log2 = c->scale_log2;
-  a.codes = static_cast<const uint8_t*>(c->c);
-  a.scale = c->scale;
-  a.part_o = c->part_o;
-  a.part_ml = c->part_ml;
-  a.err = c->dev_err;
-  a.nslot = 0;
-  while (a.nslot < kMaxSlots && decode_smem(r, NR, a.nslot + 1, quant) <= (size_t)kSmemLimit) ++a.nslot;
-  if (a.nslot < a.nch) return cudaErrorNotSupported;     // a tile's latents stay until its value mix
   {
     const cuuint64_t dims[3] = {(cuuint64_t)d.dim_rope, (cuuint64_t)R, (cuuint64_t)d.batch};
     const cuuint64_t st[2] = {(cuuint64_t)dq * 2, (cuuint64_t)R * dq * 2};
@@ -1083,11 +916,17 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
     if (!tc::make_map(&tqr, bf, static_cast<const __nv_bfloat16*>(q) + d.dim_nope, 3, dims, st, box))
       return cudaErrorInvalidValue;
   }
-  const size_t smem = decode_smem(r, NR, a.nslot, quant);
-  if (NR == 16)
-    e = quant ? launch_dec<16, true>(c, tqr, a, smem, s) : launch_dec<16, false>(c, tqr, a, smem, s);
-  else
-    e = quant ? launch_dec<32, true>(c, tqr, a, smem, s) : launch_dec<32, false>(c, tqr, a, smem, s);
+  if (r > 256) {
+    e = launch_shared_pair(c, tqr, row_len, n_tokens, R, NR, HB, X, s);
+  } else {
+    DecArgs a = dec_args(c, row_len, n_tokens, R, HB, X);
+    while (a.nslot < kMaxSlots && decode_smem(r, NR, a.nslot + 1, quant) <= (size_t)kSmemLimit) ++a.nslot;
+    const size_t smem = decode_smem(r, NR, a.nslot, quant);
+    if (NR == 16)
+      e = quant ? launch_dec<16, true>(c, tqr, a, smem, s) : launch_dec<16, false>(c, tqr, a, smem, s);
+    else
+      e = quant ? launch_dec<32, true>(c, tqr, a, smem, s) : launch_dec<32, false>(c, tqr, a, smem, s);
+  }
   if (e != cudaSuccess) return e;
 
   // join and output projection

@@ -234,7 +234,8 @@ LENS = [0, 1, 2, 127, 128, 129, 300, 517]
 @pytest.mark.parametrize("bits", [0, 8])
 @pytest.mark.parametrize("hq,hkv,r,dn,dr,dv,new", [
     (4, 4, 128, 128, 64, 128, 1), (28, 4, 256, 128, 64, 128, 1), (28, 28, 512, 128, 64, 128, 1),
-    (16, 1, 64, 64, 32, 64, 1), (5, 5, 192, 128, 32, 64, 3), (40, 8, 448, 64, 64, 128, 2), (1, 1, 320, 64, 32, 128, 8)])
+    (16, 1, 64, 64, 32, 64, 1), (5, 5, 192, 128, 32, 64, 3), (40, 8, 448, 64, 64, 128, 2), (1, 1, 320, 64, 32, 128, 8),
+    (17, 17, 384, 64, 64, 64, 1), (64, 16, 320, 64, 64, 64, 2)])
 def test_decode_matches_the_oracle(lib, bits, hq, hkv, r, dn, dr, dv, new):
     m = Layer(lib, LENS, hq=hq, hkv=hkv, r=r, dn=dn, dr=dr, dv=dv, bits=bits, new=new)
     q = m.query(new)
@@ -242,14 +243,16 @@ def test_decode_matches_the_oracle(lib, bits, hq, hkv, r, dn, dr, dv, new):
 
 
 @pytest.mark.parametrize("bits", [0, 8])
-def test_decode_many_heads_and_uneven_lengths(lib, bits):
-    m = Layer(lib, [1500, 3, 0, 900], hq=128, hkv=128, r=128, bits=bits, new=2, dn=64, dv=64)
+@pytest.mark.parametrize("r", [128, 512])
+def test_decode_many_heads_and_uneven_lengths(lib, bits, r):
+    m = Layer(lib, [1500, 3, 0, 900], hq=128, hkv=128, r=r, bits=bits, new=2, dn=64, dv=64)
     q = m.query(2)
     m.check_decode(q, *m.decode(q))
 
 
-def test_decode_long_context_over_many_splits(lib):
-    m = Layer(lib, [20000, 5], hq=6, hkv=3, r=128, bits=8)
+@pytest.mark.parametrize("r,bits", [(128, 8), (448, 8), (512, 0)])
+def test_decode_long_context_over_many_splits(lib, r, bits):
+    m = Layer(lib, [20000, 5], hq=6, hkv=3, r=r, bits=bits)
     q = m.query(1)
     m.check_decode(q, *m.decode(q))
 
@@ -262,8 +265,9 @@ def test_decode_of_rotated_keys_and_own_scale(lib):
 
 
 @pytest.mark.parametrize("amp", [0.0, 30.0])
-def test_decode_equal_and_sharp_weights(lib, amp):
-    m = Layer(lib, [700, 128], hq=16, hkv=16, r=256)
+@pytest.mark.parametrize("r", [256, 512])
+def test_decode_equal_and_sharp_weights(lib, amp, r):
+    m = Layer(lib, [700, 128], hq=16, hkv=16, r=r)
     q = m.query(1, amp)
     m.check_decode(q, *m.decode(q))
 
@@ -290,9 +294,26 @@ def test_decode_without_lse_and_twice_the_same(lib):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_decode_captured_and_replayed_with_other_lengths_and_pages(lib):
+@pytest.mark.parametrize("hq,r,new", [(28, 256, 1), (28, 512, 1), (64, 512, 1)])
+def test_decode_rising_scores_raise_the_maximum_often(lib, hq, r, new):
+    """Scores that grow along the context: the running maxima move in every tile of every run, and
+    with them every accumulator is rescaled."""
     import torch
-    m = Layer(lib, [260, 300], hq=8, hkv=8, r=128)
+    m = Layer(lib, [3000, 1000], hq=hq, hkv=hq, r=r, dn=64, dv=64, scale=1.0, stale=False)
+    ramp = np.concatenate([np.arange(n) for n in m.lens]) / 20.0
+    m.kr[:, 0] = bf16(ramp)
+    seq = np.repeat([0, 1], m.lens)
+    lib.lr_shared_append(m.cache, m.c, m.kr, i32(seq), i32(np.concatenate([np.arange(n) for n in m.lens])))
+    m.kr64 = f64(m.kr)
+    q = m.query(1, 0.3)
+    q[..., 64] = 1.0
+    m.check_decode(q, *m.decode(q))
+
+
+@pytest.mark.parametrize("r", [128, 320])
+def test_decode_captured_and_replayed_with_other_lengths_and_pages(lib, r):
+    import torch
+    m = Layer(lib, [260, 300], hq=8, hkv=8, r=r)
     q = m.query(1)
     lens = i32([260, 300])
     out = torch.zeros((2, 1, 8, 128), dtype=torch.bfloat16, device="cuda")
@@ -349,8 +370,9 @@ def test_bad_device_pages_are_clamped(lib):
     m.check_decode(q, *m.decode(q))
 
 
-def test_waits_that_give_up_are_reported_and_the_cache_recovers(lib):
-    m = Layer(lib, [500, 129], hq=8, hkv=8, r=256)
+@pytest.mark.parametrize("r,bits", [(256, 0), (512, 0), (512, 8)])
+def test_waits_that_give_up_are_reported_and_the_cache_recovers(lib, r, bits):
+    m = Layer(lib, [500, 129], hq=8, hkv=8, r=r, bits=bits)
     q = m.query(1)
     import torch
     out, lens = torch.zeros((2, 1, 8, 128), dtype=torch.bfloat16, device="cuda"), i32(m.lens)
