@@ -9,7 +9,8 @@
 // other is in its softmax: S0 S1 | PV0 S0' PV1 S1' | ...  Each tile has its own warpgroup
 // (thread = query row = TMEM lane: row maxima and sums need no shuffles).  P overlays S in
 // TMEM; the MMAs of one CTA run in issue order, so S' of a tile is written after its PV has
-// read P.  Keys and values stream through one ring of 16 KB boxes (64 columns x 128 rows).
+// read P.  Key tiles have two stages, value tiles one or two
+// (what the query tiles leave of shared memory), in boxes of 64 columns x 128 rows.
 //
 // Bound: the tensor pipe, 2 x 128 x 128 (dn + dr + dv) MACs per tile pair and key tile
 // (2560 clocks at 192 + 128) against 2048 clocks of exponentials on the same SM.
@@ -28,15 +29,20 @@ using tc::drain_wait;
 using tc::kLazy;
 
 constexpr int kBox = 128 * 128;        // 128 rows x 64 columns x 2 B
-constexpr int kRing = 8;
-constexpr int kThreads = 320;
+constexpr int kKStages = 2, kMaxVStages = 2;
+// Three warpgroups: 0 and 1 softmax of tiles 0 and 1, 2 MMA issuers (warps 8 and 10), TMA producer
+// (warp 9) and an idle warp.  Launched at 168 registers, rebalanced so that a softmax thread holds its
+// row of 128 scores (read from TMEM once).
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kCtlRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kCtlRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr int kAuxBytes = 1024;
 constexpr float kNoMax = -1e30f;
 
 struct AttArgs {
   unsigned long long wait_ns;
   const int32_t* cu_q; const int32_t* cu_k;
-  int nseq, total_q, total_k, Hq, g, dn, dv, dq, causal, slots;   // slots: tile pairs in the grid
+  int nseq, total_q, total_k, Hq, g, dn, dv, dq, causal, slots, nvs;   // slots: tile pairs a head; nvs: value stages
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
@@ -45,12 +51,14 @@ struct AttArgs {
 
 // Barriers (arrival count; who arrives -> who waits):
 //   q_full          1 + tx   producer -> MMA
-//   full/empty[s]   1 + tx / 1   boxes of K, Kr, V in the order of use
+//   k_full/k_empty[s]   1 + tx / 2   key tiles [K | Kr]; freed by both MMA warps
+//   v_full/v_empty[s]   1 + tx / 2   value tiles
 //   s_full[t]       1        MMA commit of S of tile t -> its softmax warps
-//   p_full[t]       4        softmax warps (P stored) -> MMA
+//   p_full[t][h]    4        softmax warps (P of keys 64 h .. 64 h + 63 stored) -> MMA
 //   pv_done[t]      1        MMA commit of PV -> softmax warps (O rescale, epilogue)
+//   done            2        final commits of both MMA warps
 struct Aux {
-  uint64_t q_full, full[kRing], empty[kRing], s_full[2], p_full[2], pv_done[2], done;
+  uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kMaxVStages], v_empty[kMaxVStages], s_full[2], p_full[2][2], pv_done[2], done;
   uint32_t tmem_base;
   int abort_flag;
   int b, pair;
@@ -63,6 +71,18 @@ __device__ __forceinline__ bool wait_b(uint64_t* bar, uint32_t parity, Aux* aux,
 }
 __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, Aux* aux, int* err) {
   return __all_sync(0xffffffffu, wait_b(bar, parity, aux, err));
+}
+
+// A warp-uniform value, known as such to the compiler: MMA operands then stay in uniform registers
+// (an MMA issues at the tensor core's pace; without, every ~160 cycles).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// An MMA warp is done with a stage: when its MMAs on it complete, or at once if it had none (after
+// it has seen the stage filled, so that the arrival counts for this filling).
+__device__ __forceinline__ void stage_done(uint64_t* bar, bool used, int lane) {
+  if (used) ptx::mma_commit_elect(bar);
+  else if (lane == 0) ptx::mbar_arrive(bar);
+  __syncwarp();
 }
 
 // Rows of sequence b in a packed array of `total` rows.
@@ -87,7 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* q_s = smem_raw + kAuxBytes;                 // 2 tiles x nqb boxes
   const int nqb = (p.dq + 63) >> 6;                    // 64-column boxes of a query row
   const int nkb = (p.dn >> 6) + 1, nvb = p.dv >> 6;    // boxes of a key tile (rotary last), of a value tile
-  uint8_t* ring = q_s + 2 * nqb * kBox;
+  uint8_t* k_s = q_s + 2 * nqb * kBox;                 // key stages, then p.nvs value stages
+  uint8_t* v_s = k_s + kKStages * nkb * kBox;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x % p.Hq, kvh = head / p.g;
 
@@ -106,16 +127,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     ptx::mbar_init(&aux->q_full, 1);
-    for (int s = 0; s < kRing; ++s) {
-      ptx::mbar_init(&aux->full[s], 1);
-      ptx::mbar_init(&aux->empty[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&aux->k_full[s], 1);
+      ptx::mbar_init(&aux->k_empty[s], 2);
+      ptx::mbar_init(&aux->v_full[s], 1);
+      ptx::mbar_init(&aux->v_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(&aux->s_full[t], 1);
-      ptx::mbar_init(&aux->p_full[t], 4);
+      ptx::mbar_init(&aux->p_full[t][0], 4);
+      ptx::mbar_init(&aux->p_full[t][1], 4);
       ptx::mbar_init(&aux->pv_done[t], 1);
     }
-    ptx::mbar_init(&aux->done, 1);
+    ptx::mbar_init(&aux->done, 2);
     aux->abort_flag = 0;
     aux->wait_ns = tc::wait_limit(p.wait_ns);
     ptx::fence_mbar_init();
@@ -143,104 +167,106 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int ntk = max(nt[0], nt[1]);
 
-  if (warp == 9) {
-    // ------------------------------------------------------------- TMA producer
-    if (lane == 0 && ntk > 0) {
-      const int tiles = rq.n - q0 > 128 ? 2 : 1;
-      ptx::mbar_arrive_expect_tx(&aux->q_full, (uint32_t)(tiles * nqb * kBox));
-      for (int t = 0; t < tiles; ++t)
-        for (int c = 0; c < nqb; ++c)
-          ptx::tma_load_3d(q_s + (t * nqb + c) * kBox, &tm_q, &aux->q_full, c * 64, head, rq.first + q0 + t * 128);
-      int pos = 0;
-      bool ok = true;
-      for (int j = 0; j < ntk && ok; ++j) {
-        const int row = rk.first + j * 128;
-        for (int c = 0; c < nkb + nvb; ++c) {
-          const int s = pos % kRing;
-          if (pos >= kRing && !(ok = wait_b(&aux->empty[s], (pos / kRing - 1) & 1, aux, p.err))) break;
-          ptx::mbar_arrive_expect_tx(&aux->full[s], kBox);
-          uint8_t* dst = ring + s * kBox;
-          if (c < nkb - 1) ptx::tma_load_3d(dst, &tm_k, &aux->full[s], c * 64, kvh, row);
-          else if (c == nkb - 1) ptx::tma_load_2d(dst, &tm_kr, &aux->full[s], 0, row);
-          else ptx::tma_load_3d(dst, &tm_v, &aux->full[s], (c - nkb) * 64, kvh, row);
-          ++pos;
+  if (warp >= 8) {
+    ptx::setmaxnreg_dec<kCtlRegs>();
+    if (warp == 9) {
+      // ------------------------------------------------------------- TMA producer
+      if (lane == 0 && ntk > 0) {
+        const int tiles = rq.n - q0 > 128 ? 2 : 1;
+        ptx::mbar_arrive_expect_tx(&aux->q_full, (uint32_t)(tiles * nqb * kBox));
+        for (int t = 0; t < tiles; ++t)
+          for (int c = 0; c < nqb; ++c)
+            ptx::tma_load_3d(q_s + (t * nqb + c) * kBox, &tm_q, &aux->q_full, c * 64, head, rq.first + q0 + t * 128);
+        bool ok = true;
+        int nk = 0, nv = 0;                  // tiles issued
+        for (int j = 0; j < ntk; ++j) {
+          const int row = rk.first + j * 128, ks = j & 1, vs = p.nvs == 2 ? j & 1 : 0;
+          if (j >= kKStages && !(ok = wait_b(&aux->k_empty[ks], ((j >> 1) - 1) & 1, aux, p.err))) break;
+          ptx::mbar_arrive_expect_tx(&aux->k_full[ks], (uint32_t)(nkb * kBox));
+          for (int c = 0; c < nkb - 1; ++c)
+            ptx::tma_load_2d(k_s + (ks * nkb + c) * kBox, &tm_k, &aux->k_full[ks], kvh * p.dn + c * 64, row);
+          ptx::tma_load_2d(k_s + (ks * nkb + nkb - 1) * kBox, &tm_kr, &aux->k_full[ks], 0, row);
+          ++nk;
+          if (j >= p.nvs && !(ok = wait_b(&aux->v_empty[vs], (p.nvs == 2 ? (j >> 1) - 1 : j - 1) & 1, aux, p.err)))
+            break;
+          ptx::mbar_arrive_expect_tx(&aux->v_full[vs], (uint32_t)(nvb * kBox));
+          for (int c = 0; c < nvb; ++c)
+            ptx::tma_load_2d(v_s + (vs * nvb + c) * kBox, &tm_v, &aux->v_full[vs], kvh * p.dv + c * 64, row);
+          ++nv;
         }
+        // every copy this thread issued has landed before the CTA can exit
+        drain_wait(&aux->q_full, 0);
+        for (int j = max(0, nk - 2); j < nk; ++j) drain_wait(&aux->k_full[j & 1], (j >> 1) & 1);
+        for (int j = max(0, nv - p.nvs); j < nv; ++j)
+          drain_wait(&aux->v_full[p.nvs == 2 ? j & 1 : 0], (p.nvs == 2 ? j >> 1 : j) & 1);
       }
-      // every copy this thread issued has landed before the CTA can exit
-      drain_wait(&aux->q_full, 0);
-      for (int k = max(0, pos - kRing); k < pos; ++k) drain_wait(&aux->full[k % kRing], (k / kRing) & 1);
-    }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------- MMA issuer (warp-wide)
-    if (ntk > 0) {
+    } else if (warp != 11 && ntk > 0) {
+      // ------------------------------------------------------------- MMA issuer of tile t (warp-wide)
+      // A warp per tile: an MMA's issue waits for the tensor pipe, so whatever stands between two
+      // MMAs of one warp (a barrier test costs ~130 cycles, serial code ~8 a instruction beside busy
+      // softmax warps) leaves the pipe idle unless the other tile's warp issues meanwhile.  For the
+      // same reason a key tile is one stage with one barrier, and addresses are made once.
+      const int t = warp == 10 ? 1 : 0, ntt = nt[t];
       const uint32_t ids = ptx::idesc_f16(1, 0, 0, 128, 128);                  // S: K-major x K-major
       const uint32_t idv = ptx::idesc_f16(1, 0, 1, 128, (uint32_t)p.dv);       // PV: TMEM x MN-major
-      const uint64_t qd0 = ptx::smem_desc(ptx::smem_u32(q_s), 16, 1024, 2);
-      const uint64_t kd0 = ptx::smem_desc(ptx::smem_u32(ring), 16, 1024, 2);
-      const uint64_t vd0 = ptx::smem_desc(ptx::smem_u32(ring), kBox, 1024, 2);
-      const int per = nkb + nvb;
-      auto scores = [&](int t, int j, bool wait) -> bool {
-        for (int c = 0; c < nkb; ++c) {
-          const int pos = j * per + c, s = pos % kRing;
-          if (wait && !wait_w(&aux->full[s], (pos / kRing) & 1, aux, p.err)) return false;
-          ptx::tc_fence_after();
-          // the query boxes: dn, then the rotary columns (dn and dn + 64 are box borders)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            ptx::mma_f16_elect(tmem + t * 128, qd0 + (uint64_t)(((t * nqb + c) * kBox >> 4) + kk * 2),
-                               kd0 + (uint64_t)((s * kBox >> 4) + kk * 2), ids, (c | kk) ? 1u : 0u);
-        }
-        ptx::mma_commit_elect(&aux->s_full[t]);
-        return true;
-      };
-      auto values = [&](int t, int j, bool wait) -> bool {
-        if (!wait_w(&aux->p_full[t], j & 1, aux, p.err)) return false;
-        const int pos0 = j * per + nkb;
-        if (wait)
-          for (int c = 0; c < nvb; ++c)
-            if (!wait_w(&aux->full[(pos0 + c) % kRing], ((pos0 + c) / kRing) & 1, aux, p.err)) return false;
-        ptx::tc_fence_after();
-        // a box at a time along N: the boxes of a tile need not be neighbours in the ring
-        const uint32_t idh = ptx::idesc_f16(1, 0, 1, 128, 64);
-        const int s0 = pos0 % kRing;
-        if (nvb == 2 && s0 + 1 < kRing) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            ptx::mma_f16_ta_elect(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                                  vd0 + (uint64_t)((s0 * kBox + kk * 2048) >> 4), idv, (j | kk) ? 1u : 0u);
-        } else {
-          for (int c = 0; c < nvb; ++c) {
-            const int s = (pos0 + c) % kRing;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              ptx::mma_f16_ta_elect(tmem + 256 + t * 128 + c * 64, tmem + t * 128 + kk * 8,
-                                    vd0 + (uint64_t)((s * kBox + kk * 2048) >> 4), idh, (j | kk) ? 1u : 0u);
-          }
-        }
-        ptx::mma_commit_elect(&aux->pv_done[t]);
-        return true;
-      };
-      auto release = [&](int pos, int n) {
-        for (int c = 0; c < n; ++c) ptx::mma_commit_elect(&aux->empty[(pos + c) % kRing]);
-      };
+      const uint64_t qd = ptx::smem_desc(ptx::smem_u32(q_s + t * nqb * kBox), 16, 1024, 2);
+      const uint64_t kd = ptx::smem_desc(ptx::smem_u32(k_s), 16, 1024, 2);
+      const uint64_t vd = ptx::smem_desc(ptx::smem_u32(v_s), kBox, 1024, 2);
+      const uint32_t d_s = uniform(tmem + t * 128);
+      const uint32_t k_step = (uint32_t)(nkb * kBox) >> 4, v_step = p.nvs == 2 ? (uint32_t)(nvb * kBox) >> 4 : 0u;
       bool ok = wait_w(&aux->q_full, 0, aux, p.err);
-      if (ok && nt[0] > 0) ok = scores(0, 0, true);
-      if (ok && nt[1] > 0) ok = scores(1, 0, nt[0] == 0);
-      if (ok) release(0, nkb);
-      for (int j = 0; j < ntk && ok; ++j) {
-        const bool first_v = j < nt[0], first_k = j + 1 < nt[0];
-        if (ok && first_v) ok = values(0, j, true);
-        if (ok && first_k) ok = scores(0, j + 1, true);
-        if (ok && j < nt[1]) ok = values(1, j, !first_v);
-        if (ok) release(j * per + nkb, nvb);
-        if (ok && j + 1 < nt[1]) ok = scores(1, j + 1, !first_k);
-        if (ok && j + 1 < ntk) release((j + 1) * per, nkb);
+#pragma unroll 1
+      for (int j = 0; j <= ntk && ok; ++j) {
+        // PV(j - 1), in two halves of 64 keys: the first starts while the softmax works on the second
+        if (j > 0) {
+          const int i = j - 1, vs = p.nvs == 2 ? i & 1 : 0;
+          if (!(ok = wait_w(&aux->v_full[vs], (p.nvs == 2 ? i >> 1 : i) & 1, aux, p.err))) break;
+          if (i < ntt) {
+            const uint64_t vb = vd + uniform(vs * v_step);
+            const uint32_t more = uniform(i ? 1u : 0u);
+            if (!(ok = wait_w(&aux->p_full[t][0], i & 1, aux, p.err))) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              ptx::mma_f16_ta_elect(d_s + 256, d_s + kk * 8, vb + (uint64_t)(kk * 128), idv, kk ? 1u : more);
+            if (!(ok = wait_w(&aux->p_full[t][1], i & 1, aux, p.err))) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk)
+              ptx::mma_f16_ta_elect(d_s + 256, d_s + kk * 8, vb + (uint64_t)(kk * 128), idv, 1u);
+            ptx::mma_commit_elect(&aux->pv_done[t]);
+          }
+          stage_done(&aux->v_empty[vs], i < ntt, lane);
+        }
+        // S(j): the query boxes are dn, then the rotary columns (dn and dn + 64 are box borders).
+        // Tile 1 starts when tile 0 is half through its softmax: in step, both would want the
+        // tensor pipe at one time and the exponentials at another.
+        if (j < ntk) {
+          const int ks = j & 1;
+          if (!(ok = wait_w(&aux->k_full[ks], (j >> 1) & 1, aux, p.err))) break;
+          if (j < ntt) {
+            if (t == 1 && j < nt[0] && !(ok = wait_w(&aux->p_full[0][0], j & 1, aux, p.err))) break;
+            ptx::tc_fence_after();
+            const uint64_t kb = kd + uniform(ks * k_step);
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+              if (c < nkb) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  ptx::mma_f16_elect(d_s, qd + (uint64_t)((c * kBox >> 4) + kk * 2),
+                                     kb + (uint64_t)((c * kBox >> 4) + kk * 2), ids, c + kk ? 1u : 0u);
+              }
+            ptx::mma_commit_elect(&aux->s_full[t]);
+          }
+          stage_done(&aux->k_empty[ks], j < ntt, lane);
+        }
       }
       ptx::mma_commit_elect(&aux->done);
       drain_wait(&aux->done, 0);
     }
     __syncwarp();
   } else {
+    ptx::setmaxnreg_inc<kSoftmaxRegs>();
     // ------------------------------------------------------------- softmax and epilogue, tile t
     const int t = warp >> 2, qd = warp & 3;
     const int row = qd * 32 + lane, i = q0 + t * 128 + row;
@@ -253,71 +279,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_w(&aux->s_full[t], j & 1, aux, p.err))) break;
       ptx::tc_fence_after();
       const int lim = last - j * 128;              // columns 0..lim are visible
-      const bool edge = wlast - j * 128 < 127;     // some row of the warp masks columns here
-      float mx = -INFINITY;
+      uint32_t v[4][32];                           // the row's scores, as fp32 bits
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        ptx::tmem_ld32(s_col + 32 * c, v);
-        ptx::tmem_wait_ld();
-        if (edge) {
+      for (int c = 0; c < 4; ++c) ptx::tmem_ld32(s_col + 32 * c, v[c]);
+      ptx::tmem_wait_ld();
+      if (wlast - j * 128 < 127) {                 // some row of the warp masks columns here
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * c + e <= lim) mx = fmaxf(mx, __uint_as_float(v[e]));
-        } else {
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
-        }
-      }
-      mx *= p.scale_log2;
-      if (__any_sync(0xffffffffu, mx > m + kLazy)) {
-        const float mn = fmaxf(m, mx), a = ptx::ex2_approx(m - mn);
-        m = mn;
-        l *= a;
-        if (j > 0) {
-          if (!(ok = wait_w(&aux->pv_done[t], (j - 1) & 1, aux, p.err))) break;
-          ptx::tc_fence_after();
-          for (int c = 0; c < p.dv; c += 32) {
-            uint32_t v[32];
-            ptx::tmem_ld32(o_col + c, v);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
-            ptx::tmem_st32(o_col + c, v);
-          }
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32], w[16];
-        ptx::tmem_ld32(s_col + 32 * c, v);
-        ptx::tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float p0 = ptx::ex2_approx(fmaf(__uint_as_float(v[2 * e]), p.scale_log2, -m));
-          float p1 = ptx::ex2_approx(fmaf(__uint_as_float(v[2 * e + 1]), p.scale_log2, -m));
-          if (edge) {
-            if (32 * c + 2 * e > lim) p0 = 0.f;
-            if (32 * c + 2 * e + 1 > lim) p1 = 0.f;
-          }
-          l += p0;
-          l += p1;
-          const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-          w[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        ptx::tmem_st16(s_col + 16 * c, w);
+          for (int e = 0; e < 32; ++e) v[c][e] = 32 * c + e <= lim ? v[c][e] : 0xFF800000u;   // -inf
       }
       if (j * 128 + 128 > rk.n) {
         // the rows behind the last key belong to the next sequence: weight 0, but 0 times an
         // infinity there would be NaN, so their values become 0 (each tile clears them before it
         // hands over its weights; both store the same)
-        const int pos0 = j * (nkb + nvb) + nkb;
-        for (int c = 0; c < nvb; ++c)
-          if (!(ok = wait_w(&aux->full[(pos0 + c) % kRing], ((pos0 + c) / kRing) & 1, aux, p.err))) break;
-        if (!ok) break;
+        const int vs = p.nvs == 2 ? j & 1 : 0;
+        if (!(ok = wait_w(&aux->v_full[vs], (p.nvs == 2 ? j >> 1 : j) & 1, aux, p.err))) break;
         if (j * 128 + row >= rk.n)
           for (int c = 0; c < nvb; ++c) {
-            const uint32_t base = ptx::smem_u32(ring + ((pos0 + c) % kRing) * kBox + row * 128);
+            const uint32_t base = ptx::smem_u32(v_s + (vs * nvb + c) * kBox + row * 128);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + e * 16), "r"(0) : "memory");
@@ -325,10 +305,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_proxy_async_smem();
         __syncwarp();
       }
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&aux->p_full[t]);
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = __uint_as_float(v[c][0]);
+#pragma unroll
+        for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(v[c][e]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      if (__any_sync(0xffffffffu, top > m + kLazy)) {
+        const float mn = fmaxf(m, top), a = ptx::ex2_approx(m - mn);
+        m = mn;
+        l *= a;
+        if (j > 0) {
+          if (!(ok = wait_w(&aux->pv_done[t], (j - 1) & 1, aux, p.err))) break;
+          ptx::tc_fence_after();
+          for (int c = 0; c < p.dv; c += 16) {
+            uint32_t o[16];
+            ptx::tmem_ld16(o_col + c, o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+            ptx::tmem_st16(o_col + c, o);
+          }
+        }
+      }
+      const float2 sc = make_float2(p.scale_log2, p.scale_log2), nm = make_float2(-m, -m);
+      float2 sum[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+        sum[c] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = ptx::fma2(make_float2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), sc, nm);
+          const float2 y = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
+          sum[c] = ptx::add2(sum[c], y);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
+          w[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        ptx::tmem_st16(s_col + 16 * c, w);
+        if (c & 1) {
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&aux->p_full[t][c >> 1]);
+        }
+      }
+      const float2 l2 = ptx::add2(ptx::add2(sum[0], sum[1]), ptx::add2(sum[2], sum[3]));
+      l += l2.x + l2.y;
     }
     if (ok && nt[t] > 0) ok = wait_w(&aux->pv_done[t], (nt[t] - 1) & 1, aux, p.err);
     ptx::tc_fence_after();
@@ -368,6 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+bool map2d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1) {
+  const cuuint64_t dims[2] = {d0, d1}, st[1] = {d0 * 2};
+  const cuuint32_t box[2] = {64, 128};
+  return tc::make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, 2, dims, st, box);
+}
 bool map3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2) {
   const cuuint64_t dims[3] = {d0, d1, d2}, st[2] = {d0 * 2, d0 * d1 * 2};
   const cuuint32_t box[3] = {64, 1, 128};
@@ -403,17 +433,21 @@ cudaError_t launch_shared_attn(lr_shared* c, const void* q, const void* k, const
   CUtensorMap tq, tk, tkr, tv;
   if (total_k == 0) k = kr = v = q;      // no key tile is ever loaded; the maps need an address
   const cuuint64_t rows = std::max(total_k, 1);
-  if (!map3d(&tq, q, a.dq, a.Hq, total_q) || !map3d(&tk, k, a.dn, d.n_kv_heads, rows) ||
-      !map3d(&tv, v, a.dv, d.n_kv_heads, rows))
+  if (!map3d(&tq, q, a.dq, a.Hq, total_q) || !map2d(&tk, k, (uint64_t)d.n_kv_heads * a.dn, rows) ||
+      !map2d(&tv, v, (uint64_t)d.n_kv_heads * a.dv, rows) || !map2d(&tkr, kr, d.dim_rope, rows))
     return cudaErrorInvalidValue;
-  {
-    const cuuint64_t dims[2] = {(cuuint64_t)d.dim_rope, rows}, st[1] = {(cuuint64_t)d.dim_rope * 2};
-    const cuuint32_t box[2] = {64, 128};
-    if (!tc::make_map(&tkr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kr, 2, dims, st, box)) return cudaErrorInvalidValue;
-  }
-  const size_t smem = kAuxBytes + (size_t)(2 * ((a.dq + 63) / 64) + kRing) * kBox;
+  const int nqb = (a.dq + 63) / 64, fixed = 2 * nqb + kKStages * (a.dn / 64 + 1), nvb = a.dv / 64;   // boxes
+  a.nvs = kAuxBytes + (size_t)(fixed + 2 * nvb) * kBox <= (size_t)tc::kSmemLimit ? 2 : 1;
+  const size_t smem = kAuxBytes + (size_t)(fixed + a.nvs * nvb) * kBox;
   static std::atomic<uint32_t> optin{0};
   cudaError_t e = smem_optin(k_shared_attn, optin);
   if (e != cudaSuccess) return e;
+  // the register split was sized for exactly this launch allocation (an increase beyond it waits)
+  static std::atomic<int> regs{-1};
+  if (regs.load() < 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, k_shared_attn) == cudaSuccess) regs.store(fa.numRegs);
+  }
+  if (regs.load() != kLaunchRegs) return cudaErrorInvalidConfiguration;
   return launch_pdl(k_shared_attn, dim3((unsigned)(slots * a.Hq)), dim3(kThreads), smem, s, tq, tk, tkr, tv, a);
 }
