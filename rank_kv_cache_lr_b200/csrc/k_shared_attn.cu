@@ -9,8 +9,8 @@
 // other is in its softmax: S0 S1 | PV0 S0' PV1 S1' | ...  Each tile has its own warpgroup
 // (thread = query row = TMEM lane: row maxima and sums need no shuffles).  P overlays S in
 // TMEM; the MMAs of one CTA run in issue order, so S' of a tile is written after its PV has
-// read P.  Key tiles have two stages, value tiles one or two
-// (what the query tiles leave of shared memory), in boxes of 64 columns x 128 rows.
+// read P.  Keys and values pass through one ring of 16 KB slots
+// (what the query tiles leave of shared memory; 8 slots against 5 a tile at 192 + 128).
 //
 // Bound: the tensor pipe, 2 x 128 x 128 (dn + dr + dv) MACs per tile pair and key tile
 // (2560 clocks at 192 + 128) against 2048 clocks of exponentials on the same SM.
@@ -29,7 +29,7 @@ using tc::drain_wait;
 using tc::kLazy;
 
 constexpr int kBox = 128 * 128;        // 128 rows x 64 columns x 2 B
-constexpr int kKStages = 2, kMaxVStages = 2;
+constexpr int kVBox = kBox / 2;        // 64 rows x 64 columns x 2 B
 // Three warpgroups: 0 and 1 softmax of tiles 0 and 1, 2 MMA issuers (warps 8 and 10), TMA producer
 // (warp 9) and an idle warp.  Launched at 168 registers, rebalanced so that a softmax thread holds its
 // row of 128 scores (read from TMEM once).
@@ -42,23 +42,23 @@ constexpr float kNoMax = -1e30f;
 struct AttArgs {
   unsigned long long wait_ns;
   const int32_t* cu_q; const int32_t* cu_k;
-  int nseq, total_q, total_k, Hq, g, dn, dv, dq, causal, slots, nvs;   // slots: tile pairs a head; nvs: value stages
+  int nseq, total_q, total_k, Hq, g, dn, dv, dq, causal, slots, ring;   // slots: tile pairs a head; ring: 16 KB slots for keys and values
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
   int* err;
 };
 
-// Barriers (arrival count; who arrives -> who waits):
-//   q_full          1 + tx   producer -> MMA
-//   k_full/k_empty[s]   1 + tx / 2   key tiles [K | Kr]; freed by both MMA warps
-//   v_full/v_empty[s]   1 + tx / 2   value tiles
-//   s_full[t]       1        MMA commit of S of tile t -> its softmax warps
-//   p_full[t][h]    4        softmax warps (P of keys 64 h .. 64 h + 63 stored) -> MMA
-//   pv_done[t]      1        MMA commit of PV -> softmax warps (O rescale, epilogue)
-//   done            2        final commits of both MMA warps
+// Barriers (arrival count; who arrives -> who waits).  [2]: by the parity of the key tile, so that a
+// waiter may be one key tile behind the arriver.
+//   q_full            1 + tx   producer -> MMA
+//   k_full, v_full[2] 1 + tx   producer -> MMA (values also -> softmax, which clears the last tile's rest)
+//   s_full[t][2]      1        MMA commit of S of tile t -> its softmax warps, producer (the keys' slots)
+//   p_full[t][h][2]   4        softmax warps (P of keys 64 h .. 64 h + 63 stored) -> MMA
+//   pv_done[t][2]     1        MMA commit of PV -> producer (the values' slots), epilogue
+//   done              2        final commits of both MMA warps
 struct Aux {
-  uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kMaxVStages], v_empty[kMaxVStages], s_full[2], p_full[2][2], pv_done[2], done;
+  uint64_t q_full, k_full[2], v_full[2], s_full[2][2], p_full[2][2][2], pv_done[2][2], done;
   uint32_t tmem_base;
   int abort_flag;
   int b, pair;
@@ -76,14 +76,6 @@ __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, Aux* aux,
 // A warp-uniform value, known as such to the compiler: MMA operands then stay in uniform registers
 // (an MMA issues at the tensor core's pace; without, every ~160 cycles).
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// An MMA warp is done with a stage: when its MMAs on it complete, or at once if it had none (after
-// it has seen the stage filled, so that the arrival counts for this filling).
-__device__ __forceinline__ void stage_done(uint64_t* bar, bool used, int lane) {
-  if (used) ptx::mma_commit_elect(bar);
-  else if (lane == 0) ptx::mbar_arrive(bar);
-  __syncwarp();
-}
 
 // Rows of sequence b in a packed array of `total` rows.
 struct Rows {
@@ -106,9 +98,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Aux* aux = reinterpret_cast<Aux*>(smem_raw);
   uint8_t* q_s = smem_raw + kAuxBytes;                 // 2 tiles x nqb boxes
   const int nqb = (p.dq + 63) >> 6;                    // 64-column boxes of a query row
-  const int nkb = (p.dn >> 6) + 1, nvb = p.dv >> 6;    // boxes of a key tile (rotary last), of a value tile
-  uint8_t* k_s = q_s + 2 * nqb * kBox;                 // key stages, then p.nvs value stages
-  uint8_t* v_s = k_s + kKStages * nkb * kBox;
+  // slots of a key tile (rotary last): 128 keys x 64 columns each; of a value tile: all columns of 64
+  // keys (dv = 128) or of 128 keys (dv = 64), so that half h of the keys is one operand
+  const int nkb = (p.dn >> 6) + 1, nvb = p.dv >> 6, unit = nkb + nvb;
+  uint8_t* kv_s = q_s + 2 * nqb * kBox;                // the ring: K0 V0 K1 V1 ..., p.ring slots of kBox
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x % p.Hq, kvh = head / p.g;
 
@@ -129,15 +122,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&aux->q_full, 1);
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&aux->k_full[s], 1);
-      ptx::mbar_init(&aux->k_empty[s], 2);
       ptx::mbar_init(&aux->v_full[s], 1);
-      ptx::mbar_init(&aux->v_empty[s], 2);
-    }
-    for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(&aux->s_full[t], 1);
-      ptx::mbar_init(&aux->p_full[t][0], 4);
-      ptx::mbar_init(&aux->p_full[t][1], 4);
-      ptx::mbar_init(&aux->pv_done[t], 1);
+      for (int t = 0; t < 2; ++t) {
+        ptx::mbar_init(&aux->s_full[t][s], 1);
+        ptx::mbar_init(&aux->p_full[t][0][s], 4);
+        ptx::mbar_init(&aux->p_full[t][1][s], 4);
+        ptx::mbar_init(&aux->pv_done[t][s], 1);
+      }
     }
     ptx::mbar_init(&aux->done, 2);
     aux->abort_flag = 0;
@@ -177,89 +168,121 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < tiles; ++t)
           for (int c = 0; c < nqb; ++c)
             ptx::tma_load_3d(q_s + (t * nqb + c) * kBox, &tm_q, &aux->q_full, c * 64, head, rq.first + q0 + t * 128);
+        // Slots are taken and given back in one order, K0 V0 K1 V1 ..., so V_j goes where K_{j-1} was (free
+        // early: its scores are done) and K_{j+1} partly where V_{j-1} was.
         bool ok = true;
-        int nk = 0, nv = 0;                  // tiles issued
-        for (int j = 0; j < ntk; ++j) {
-          const int row = rk.first + j * 128, ks = j & 1, vs = p.nvs == 2 ? j & 1 : 0;
-          if (j >= kKStages && !(ok = wait_b(&aux->k_empty[ks], ((j >> 1) - 1) & 1, aux, p.err))) break;
-          ptx::mbar_arrive_expect_tx(&aux->k_full[ks], (uint32_t)(nkb * kBox));
-          for (int c = 0; c < nkb - 1; ++c)
-            ptx::tma_load_2d(k_s + (ks * nkb + c) * kBox, &tm_k, &aux->k_full[ks], kvh * p.dn + c * 64, row);
-          ptx::tma_load_2d(k_s + (ks * nkb + nkb - 1) * kBox, &tm_kr, &aux->k_full[ks], 0, row);
-          ++nk;
-          if (j >= p.nvs && !(ok = wait_b(&aux->v_empty[vs], (p.nvs == 2 ? (j >> 1) - 1 : j - 1) & 1, aux, p.err)))
-            break;
-          ptx::mbar_arrive_expect_tx(&aux->v_full[vs], (uint32_t)(nvb * kBox));
-          for (int c = 0; c < nvb; ++c)
-            ptx::tma_load_2d(v_s + (vs * nvb + c) * kBox, &tm_v, &aux->v_full[vs], kvh * p.dv + c * 64, row);
-          ++nv;
+        int at = 0, left = p.ring, ftile = 0;          // next slot, free slots, next tile to be freed
+        auto slot = [&]() -> uint8_t* {                // the next slot, once its last tile was used by both query tiles
+          while (left == 0 && ok) {
+            const int i = ftile >> 1, s = i & 1, ph = (i >> 1) & 1;
+            for (int t = 0; t < 2 && ok; ++t)
+              if (i < nt[t]) ok = wait_b(ftile & 1 ? &aux->pv_done[t][s] : &aux->s_full[t][s], ph, aux, p.err);
+            left += ftile & 1 ? nvb : nkb;
+            ++ftile;
+          }
+          uint8_t* const dst = kv_s + at * kBox;
+          if (++at == p.ring) at = 0;
+          --left;
+          return dst;
+        };
+        int nk = 0, nv = 0;                            // key and value tiles begun
+        for (int j = 0; j < ntk && ok; ++j) {
+          const int row = rk.first + j * 128, s = j & 1;
+          for (int c = 0; c < nkb; ++c) {
+            uint8_t* dst = slot();
+            if (!ok) break;
+            if (c == 0) {
+              ptx::mbar_arrive_expect_tx(&aux->k_full[s], (uint32_t)(nkb * kBox));
+              ++nk;
+            }
+            if (c < nkb - 1) ptx::tma_load_2d(dst, &tm_k, &aux->k_full[s], kvh * p.dn + c * 64, row);
+            else ptx::tma_load_2d(dst, &tm_kr, &aux->k_full[s], 0, row);
+          }
+          for (int c = 0; c < nvb && ok; ++c) {
+            uint8_t* dst = slot();
+            if (!ok) break;
+            if (c == 0) {
+              ptx::mbar_arrive_expect_tx(&aux->v_full[s], (uint32_t)(nvb * kBox));
+              ++nv;
+            }
+            for (int e = 0; e < 2; ++e)                // dv = 128: columns 64 e of key half c; else key half e
+              ptx::tma_load_2d(dst + e * kVBox, &tm_v, &aux->v_full[s], kvh * p.dv + (nvb == 2 ? e * 64 : 0),
+                               row + (nvb == 2 ? c : e) * 64);
+          }
         }
         // every copy this thread issued has landed before the CTA can exit
         drain_wait(&aux->q_full, 0);
         for (int j = max(0, nk - 2); j < nk; ++j) drain_wait(&aux->k_full[j & 1], (j >> 1) & 1);
-        for (int j = max(0, nv - p.nvs); j < nv; ++j)
-          drain_wait(&aux->v_full[p.nvs == 2 ? j & 1 : 0], (p.nvs == 2 ? j >> 1 : j) & 1);
+        for (int j = max(0, nv - 2); j < nv; ++j) drain_wait(&aux->v_full[j & 1], (j >> 1) & 1);
       }
     } else if (warp != 11 && ntk > 0) {
       // ------------------------------------------------------------- MMA issuer of tile t (warp-wide)
       // A warp per tile: an MMA's issue waits for the tensor pipe, so whatever stands between two
-      // MMAs of one warp (a barrier test costs ~130 cycles, serial code ~8 a instruction beside busy
-      // softmax warps) leaves the pipe idle unless the other tile's warp issues meanwhile.  For the
-      // same reason a key tile is one stage with one barrier, and addresses are made once.
+      // MMAs of one warp (a barrier test costs ~130 cycles, a commit ~60, serial code ~8 an instruction
+      // beside busy softmax warps) leaves the pipe idle unless the other tile's warp issues meanwhile.
+      // For the same reason a tile of keys or values has one barrier, and everything that S(j) needs
+      // is made ready before PV(j - 1)'s last wait.
       const int t = warp == 10 ? 1 : 0, ntt = nt[t];
       const uint32_t ids = ptx::idesc_f16(1, 0, 0, 128, 128);                  // S: K-major x K-major
       const uint32_t idv = ptx::idesc_f16(1, 0, 1, 128, (uint32_t)p.dv);       // PV: TMEM x MN-major
       const uint64_t qd = ptx::smem_desc(ptx::smem_u32(q_s + t * nqb * kBox), 16, 1024, 2);
-      const uint64_t kd = ptx::smem_desc(ptx::smem_u32(k_s), 16, 1024, 2);
-      const uint64_t vd = ptx::smem_desc(ptx::smem_u32(v_s), kBox, 1024, 2);
+      const uint64_t kd = ptx::smem_desc(ptx::smem_u32(kv_s), 16, 1024, 2);
+      const uint64_t vd = ptx::smem_desc(ptx::smem_u32(kv_s), kVBox, 1024, 2);
       const uint32_t d_s = uniform(tmem + t * 128);
-      const uint32_t k_step = (uint32_t)(nkb * kBox) >> 4, v_step = p.nvs == 2 ? (uint32_t)(nvb * kBox) >> 4 : 0u;
+      int kp = 0;                                      // ring slot of key tile j
+      uint64_t vb[2] = {vd, vd};                       // halves of value tile j - 1
       bool ok = wait_w(&aux->q_full, 0, aux, p.err);
 #pragma unroll 1
-      for (int j = 0; j <= ntk && ok; ++j) {
-        // PV(j - 1), in two halves of 64 keys: the first starts while the softmax works on the second
-        if (j > 0) {
-          const int i = j - 1, vs = p.nvs == 2 ? i & 1 : 0;
-          if (!(ok = wait_w(&aux->v_full[vs], (p.nvs == 2 ? i >> 1 : i) & 1, aux, p.err))) break;
-          if (i < ntt) {
-            const uint64_t vb = vd + uniform(vs * v_step);
-            const uint32_t more = uniform(i ? 1u : 0u);
-            if (!(ok = wait_w(&aux->p_full[t][0], i & 1, aux, p.err))) break;
-            ptx::tc_fence_after();
+      for (int j = 0; j <= ntt && ok; ++j) {
+        const int s = j & 1, ph = (j >> 1) & 1;
+        uint64_t kb[3];
+        int vp = kp;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              ptx::mma_f16_ta_elect(d_s + 256, d_s + kk * 8, vb + (uint64_t)(kk * 128), idv, kk ? 1u : more);
-            if (!(ok = wait_w(&aux->p_full[t][1], i & 1, aux, p.err))) break;
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int kk = 4; kk < 8; ++kk)
-              ptx::mma_f16_ta_elect(d_s + 256, d_s + kk * 8, vb + (uint64_t)(kk * 128), idv, 1u);
-            ptx::mma_commit_elect(&aux->pv_done[t]);
+        for (int c = 0; c < 3; ++c)
+          if (c < nkb) {
+            kb[c] = kd + uniform((uint32_t)vp * (kBox >> 4));
+            if (++vp == p.ring) vp = 0;
           }
-          stage_done(&aux->v_empty[vs], i < ntt, lane);
+        bool k_in = j == ntt;
+        // PV(j - 1), in two halves of 64 keys: the first runs while the softmax works on the second
+        if (j > 0) {
+          const int si = s ^ 1, phi = ((j - 1) >> 1) & 1;
+          const uint32_t more = uniform(j > 1 ? 1u : 0u);
+          if (!(ok = wait_w(&aux->v_full[si], phi, aux, p.err))) break;
+          if (!(ok = wait_w(&aux->p_full[t][0][si], phi, aux, p.err))) break;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_f16_ta_elect(d_s + 256, d_s + kk * 8, vb[0] + (uint64_t)(kk * 128), idv, kk ? 1u : more);
+          if (!k_in) k_in = __all_sync(0xffffffffu, ptx::mbar_test_wait(&aux->k_full[s], ph));
+          if (!(ok = wait_w(&aux->p_full[t][1][si], phi, aux, p.err))) break;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_f16_ta_elect(d_s + 256, d_s + 32 + kk * 8, vb[1] + (uint64_t)(kk * 128), idv, 1u);
+          ptx::mma_commit_elect(&aux->pv_done[t][si]);
         }
+        if (j == ntt) break;
         // S(j): the query boxes are dn, then the rotary columns (dn and dn + 64 are box borders).
         // Tile 1 starts when tile 0 is half through its softmax: in step, both would want the
         // tensor pipe at one time and the exponentials at another.
-        if (j < ntk) {
-          const int ks = j & 1;
-          if (!(ok = wait_w(&aux->k_full[ks], (j >> 1) & 1, aux, p.err))) break;
-          if (j < ntt) {
-            if (t == 1 && j < nt[0] && !(ok = wait_w(&aux->p_full[0][0], j & 1, aux, p.err))) break;
-            ptx::tc_fence_after();
-            const uint64_t kb = kd + uniform(ks * k_step);
+        if (!k_in && !(ok = wait_w(&aux->k_full[s], ph, aux, p.err))) break;
+        if (t == 1 && j < nt[0] && !(ok = wait_w(&aux->p_full[0][0][s], ph, aux, p.err))) break;
+        ptx::tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-              if (c < nkb) {
+        for (int c = 0; c < 3; ++c)
+          if (c < nkb) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  ptx::mma_f16_elect(d_s, qd + (uint64_t)((c * kBox >> 4) + kk * 2),
-                                     kb + (uint64_t)((c * kBox >> 4) + kk * 2), ids, c + kk ? 1u : 0u);
-              }
-            ptx::mma_commit_elect(&aux->s_full[t]);
+            for (int kk = 0; kk < 4; ++kk)
+              ptx::mma_f16_elect(d_s, qd + (uint64_t)((c * kBox >> 4) + kk * 2), kb[c] + (uint64_t)(kk * 2), ids, c + kk ? 1u : 0u);
           }
-          stage_done(&aux->k_empty[ks], j < ntt, lane);
-        }
+        ptx::mma_commit_elect(&aux->s_full[t][s]);
+        // value tile j lies behind key tile j
+        const int v1 = vp + 1 == p.ring ? 0 : vp + 1;
+        vb[0] = vd + uniform((uint32_t)vp * (kBox >> 4));
+        vb[1] = nvb == 2 ? vd + uniform((uint32_t)v1 * (kBox >> 4)) : vb[0] + (kVBox >> 4);
+        kp += unit;
+        if (kp >= p.ring) kp -= p.ring;
       }
       ptx::mma_commit_elect(&aux->done);
       drain_wait(&aux->done, 0);
@@ -276,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = kNoMax, l = 0.f;
     bool ok = true;
     for (int j = 0; j < nt[t]; ++j) {
-      if (!(ok = wait_w(&aux->s_full[t], j & 1, aux, p.err))) break;
+      if (!(ok = wait_w(&aux->s_full[t][j & 1], (j >> 1) & 1, aux, p.err))) break;
       ptx::tc_fence_after();
       const int lim = last - j * 128;              // columns 0..lim are visible
       uint32_t v[4][32];                           // the row's scores, as fp32 bits
@@ -293,15 +316,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the rows behind the last key belong to the next sequence: weight 0, but 0 times an
         // infinity there would be NaN, so their values become 0 (each tile clears them before it
         // hands over its weights; both store the same)
-        const int vs = p.nvs == 2 ? j & 1 : 0;
-        if (!(ok = wait_w(&aux->v_full[vs], (p.nvs == 2 ? j >> 1 : j) & 1, aux, p.err))) break;
-        if (j * 128 + row >= rk.n)
+        if (!(ok = wait_w(&aux->v_full[j & 1], (j >> 1) & 1, aux, p.err))) break;
+        if (j * 128 + row >= rk.n) {
+          const int h = row >> 6;                      // key half: a slot of its own, or half of one
+          uint8_t* vs = kv_s + ((j * unit + nkb + (nvb == 2 ? h : 0)) % p.ring) * kBox + (nvb == 2 ? 0 : h * kVBox);
           for (int c = 0; c < nvb; ++c) {
-            const uint32_t base = ptx::smem_u32(v_s + (vs * nvb + c) * kBox + row * 128);
+            const uint32_t base = ptx::smem_u32(vs + c * kVBox + (row & 63) * 128);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + e * 16), "r"(0) : "memory");
           }
+        }
         ptx::fence_proxy_async_smem();
         __syncwarp();
       }
@@ -317,9 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mn = fmaxf(m, top), a = ptx::ex2_approx(m - mn);
         m = mn;
         l *= a;
-        if (j > 0) {
-          if (!(ok = wait_w(&aux->pv_done[t], (j - 1) & 1, aux, p.err))) break;
-          ptx::tc_fence_after();
+        if (j > 0) {                               // (PV(j - 1) came before S(j), which is complete)
           for (int c = 0; c < p.dv; c += 16) {
             uint32_t o[16];
             ptx::tmem_ld16(o_col + c, o);
@@ -349,13 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&aux->p_full[t][c >> 1]);
+          if (lane == 0) ptx::mbar_arrive(&aux->p_full[t][c >> 1][j & 1]);
         }
       }
       const float2 l2 = ptx::add2(ptx::add2(sum[0], sum[1]), ptx::add2(sum[2], sum[3]));
       l += l2.x + l2.y;
     }
-    if (ok && nt[t] > 0) ok = wait_w(&aux->pv_done[t], (nt[t] - 1) & 1, aux, p.err);
+    if (ok && nt[t] > 0) ok = wait_w(&aux->pv_done[t][(nt[t] - 1) & 1], ((nt[t] - 1) >> 1) & 1, aux, p.err);
     ptx::tc_fence_after();
     if (ok) {
       const size_t o = ((size_t)rq.first + i) * p.Hq + head;
@@ -393,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-bool map2d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1) {
+bool map2d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint32_t rows = 128) {
   const cuuint64_t dims[2] = {d0, d1}, st[1] = {d0 * 2};
-  const cuuint32_t box[2] = {64, 128};
+  const cuuint32_t box[2] = {64, rows};
   return tc::make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, 2, dims, st, box);
 }
 bool map3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2) {
@@ -434,11 +457,12 @@ cudaError_t launch_shared_attn(lr_shared* c, const void* q, const void* k, const
   if (total_k == 0) k = kr = v = q;      // no key tile is ever loaded; the maps need an address
   const cuuint64_t rows = std::max(total_k, 1);
   if (!map3d(&tq, q, a.dq, a.Hq, total_q) || !map2d(&tk, k, (uint64_t)d.n_kv_heads * a.dn, rows) ||
-      !map2d(&tv, v, (uint64_t)d.n_kv_heads * a.dv, rows) || !map2d(&tkr, kr, d.dim_rope, rows))
+      !map2d(&tv, v, (uint64_t)d.n_kv_heads * a.dv, rows, 64) || !map2d(&tkr, kr, d.dim_rope, rows))
     return cudaErrorInvalidValue;
-  const int nqb = (a.dq + 63) / 64, fixed = 2 * nqb + kKStages * (a.dn / 64 + 1), nvb = a.dv / 64;   // boxes
-  a.nvs = kAuxBytes + (size_t)(fixed + 2 * nvb) * kBox <= (size_t)tc::kSmemLimit ? 2 : 1;
-  const size_t smem = kAuxBytes + (size_t)(fixed + a.nvs * nvb) * kBox;
+  // the ring: what the query tiles leave of shared memory, at most two tiles of keys and values
+  const int nqb = (a.dq + 63) / 64, unit = a.dn / 64 + 1 + a.dv / 64;
+  a.ring = std::min(2 * unit, (int)((tc::kSmemLimit - kAuxBytes) / kBox) - 2 * nqb);
+  const size_t smem = kAuxBytes + (size_t)(2 * nqb + a.ring) * kBox;
   static std::atomic<uint32_t> optin{0};
   cudaError_t e = smem_optin(k_shared_attn, optin);
   if (e != cudaSuccess) return e;
