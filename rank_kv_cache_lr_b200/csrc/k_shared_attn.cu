@@ -52,13 +52,13 @@ struct AttArgs {
 // Barriers (arrival count; who arrives -> who waits).  [2]: by the parity of the key tile, so that a
 // waiter may be one key tile behind the arriver.
 //   q_full            1 + tx   producer -> MMA
-//   k_full, v_full[2] 1 + tx   producer -> MMA (values also -> softmax, which clears the last tile's rest)
+//   k_full, v_full[2] 1 + tx   producer -> MMA (values also -> softmax, which clears what lies behind the last key)
 //   s_full[t][2]      1        MMA commit of S of tile t -> its softmax warps, producer (the keys' slots)
 //   p_full[t][h][2]   4        softmax warps (P of keys 64 h .. 64 h + 63 stored) -> MMA
-//   pv_done[t][2]     1        MMA commit of PV -> producer (the values' slots), epilogue
+//   pv_done[t][h][2]  1        MMA commit of PV of key half h -> producer (the values' slots), epilogue
 //   done              2        final commits of both MMA warps
 struct Aux {
-  uint64_t q_full, k_full[2], v_full[2], s_full[2][2], p_full[2][2][2], pv_done[2][2], done;
+  uint64_t q_full, k_full[2], v_full[2], s_full[2][2], p_full[2][2][2], pv_done[2][2][2], done;
   uint32_t tmem_base;
   int abort_flag;
   int b, pair;
@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(&aux->s_full[t][s], 1);
         ptx::mbar_init(&aux->p_full[t][0][s], 4);
         ptx::mbar_init(&aux->p_full[t][1][s], 4);
-        ptx::mbar_init(&aux->pv_done[t][s], 1);
+        ptx::mbar_init(&aux->pv_done[t][0][s], 1);
+        ptx::mbar_init(&aux->pv_done[t][1][s], 1);
       }
     }
     ptx::mbar_init(&aux->done, 2);
@@ -169,16 +170,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < nqb; ++c)
             ptx::tma_load_3d(q_s + (t * nqb + c) * kBox, &tm_q, &aux->q_full, c * 64, head, rq.first + q0 + t * 128);
         // Slots are taken and given back in one order, K0 V0 K1 V1 ..., so V_j goes where K_{j-1} was (free
-        // early: its scores are done) and K_{j+1} partly where V_{j-1} was.
+        // early: its scores are done) and K_{j+1} partly where V_{j-1} was, half by half.
         bool ok = true;
-        int at = 0, left = p.ring, ftile = 0;          // next slot, free slots, next tile to be freed
-        auto slot = [&]() -> uint8_t* {                // the next slot, once its last tile was used by both query tiles
-          while (left == 0 && ok) {
-            const int i = ftile >> 1, s = i & 1, ph = (i >> 1) & 1;
+        int at = 0, left = p.ring;                     // next slot, free slots
+        int fi = 0, fu = 0;                            // next slot to be freed: unit fu of tile fi (keys, then values)
+        auto slot = [&]() -> uint8_t* {                // the next slot, once both query tiles are done with what it held
+          if (left == 0) {
+            const int s = fi & 1, h = fu - nkb + 2 - nvb;
             for (int t = 0; t < 2 && ok; ++t)
-              if (i < nt[t]) ok = wait_b(ftile & 1 ? &aux->pv_done[t][s] : &aux->s_full[t][s], ph, aux, p.err);
-            left += ftile & 1 ? nvb : nkb;
-            ++ftile;
+              if (fi < nt[t]) ok = wait_b(h >= 0 ? &aux->pv_done[t][h][s] : &aux->s_full[t][s], (fi >> 1) & 1, aux, p.err);
+            const int run = fu == 0 ? nkb : 1;         // a key tile is free as a whole
+            left = run;
+            fu += run;
+            if (fu == unit) {
+              fu = 0;
+              ++fi;
+            }
           }
           uint8_t* const dst = kv_s + at * kBox;
           if (++at == p.ring) at = 0;
@@ -220,8 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A warp per tile: an MMA's issue waits for the tensor pipe, so whatever stands between two
       // MMAs of one warp (a barrier test costs ~130 cycles, a commit ~60, serial code ~8 an instruction
       // beside busy softmax warps) leaves the pipe idle unless the other tile's warp issues meanwhile.
-      // For the same reason a tile of keys or values has one barrier, and everything that S(j) needs
-      // is made ready before PV(j - 1)'s last wait.
+      // So what S(j) needs is made ready before PV(j - 1)'s last wait.
       const int t = warp == 10 ? 1 : 0, ntt = nt[t];
       const uint32_t ids = ptx::idesc_f16(1, 0, 0, 128, 128);                  // S: K-major x K-major
       const uint32_t idv = ptx::idesc_f16(1, 0, 1, 128, (uint32_t)p.dv);       // PV: TMEM x MN-major
@@ -243,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             kb[c] = kd + uniform((uint32_t)vp * (kBox >> 4));
             if (++vp == p.ring) vp = 0;
           }
-        bool k_in = j == ntt;
+        bool k_in = false;                             // key tile j has landed
         // PV(j - 1), in two halves of 64 keys: the first runs while the softmax works on the second
         if (j > 0) {
           const int si = s ^ 1, phi = ((j - 1) >> 1) & 1;
@@ -254,13 +260,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             ptx::mma_f16_ta_elect(d_s + 256, d_s + kk * 8, vb[0] + (uint64_t)(kk * 128), idv, kk ? 1u : more);
-          if (!k_in) k_in = __all_sync(0xffffffffu, ptx::mbar_test_wait(&aux->k_full[s], ph));
+          ptx::mma_commit_elect(&aux->pv_done[t][0][si]);
+          if (j < ntt) k_in = __all_sync(0xffffffffu, ptx::mbar_test_wait(&aux->k_full[s], ph));
           if (!(ok = wait_w(&aux->p_full[t][1][si], phi, aux, p.err))) break;
           ptx::tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             ptx::mma_f16_ta_elect(d_s + 256, d_s + 32 + kk * 8, vb[1] + (uint64_t)(kk * 128), idv, 1u);
-          ptx::mma_commit_elect(&aux->pv_done[t][si]);
+          ptx::mma_commit_elect(&aux->pv_done[t][1][si]);
         }
         if (j == ntt) break;
         // S(j): the query boxes are dn, then the rotary columns (dn and dn + 64 are box borders).
@@ -378,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 l2 = ptx::add2(ptx::add2(sum[0], sum[1]), ptx::add2(sum[2], sum[3]));
       l += l2.x + l2.y;
     }
-    if (ok && nt[t] > 0) ok = wait_w(&aux->pv_done[t][(nt[t] - 1) & 1], ((nt[t] - 1) >> 1) & 1, aux, p.err);
+    if (ok && nt[t] > 0) ok = wait_w(&aux->pv_done[t][1][(nt[t] - 1) & 1], ((nt[t] - 1) >> 1) & 1, aux, p.err);
     ptx::tc_fence_after();
     if (ok) {
       const size_t o = ((size_t)rq.first + i) * p.Hq + head;
