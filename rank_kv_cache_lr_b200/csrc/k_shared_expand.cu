@@ -89,6 +89,10 @@ __device__ __forceinline__ int span_tiles(const ExpArgs& p, int b) {
   return s.hi > s.lo ? ((s.hi + 127) >> 7) - (s.lo >> 7) : 0;
 }
 
+// A warp-uniform value, known as such to the compiler: MMA operands then stay in uniform registers
+// (an MMA issues at the tensor core's pace; without, every ~160 cycles).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // A role's place in the run: unit u is column block blk of tile k.
 struct Place {
   int u, k, blk;
@@ -183,7 +187,6 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
   const uint32_t tmem = aux->tmem_base;
   const int units = aux->units;
   Place w{0, 0, aux->blk0};
-  
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer
@@ -226,27 +229,32 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
     // ------------------------------------------------------------- MMA issuer (warp-wide)
     const uint64_t ad0 = ptx::smem_desc(ptx::smem_u32(a_s), 16, 1024, 2);
     const uint64_t bd0 = ptx::smem_desc(ptx::smem_u32(b_s), 16, 1024, 2);
-    int pos = 0, nt = 0;
+    int st = 0, nt = 0;
+    uint32_t ph = 0;
     bool ok = true;
     for (; ok && w.u < units; w.next(p.NB)) {
-      const uint32_t id = ptx::idesc_f16(1, 0, 0, 128, (uint32_t)min(256, p.W - w.blk * 256));
+      const uint32_t id = uniform(ptx::idesc_f16(1, 0, 0, 128, (uint32_t)min(256, p.W - w.blk * 256)));
       const bool fresh = w.fresh(), last = w.last(units, p.NB);
       const int u = w.u;
       if (fresh) ++nt;
-      const uint32_t d = tmem + (uint32_t)(u & 1) * 256;
+      const uint32_t d = uniform(tmem + (uint32_t)(u & 1) * 256);
       if (u >= 2 && !(ok = wait_w(&aux->d_empty[u & 1], ((u >> 1) - 1) & 1, aux, p.err))) break;
-      for (int h = 0; h < nsub; ++h, ++pos) {
-        const int st = pos % kStages;
+      for (int h = 0; h < nsub; ++h) {
         if (fresh && !(ok = wait_w(&aux->a_full[h], (nt - 1) & 1, aux, p.err))) break;
-        if (!(ok = wait_w(&aux->b_full[st], (pos / kStages) & 1, aux, p.err))) break;
+        if (!(ok = wait_w(&aux->b_full[st], ph, aux, p.err))) break;
         ptx::tc_fence_after();
-        const uint64_t ad = ad0 + (uint64_t)((h * kSub) >> 4);
-        const uint64_t bd = bd0 + (uint64_t)((st * kStage) >> 4);
+        const uint64_t ad = ad0 + uniform((uint32_t)(h * kSub) >> 4);
+        const uint64_t bd = bd0 + uniform((uint32_t)(st * kStage) >> 4);
+        const uint32_t more = uniform(h ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_f16_elect(d, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), id, (h | kk) ? 1u : 0u);
+          ptx::mma_f16_elect(d, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), id, kk ? 1u : more);
         ptx::mma_commit_elect(&aux->b_empty[st]);
         if (last) ptx::mma_commit_elect(&aux->a_empty[h]);
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
       }
       if (ok) ptx::mma_commit_elect(&aux->d_full[u & 1]);
     }
