@@ -2,58 +2,205 @@
 // stored token, without rebuilding keys or values.
 //
 //   q~_j = B_k,h q_nope,j                              k_shared_qproj   (rank space, per head)
-//   s_tj = scale (c_t . q~_j + kr_t . q_rope,j)        k_shared_decode  GEMM1, M = 128 tokens
+//   s_tj = scale (c_t . q~_j + kr_t . q_rope,j)        k_shared_decode  GEMM1, M = 64 tokens
 //   o~_j = sum_t p_tj c_t,  p = softmax over visible t k_shared_decode  GEMM2, M = 128 ranks
 //   out_j = o~_j B_v,h / l_j                           k_shared_out     (merges the splits)
 //
-// One 128-token tile of latents in shared memory serves as keys (rows of GEMM1's A operand,
-// K-major) and, through a second descriptor of the same bytes, as values (GEMM2's A operand,
-// MN-major): each stored byte crosses HBM once per step.  Heads are the N side of both MMAs, so
-// a block of NR = 16 or 32 query rows pays for no empty rows of a 128-row operand.
+// One tile of latents in shared memory serves as keys (rows of GEMM1's A operand, K-major) and,
+// through a second descriptor of the same bytes, as values (GEMM2's A operand, MN-major): each
+// stored byte crosses HBM once per block of query rows.  Heads are the N side of both MMAs, so a
+// block of NR = 16 or 32 query rows pays for no empty rows of a 128-row operand.
 //
-// Roundings: q~ enters GEMM1 as two bf16 halves, hi and lo = q~ - hi, stacked on N (the
-// A operand's shared-memory reads set the pace for N <= 64, so the second half is nearly
-// free) and added in fp32: the scores, and so lse, carry ~16 bits of q~.  The rotary query is
-// bf16 as given.  p enters GEMM2 as one bf16 (2^-8 relative at most, at random over the tokens,
-// below the output's own rounding); its sum, for lse and the normaliser, is of the unrounded
-// weights in fp32.
+// Tiles are 64 tokens, half a page: beside the query latents (64 KB at r = 512) two such tiles
+// fit, so one is fetched while the other is at work.  With 128-token tiles only one fits, and its
+// fetch, scores, softmax and value mix follow one another (4.1 us a tile of bf16, 6.2 us of 8
+// bits, against 1.9 us of copies); splitting the rank over two CTAs instead costs two exchanges a
+// tile and came out the same.  A GEMM1 step of 64 x 64 takes 33 clocks (128 x 64: 48), so smaller
+// tiles cost the tensor pipe 1.4 times the time per token, ~1800 clocks a tile at r = 512, still
+// below the 3300 that a bf16 tile takes from HBM.
 //
-// Work: the 128-token tiles of all sequences, in order, are cut into equal runs on the device
-// (tile_run), one run per CTA column, so ragged batches stay balanced and a captured graph
-// serves any lengths.  A run's part of one sequence is one partial (m, l, o~), joined by
-// k_shared_out.
-#include "shared_decode.cuh"
+// Roundings: q~ enters GEMM1 as two bf16 halves, hi and lo = q~ - hi, stacked on N and added in
+// fp32: the scores, and so lse, carry ~16 bits of q~.  The rotary query is bf16 as given.  p enters
+// GEMM2 as one bf16 (2^-8 relative at most, at random over the tokens, below the output's own
+// rounding); its sum, for lse and the normaliser, is of the unrounded weights in fp32.
+//
+// Work: the tiles of all sequences, in order, are cut into equal runs on the device (tile_run),
+// one run per CTA column, so ragged batches stay balanced and a captured graph serves any
+// lengths.  A run's part of one sequence is one partial (m, l, o~), joined by k_shared_out.
+#include "shared_internal.cuh"
+#include "tc_common.cuh"
 
 #include <algorithm>
 
 namespace {
 
-constexpr int kSCol = 0;               // TMEM: S of tile t in columns [64 (t % 2), + 2 NR)
-constexpr int kOCol = 128;             // TMEM: O~ of 128-rank chunk c in columns [128 + c NR, + NR)
+using tc::drain_wait;
+using tc::kLazy;
+using tc::kSmemLimit;
 
-// Barriers (arrival count; who arrives -> who waits); phase k is waited with parity k & 1.
-//   raw_full[s]     1 + tx   8 bits: producer's codes and scales -> expansion warps
-//   slot_full[s]    1 + tx / 8   producer's boxes (bf16) or the expansion warps -> MMA issuer
-//   slot_empty[s]   1        MMA commit of GEMM2 -> producer
-//   rope_full       1 + tx   producer -> MMA issuer
-//   rope_empty      1        MMA commit of GEMM1 -> producer
+constexpr int kTok = 64;               // tokens of a tile
+constexpr int kSub = kTok * 128;       // 64 tokens x 64 ranks x 2 B (one TMA box)
+constexpr int kWSub = 128 * 128;       // 128 rows x 64 columns x 2 B (the projections' operands)
+constexpr int kScaleBytes = kTok * 4;  // 8 bits: exponent bytes of 64 tokens x 4 groups, per 128 ranks
+constexpr int kAuxBytes = 2048;
+constexpr int kMaxSlots = 4;
+constexpr float kNoMax = -1e30f;       // running max before any visible token (finite: no inf - inf)
+constexpr int kSCol = 0;               // TMEM: S of tile t in columns [64 (t % 2), + 2 NR)
+constexpr int kOCol = 128;             // TMEM: O~ of 128-rank block k in columns [128 + k NR, + NR)
+
+struct DecArgs {
+  unsigned long long wait_ns;
+  const int32_t* row_len;
+  RowMap map;
+  int B, cap, r, Hq, n_tok, R, HB, X, nslot;
+  float scale_log2;
+  const uint8_t* codes;
+  const uint8_t* scale;
+  float* part_o;
+  float* part_ml;
+  int* err;
+};
+
+// The next sequence part of a run: false at its end.  Every role walks its own copy.
+struct Seg {
+  int b, t0, nt, len;
+};
+__device__ __forceinline__ bool next_seg(TileRun* run, const DecArgs& p, Seg* s) {
+  while (run->left > 0 && run->b < p.B) {
+    const int len = shared_len(p.row_len, run->b, p.cap);
+    const int nt = (len + kTok - 1) / kTok - run->tile;
+    if (nt <= 0) {
+      ++run->b;
+      run->tile = 0;
+      continue;
+    }
+    s->b = run->b;
+    s->t0 = run->tile;
+    s->nt = min(nt, run->left);
+    s->len = len;
+    run->left -= s->nt;
+    ++run->b;
+    run->tile = 0;
+    return true;
+  }
+  return false;
+}
+
+// Two e4m3 codes as bf16 before their scale: a code's sign, exponent and mantissa bits placed in
+// a bf16 stand for its value times 2^-120 (subnormals included).  sel picks bytes (i, j) as
+// halves with the sign replicated above each (selector bit 3).
+template <uint32_t kSel>
+__device__ __forceinline__ __nv_bfloat162 place2(uint32_t w) {
+  uint32_t a;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(a) : "r"(w), "n"(kSel));
+  a = (a << 4) & 0x87F087F0u;
+  return *reinterpret_cast<const __nv_bfloat162*>(&a);
+}
+// Sixteen codes of one token (their words in the order in which they are stored), times 2^e, to
+// two 16-byte columns of a swizzled row: w.x, w.y to address a0 and w.z, w.w to a1.  e <= 7
+// (exponent byte at most 134): 2^(120 + e) is a bf16, so one exact product; kTwo: two products.
+template <bool kTwo>
+__device__ __forceinline__ void expand16(const uint4& w, uint32_t eb, uint32_t a0, uint32_t a1) {
+  // 2^e = 2^(b1 - 127) 2^(b2 - 127) with 120 folded into the first; byte 255 (a group that held a
+  // NaN or an infinity) is NaN
+  const uint32_t b1 = kTwo ? min(eb + 120u, 254u) : eb + 120u;
+  const uint32_t h1 = kTwo && eb == 255u ? 0x7FC07FC0u : b1 * 0x00800080u;
+  const uint32_t h2 = (eb + 247u - b1) * 0x00800080u;
+  const __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162*>(&h1);
+  const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&h2);
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    __nv_bfloat162 x = __hmul2(place2<0x9180>(in[k]), s1), y = __hmul2(place2<0xB3A2>(in[k]), s1);
+    if (kTwo) {
+      x = __hmul2(x, s2);
+      y = __hmul2(y, s2);
+    }
+    o[2 * k] = *reinterpret_cast<const uint32_t*>(&x);
+    o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+               : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+               : "memory");
+}
+// A warp-uniform value, known as such to the compiler: MMA operands then stay in uniform registers
+// (an MMA issues at the tensor core's pace; without, every ~160 cycles).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Expand one 128-rank chunk of a tile by 128 threads (tid): codes in the second of the chunk's two
+// boxes at `dst`, exponent bytes `sc` [64][4], to bf16 boxes; `full`: 128 ranks (else 64); token
+// rows at `valid` and beyond, which hold whatever the page held, become 0.
+__device__ __forceinline__ void expand_chunk(uint8_t* dst, const uint8_t* sc, int tid, bool full, int valid) {
+  // 16 codes a thread and step: 8 (a last chunk of 64 ranks: 4) threads per token row
+  const int sh = full ? 3 : 2, steps = full ? 4 : 2;
+  const int col = tid & ((1 << sh) - 1), tok0 = tid >> sh, dtok = 128 >> sh;
+  uint4 w[4];
+  uint32_t eb[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    eb[k] = 127u;
+    if (k < steps) {
+      w[k] = reinterpret_cast<const uint4*>(dst + kSub)[k * 128 + tid];
+      eb[k] = sc[(k * dtok + tok0) * 4 + (col >> 1)];
+    }
+  }
+  // A whole chunk's codes of a token lie where its second box row goes, and a warp holds
+  // whole tokens: once its lanes have read, it may write.
+  __syncwarp();
+  // 128-byte swizzle: 16-byte column v of row tok sits at v ^ (tok % 8), and tok % 8 is
+  // the same in every step; the lanes of the second box take their two columns in the
+  // other order, so that the eight lanes of a row store to eight different columns
+  const bool swap = col >= 4;
+  const uint32_t base = ptx::smem_u32(dst + (col >> 2) * kSub + tok0 * 128);
+  const uint32_t a0 = base + ((((col & 3) * 2 + swap) ^ (tok0 & 7)) << 4);
+  const uint32_t a1 = base + ((((col & 3) * 2 + !swap) ^ (tok0 & 7)) << 4);
+  const bool two = __any_sync(0xffffffffu, max(max(eb[0], eb[1]), max(eb[2], eb[3])) > 134u);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < steps) {
+      const uint32_t off = k * dtok * 128;
+      uint4 x = w[k];
+      if (swap) x = make_uint4(w[k].z, w[k].w, w[k].x, w[k].y);
+      if (two) expand16<true>(x, eb[k], a0 + off, a1 + off);
+      else expand16<false>(x, eb[k], a0 + off, a1 + off);
+    }
+  if (valid < kTok) {
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < steps && k * dtok + tok0 >= valid) {
+        const uint32_t off = k * dtok * 128;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a0 + off), "r"(0) : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a1 + off), "r"(0) : "memory");
+      }
+  }
+}
+
+// Barriers (arrival count; who arrives -> who waits); phase k is waited with parity k & 1.  NG =
+// NR / 16 groups of four softmax warps.
+//   raw_full[s]     1 + tx   8 bits: producer's codes, scales and rotary keys -> expansion warps
+//   full[s]         1 + tx (8 bits: 8)   producer's boxes (expansion warps) -> GEMM1 issuer
+//   empty[s]        1        GEMM2's commit -> producer
 //   q_full/q_empty  1 + tx / 1   per sequence of the run
-//   s_full[2]       1        MMA commit of GEMM1 -> softmax warps
-//   s_empty[2]      NR / 2   softmax warps (scores read) -> MMA issuer
-//   p_full          NR / 2   softmax warps -> MMA issuer
-//   p_empty         1        MMA commit of GEMM2 -> softmax warps
-//   o_full          1        MMA commit, last tile of a sequence -> softmax warps
-//   o_empty         NR / 2   softmax warps (O~ read) -> MMA issuer
-//   done            1        final commit: every MMA complete before TMEM is freed
+//   s_full[2]       1        GEMM1's commit -> softmax warps
+//   s_empty[2]      4 NG     softmax warps (scores read) -> GEMM1 issuer
+//   p_full[2]       4 NG     softmax warps -> GEMM2 issuer
+//   p_empty[2]      1        GEMM2's commit -> softmax warps (P may be rewritten, O~ rescaled)
+//   o_full          1        GEMM2's commit, last tile of a sequence -> softmax warps
+//   o_empty         4 NG     softmax warps (O~ read) -> GEMM2 issuer
+//   done            2        final commits of both issuers: every MMA complete before TMEM is freed
 struct Aux {
-  uint64_t raw_full[kMaxSlots], slot_full[kMaxSlots], slot_empty[kMaxSlots];
-  uint64_t rope_full, rope_empty, q_full, q_empty, s_full[2], s_empty[2], p_full, p_empty, o_full, o_empty, done;
+  uint64_t raw_full[kMaxSlots], full[kMaxSlots], empty[kMaxSlots];
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], p_empty[2], o_full, o_empty, done;
   uint32_t tmem_base;
   int abort_flag;
   unsigned long long wait_ns;
   TileRun run;
-  float red[4][4][8];          // [column group][lane quarter][column]
-  int off_s[32];               // row j sees tokens t < len + off_s[j]
+  float red[2][4][16];               // [group][lane quarter][row]
+  alignas(16) float alpha[2][16];    // [group][row]: factors of a rescale
+  int off_s[32];                     // row j sees tokens t < len + off_s[j]
 };
 static_assert(sizeof(Aux) <= kAuxBytes, "aux block");
 
@@ -64,16 +211,45 @@ __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, Aux* aux,
   return __all_sync(0xffffffffu, wait_b(bar, parity, aux, err));
 }
 
-// Shared memory: [aux][q~: r/64 blocks of (2 NR rows hi | lo) x 128 B][q_rope: NR rows x 128 B]
-// [P: 128 tokens x NR][slots][rotary tile][8 bits: scales per slot].
-// Warps: 0 TMA producer, 1 MMA issuer, then NR / 2 softmax warps (thread = token row = TMEM lane
-// of one group of 8 query rows; four warps a group; in the epilogue thread = rank row), then
-// (8 bits) 8 warps that expand codes to bf16.  One warp per lane quarter for all 32 columns had
-// taken ~4 us a tile: a single warp per scheduler cannot hide its own latencies.
+// A use count of a ring: slot and phase parity, without divisions.
+struct Ring {
+  int slot = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Sum or maximum over the lanes that share lane % 4 (the same score columns).
+template <bool kMax>
+__device__ __forceinline__ float reduce_rows(float v) {
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, v, o);
+    v = kMax ? fmaxf(v, got) : v + got;
+  }
+  return v;
+}
+
+// Warps: 0 TMA producer, 1 GEMM1 issuer, 2 GEMM2 issuer (a warp each: what stands between two MMAs
+// of one warp, a barrier test or a commit, would leave the tensor pipe idle), 3 idle; then NG groups
+// of four softmax warps, 16 query rows each; (8 bits) 8 warps that expand codes to bf16.
 template <int NR, bool kQuant>
 constexpr int dec_threads() {
-  return 64 + NR * 16 + (kQuant ? 256 : 0);
+  return 128 + NR * 8 + (kQuant ? 256 : 0);
 }
+__host__ __device__ constexpr int dec_boxes(int r, bool quant) {   // of a tile, its rotary box last
+  return (quant ? (r + 127) / 128 * 2 : r / 64) + 1;
+}
+__host__ __device__ constexpr int dec_slot(int r, bool quant) {
+  return dec_boxes(r, quant) * kSub + (quant ? ((r + 127) / 128 * kScaleBytes + 1023) & ~1023 : 0);
+}
+
+// Shared memory: [aux][q~: r/64 blocks of (2 NR rows hi | lo) x 128 B][q_rope: NR rows x 128 B]
+// [P: 2 x 64 tokens x NR][slots: boxes, 8 bits: scales].
 template <int NR, bool kQuant>
 __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     k_shared_decode(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
@@ -84,16 +260,14 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     if (threadIdx.x == 0) atomicExch(p.err, (int)LR_ERR_UNSUPPORTED);
     return;
   }
-  constexpr int kQSub = 2 * NR * 128;
-  constexpr int kPBytes = 128 * NR * 2;
-  const int nsub = p.r >> 6;
+  constexpr int NG = NR / 16, kQSub = 2 * NR * 128, kPBuf = kTok * NR * 2;
+  const int nsub = p.r >> 6, nch = (p.r + 127) >> 7;
+  const int rope_box = dec_boxes(p.r, kQuant) - 1, slot_bytes = dec_slot(p.r, kQuant);
   Aux* aux = reinterpret_cast<Aux*>(smem_raw);
   uint8_t* q_s = smem_raw + kAuxBytes;
   uint8_t* qr_s = q_s + nsub * kQSub;
   uint8_t* p_s = qr_s + NR * 128;
-  uint8_t* ring = smem_raw + kAuxBytes + ((nsub * kQSub + NR * 128 + kPBytes + 1023) & ~1023);
-  uint8_t* rope_s = ring + p.nslot * kSlot;
-  uint8_t* sc_s = rope_s + kSub;
+  uint8_t* ring = p_s + 2 * kPBuf;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int x = blockIdx.x, hb = blockIdx.y;
@@ -101,28 +275,28 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nslot; ++s) {
       ptx::mbar_init(&aux->raw_full[s], 1);
-      ptx::mbar_init(&aux->slot_full[s], kQuant ? 8 : 1);
-      ptx::mbar_init(&aux->slot_empty[s], 1);
+      ptx::mbar_init(&aux->full[s], kQuant ? 8 : 1);
+      ptx::mbar_init(&aux->empty[s], 1);
     }
-    ptx::mbar_init(&aux->rope_full, 1);
-    ptx::mbar_init(&aux->rope_empty, 1);
     ptx::mbar_init(&aux->q_full, 1);
     ptx::mbar_init(&aux->q_empty, 1);
     for (int k = 0; k < 2; ++k) {
       ptx::mbar_init(&aux->s_full[k], 1);
-      ptx::mbar_init(&aux->s_empty[k], NR / 2);
+      ptx::mbar_init(&aux->s_empty[k], 4 * NG);
+      ptx::mbar_init(&aux->p_full[k], 4 * NG);
+      ptx::mbar_init(&aux->p_empty[k], 1);
     }
-    ptx::mbar_init(&aux->p_full, NR / 2);
-    ptx::mbar_init(&aux->p_empty, 1);
     ptx::mbar_init(&aux->o_full, 1);
-    ptx::mbar_init(&aux->o_empty, NR / 2);
-    ptx::mbar_init(&aux->done, 1);
+    ptx::mbar_init(&aux->o_empty, 4 * NG);
+    ptx::mbar_init(&aux->done, 2);
     aux->abort_flag = 0;
     aux->wait_ns = tc::wait_limit(p.wait_ns);
     ptx::fence_mbar_init();
   }
-  if (threadIdx.x >= 64 && threadIdx.x < 96)   // query row j of this block belongs to token (hb NR + j) / Hq
-    aux->off_s[lane] = min((hb * NR + lane) / p.Hq, p.n_tok - 1) - (p.n_tok - 1);
+  if (threadIdx.x >= 96 && threadIdx.x < 96 + NR) {   // query row j of this block belongs to token (hb NR + j) / Hq
+    const int j = threadIdx.x - 96;
+    aux->off_s[j] = min((hb * NR + j) / p.Hq, p.n_tok - 1) - (p.n_tok - 1);
+  }
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&tm_q);
     ptx::prefetch_tmap(&tm_qr);
@@ -130,14 +304,15 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     ptx::prefetch_tmap(&tm_kr);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&aux->tmem_base, 512);
+    ptx::tmem_alloc(&aux->tmem_base, 256);
     ptx::tmem_relinquish();
   }
   pdl_wait();       // lengths, pages, rows and q~ may come from the work just before
   pdl_trigger();
   if (warp == 0) {
     int chunk;
-    const TileRun run = tile_run([&](int b) { return (shared_len(p.row_len, b, p.cap) + 127) >> 7; }, p.B, p.X, x, &chunk);
+    const TileRun run = tile_run([&](int b) { return (shared_len(p.row_len, b, p.cap) + kTok - 1) / kTok; }, p.B,
+                                 p.X, x, &chunk);
     if (lane == 0) aux->run = run;
   }
   ptx::tc_fence_before();
@@ -150,266 +325,271 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer
     if (lane == 0) {
-      int gt = 0, pos = 0, nseg = 0;     // tiles, slot uses and sequences issued
+      int gt = 0, nseg = 0;              // tiles and sequences issued
+      Ring w;
       bool ok = true;
       while (ok && next_seg(&run, p, &sg)) {
-        if (nseg > 0 && !(ok = wait_b(&aux->q_empty, (nseg - 1) & 1, aux, p.err))) break;
-        ptx::mbar_arrive_expect_tx(&aux->q_full, (uint32_t)(nsub * kQSub + NR * 128));
-        for (int s = 0; s < nsub; ++s)
-          ptx::tma_load_2d(q_s + s * kQSub, &tm_q, &aux->q_full, s * 64, (sg.b * p.HB + hb) * 2 * NR);
-        ptx::tma_load_3d(qr_s, &tm_qr, &aux->q_full, 0, hb * NR, sg.b);
-        ++nseg;
-        int next_page = p.map.page(sg.b, sg.t0 * 128);
-        for (int i = 0; i < sg.nt && ok; ++i, ++gt) {
-          const int page = next_page;
-          // the table is read one tile ahead, so that its latency is not between two copies
-          if (i + 1 < sg.nt) next_page = p.map.page(sg.b, (sg.t0 + i + 1) * 128);
-          for (int c = 0; c < p.nch; ++c) {
-            const int slot = pos % p.nslot, round = pos / p.nslot;
-            if (round > 0 && !(ok = wait_b(&aux->slot_empty[slot], (round - 1) & 1, aux, p.err))) break;
-            uint8_t* dst = ring + slot * kSlot;
-            if (kQuant) {
-              // codes into the upper half of their slot, where the expansion reads them before
-              // it writes
-              const uint32_t bytes = c * 128 + 64 < p.r ? kSub : kSub / 2;
-              ptx::mbar_arrive_expect_tx(&aux->raw_full[slot], bytes + kScaleBytes);
-              ptx::bulk_load(dst + kSub, p.codes + (long long)page * 128 * p.r + c * kSub, bytes, &aux->raw_full[slot]);
-              ptx::bulk_load(sc_s + slot * kScaleBytes, p.scale + ((long long)page * p.nch + c) * kScaleBytes,
-                             kScaleBytes, &aux->raw_full[slot]);
-            } else {
-              const int nb = c * 128 + 64 < p.r ? 2 : 1;
-              ptx::mbar_arrive_expect_tx(&aux->slot_full[slot], nb * kSub);
-              for (int s = 0; s < nb; ++s)
-                ptx::tma_load_2d(dst + s * kSub, &tm_c, &aux->slot_full[slot], c * 128 + s * 64, page * 128);
+        for (int i = 0; i < sg.nt; ++i) {
+          const int tok = (sg.t0 + i) * kTok, half = tok & 64;
+          const long long page = p.map.page(sg.b, tok);
+          if (gt >= p.nslot && !(ok = wait_b(&aux->empty[w.slot], w.ph ^ 1, aux, p.err))) break;
+          uint8_t* dst = ring + w.slot * slot_bytes;
+          const int row = (int)page * 128 + half;
+          uint64_t* load = kQuant ? &aux->raw_full[w.slot] : &aux->full[w.slot];
+          if (kQuant) {
+            ptx::mbar_arrive_expect_tx(load, (uint32_t)(nsub * (kSub / 2) + nch * kScaleBytes + kSub));
+            for (int c = 0; c < nch; ++c) {
+              const int width = min(128, p.r - c * 128);       // bytes of a token's codes
+              ptx::bulk_load(dst + (2 * c + 1) * kSub, p.codes + page * 128 * p.r + c * 16384 + half * width,
+                             (uint32_t)(kTok * width), load);
+              ptx::bulk_load(dst + (rope_box + 1) * kSub + c * kScaleBytes,
+                             p.scale + (page * nch + c) * 512 + half * 4, kScaleBytes, load);
             }
-            ++pos;
+          } else {
+            ptx::mbar_arrive_expect_tx(load, (uint32_t)((nsub + 1) * kSub));
+            for (int s = 0; s < nsub; ++s) ptx::tma_load_2d(dst + s * kSub, &tm_c, load, s * 64, row);
           }
-          if (!ok) break;
-          if (gt > 0 && !(ok = wait_b(&aux->rope_empty, (gt - 1) & 1, aux, p.err))) break;
-          ptx::mbar_arrive_expect_tx(&aux->rope_full, kSub);
-          ptx::tma_load_2d(rope_s, &tm_kr, &aux->rope_full, 0, page * 128);
+          ptx::tma_load_2d(dst + rope_box * kSub, &tm_kr, load, 0, row);
+          ++gt;
+          w.next(p.nslot);
+          if (i > 0) continue;
+          // the query latents, behind the first tile: it has further to come
+          if (nseg > 0 && !(ok = wait_b(&aux->q_empty, (nseg - 1) & 1, aux, p.err))) break;
+          ptx::mbar_arrive_expect_tx(&aux->q_full, (uint32_t)(nsub * kQSub + NR * 128));
+          for (int s = 0; s < nsub; ++s)
+            ptx::tma_load_2d(q_s + s * kQSub, &tm_q, &aux->q_full, s * 64, (sg.b * p.HB + hb) * 2 * NR);
+          ptx::tma_load_3d(qr_s, &tm_qr, &aux->q_full, 0, hb * NR, sg.b);
+          ++nseg;
         }
       }
       // every copy this thread issued has landed before the CTA can exit
       if (nseg > 0) drain_wait(&aux->q_full, (nseg - 1) & 1);
-      for (int k = max(0, pos - p.nslot); k < pos; ++k)
-        drain_wait(kQuant ? &aux->raw_full[k % p.nslot] : &aux->slot_full[k % p.nslot], (k / p.nslot) & 1);
-      if (gt > 0) drain_wait(&aux->rope_full, (gt - 1) & 1);   // gt: tiles whose rotary part was issued
+      for (int k = min(gt, p.nslot); k > 0; --k) {
+        if (w.slot == 0) w.ph ^= 1;
+        w.slot = w.slot ? w.slot - 1 : p.nslot - 1;
+        drain_wait(kQuant ? &aux->raw_full[w.slot] : &aux->full[w.slot], w.ph);
+      }
     }
+    __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------- MMA issuer (warp-wide)
-    const uint32_t id1 = ptx::idesc_f16(1, 0, 0, 128, 2 * NR);   // GEMM1: K-major x K-major (hi | lo)
-    const uint32_t idr = ptx::idesc_f16(1, 0, 0, 128, NR);       //        rotary part, into the hi columns
-    const uint32_t id2 = ptx::idesc_f16(1, 1, 1, 128, NR);       // GEMM2: MN-major x MN-major
-    // Operands go through `uniform`: the compiler then keeps them in uniform registers, and an
-    // MMA issues every ~40 cycles (the pace of an operand read from shared memory) and not ~115.
+    // ------------------------------------------------------------- GEMM1 issuer (warp-wide)
+    const uint32_t id1 = ptx::idesc_f16(1, 0, 0, kTok, 2 * NR);  // K-major x K-major (hi | lo)
+    const uint32_t idr = ptx::idesc_f16(1, 0, 0, kTok, NR);      // rotary part, into the hi columns
     const uint64_t kd0 = ptx::smem_desc(ptx::smem_u32(ring), 16, 1024, 2);
-    const uint64_t vd0 = ptx::smem_desc(ptx::smem_u32(ring), kSub, 1024, 2);
-    const uint64_t qd0 = ptx::smem_desc(ptx::smem_u32(q_s), 16, 1024, 2);
-    const uint64_t rd0 = ptx::smem_desc(ptx::smem_u32(rope_s), 16, 1024, 2);
-    const uint64_t qrd0 = ptx::smem_desc(ptx::smem_u32(qr_s), 16, 1024, 2);
-    const uint64_t pd0 = ptx::smem_desc(ptx::smem_u32(p_s), 128, 2048, 0);
-    int gt0 = 0, nseg = 0;
+    const uint64_t qd = ptx::smem_desc(ptx::smem_u32(q_s), 16, 1024, 2);
+    const uint64_t qrd = ptx::smem_desc(ptx::smem_u32(qr_s), 16, 1024, 2);
+    int gt = 0, nseg = 0;
+    Ring w;
     bool ok = true;
-    // With slots for two tiles the scores of tile i + 1 go before the value mix of tile i, and
-    // so run during its softmax; a tile's slots are held until its value mix.
-    const bool ahead = p.nslot >= 2 * p.nch;
     while (ok && next_seg(&run, p, &sg)) {
       if (!(ok = wait_w(&aux->q_full, nseg & 1, aux, p.err))) break;
-      ptx::tc_fence_after();
-      for (int u = 0; u < 2 * sg.nt && ok; ++u) {
-        int i = u >> 1;
-        bool isv = u & 1;
-        if (ahead) tc::unit_of(u, sg.nt, &i, &isv);
-        const int gt = gt0 + i;
-        if (!isv) {
-          const int sb = gt & 1;
-          if (gt >= 2 && !(ok = wait_w(&aux->s_empty[sb], ((gt - 2) >> 1) & 1, aux, p.err))) break;
-          ptx::tc_fence_after();
-          const uint32_t d_s = uniform(tmem + kSCol + 64 * sb);
-          for (int c = 0; c < p.nch; ++c) {
-            const int pos = gt * p.nch + c, slot = pos % p.nslot;
-            if (!(ok = wait_w(&aux->slot_full[slot], (pos / p.nslot) & 1, aux, p.err))) break;
-            ptx::tc_fence_after();
-            const uint64_t a0 = kd0 + uniform((slot * kSlot) >> 4);
-            const uint64_t b0 = qd0 + uniform((c * 2 * kQSub) >> 4);
-            const uint32_t first = uniform(c ? 1u : 0u);
+      for (int i = 0; i < sg.nt; ++i, ++gt, w.next(p.nslot)) {
+        const uint64_t kd = kd0 + uniform((uint32_t)(w.slot * slot_bytes) >> 4);
+        const uint64_t rd = kd + uniform((uint32_t)(rope_box * kSub) >> 4);
+        const uint32_t d_s = uniform(tmem + kSCol + 64 * (gt & 1));
+        if (gt >= 2 && !(ok = wait_w(&aux->s_empty[gt & 1], ((gt >> 1) - 1) & 1, aux, p.err))) break;
+        if (!(ok = wait_w(&aux->full[w.slot], w.ph, aux, p.err))) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < nsub) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              ptx::mma_f16_elect(d_s, a0 + (uint64_t)(kk * 2), b0 + (uint64_t)(kk * 2), id1, kk ? 1u : first);
-            if (c * 128 + 64 < p.r) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                ptx::mma_f16_elect(d_s, a0 + (uint64_t)((kSub >> 4) + kk * 2), b0 + (uint64_t)((kQSub >> 4) + kk * 2),
-                                   id1, 1u);
-            }
+              ptx::mma_f16_elect(d_s, kd + (uint64_t)((s * kSub >> 4) + kk * 2), qd + (uint64_t)((s * kQSub >> 4) + kk * 2),
+                                 id1, s + kk ? 1u : 0u);
           }
-          if (!ok || !(ok = wait_w(&aux->rope_full, gt & 1, aux, p.err))) break;
-          ptx::tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)       // columns past dim_rope are 0 on both sides
-            ptx::mma_f16_elect(d_s, rd0 + (uint64_t)(kk * 2), qrd0 + (uint64_t)(kk * 2), idr, 1u);
-          ptx::mma_commit_elect(&aux->rope_empty);
-          if (i == sg.nt - 1) ptx::mma_commit_elect(&aux->q_empty);
-          ptx::mma_commit_elect(&aux->s_full[sb]);
-        } else {
-          if (!(ok = wait_w(&aux->p_full, gt & 1, aux, p.err))) break;
-          if (i == 0 && nseg > 0 && !(ok = wait_w(&aux->o_empty, (nseg - 1) & 1, aux, p.err))) break;
-          ptx::tc_fence_after();
-          const uint32_t first = uniform(i ? 1u : 0u);
-          for (int c = 0; c < p.nch; ++c) {
-            const int slot = (gt * p.nch + c) % p.nslot;
-            const uint64_t a0 = vd0 + uniform((slot * kSlot) >> 4);
-            const uint32_t d_o = uniform(tmem + kOCol + c * NR);
-#pragma unroll
-            for (int kt = 0; kt < 8; ++kt)
-              ptx::mma_f16_elect(d_o, a0 + (uint64_t)(kt * 128), pd0 + (uint64_t)(kt * 16), id2, kt ? 1u : first);
-            ptx::mma_commit_elect(&aux->slot_empty[slot]);
-          }
-          ptx::mma_commit_elect(&aux->p_empty);
-          if (i == sg.nt - 1) ptx::mma_commit_elect(&aux->o_full);
-        }
+        for (int kk = 0; kk < 4; ++kk)       // columns past dim_rope are 0 on both sides
+          ptx::mma_f16_elect(d_s, rd + (uint64_t)(kk * 2), qrd + (uint64_t)(kk * 2), idr, 1u);
+        ptx::mma_commit_elect(&aux->s_full[gt & 1]);
+        if (i == sg.nt - 1) ptx::mma_commit_elect(&aux->q_empty);
       }
-      gt0 += sg.nt;
       ++nseg;
     }
     ptx::mma_commit_elect(&aux->done);
     drain_wait(&aux->done, 0);
     __syncwarp();
-  } else if (warp < 2 + NR / 2) {
-    // ------------------------------------------------------------- softmax / epilogue
-    const int qd = warp & 3, g = (warp - 2) >> 2;        // lane quarter, column group
-    const int row = qd * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
-    const int bar = 1 + g;                               // the group's four warps
+  } else if (warp == 2) {
+    // ------------------------------------------------------------- GEMM2 issuer (warp-wide)
+    const uint32_t id2 = ptx::idesc_f16(1, 1, 1, 128, NR);       // MN-major x MN-major
+    const uint64_t vd0 = ptx::smem_desc(ptx::smem_u32(ring), kSub, 1024, 2);
+    const uint64_t pd0 = ptx::smem_desc(ptx::smem_u32(p_s), 128, 1024, 0);
     int gt = 0, nseg = 0;
+    Ring w;
     bool ok = true;
     while (ok && next_seg(&run, p, &sg)) {
-      float m[8], l[8];                                  // in units of log2; alike in the whole group
+      for (int i = 0; i < sg.nt; ++i, ++gt, w.next(p.nslot)) {
+        const uint64_t vd = vd0 + uniform((uint32_t)(w.slot * slot_bytes) >> 4);
+        const uint64_t pd = pd0 + uniform((uint32_t)((gt & 1) * kPBuf) >> 4);
+        const uint32_t first = uniform(i ? 1u : 0u), d_o = uniform(tmem + kOCol);
+        if (i == 0 && nseg > 0 && !(ok = wait_w(&aux->o_empty, (nseg - 1) & 1, aux, p.err))) break;
+        if (!(ok = wait_w(&aux->p_full[gt & 1], (gt >> 1) & 1, aux, p.err))) break;
+        ptx::tc_fence_after();
+        // a last block of 64 ranks mixes the box behind it into rows that nobody reads
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = kNoMax;
-        l[j] = 0.f;
+        for (int c = 0; c < 4; ++c)
+          if (c < nch) {
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+              ptx::mma_f16_elect(d_o + c * NR, vd + (uint64_t)((2 * c * kSub >> 4) + kt * 128), pd + (uint64_t)(kt * 16),
+                                 id2, kt ? 1u : first);
+          }
+        ptx::mma_commit_elect(&aux->empty[w.slot]);
+        ptx::mma_commit_elect(&aux->p_empty[gt & 1]);
+        if (i == sg.nt - 1) ptx::mma_commit_elect(&aux->o_full);
       }
-      for (int i = 0; i < sg.nt; ++i, ++gt) {
-        const int k2 = gt & 1;
-        const int t = (sg.t0 + i) * 128 + row;
-        const uint32_t s_col = tmem + lane_off + kSCol + 64 * k2 + 8 * g;
-        // after an abort every wait returns at once: the group's warps finish the sequence in step
-        // (their barriers stay matched) and leave at the verdict below
+      ++nseg;
+    }
+    ptx::mma_commit_elect(&aux->done);
+    drain_wait(&aux->done, 0);
+    __syncwarp();
+  } else if (warp >= 4 && warp < 4 + 4 * NG) {
+    // ------------------------------------------------------------- softmax / epilogue
+    // Scores of 64 tokens stand in lanes 0..15 of each lane quarter; the fragment load spreads 16
+    // lanes x 16 columns over the warp: lane l has tokens l / 4 and l / 4 + 8 of the quarter's 16,
+    // columns 2 (l % 4), + 1, and the same + 8.
+    const int qd = warp & 3, g = (warp - 4) >> 2;        // lane quarter, group of 16 query rows
+    const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+    const int tok0 = qd * 16 + (lane >> 2), col0 = 16 * g + 2 * (lane & 3);
+    const uint32_t p_at = ptx::smem_u32(p_s + 2 * g * (kTok * 16) + tok0 * 16 + (lane & 3) * 4);
+    int off[4];                                          // visibility of the thread's columns
+#pragma unroll
+    for (int k = 0; k < 4; ++k) off[k] = aux->off_s[col0 + 8 * (k >> 1) + (k & 1)];
+    int gt = 0, nseg = 0;
+    Ring w;
+    bool ok = true;
+    while (ok && next_seg(&run, p, &sg)) {
+      float m[4], l[4];                                  // of the columns; m in units of log2, alike in the whole group
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[k] = kNoMax;
+        l[k] = 0.f;
+      }
+      for (int i = 0; i < sg.nt; ++i, ++gt, w.next(p.nslot)) {
+        const int k2 = gt & 1, t = (sg.t0 + i) * kTok + tok0;
+        const uint32_t s_col = tmem + lane_off + kSCol + 64 * k2 + 16 * g;
+        // after an abort every wait returns at once: the warps finish the sequence in step (their
+        // barriers stay matched) and leave at the verdict below
         (void)wait_w(&aux->s_full[k2], (gt >> 1) & 1, aux, p.err);
         ptx::tc_fence_after();
-        // a tile every row sees whole needs no masks; otherwise row j sees t < len + off_s[j]
-        const bool edge = (sg.t0 + i) * 128 + 128 > sg.len - (p.n_tok - 1);
-        float s[8];
-        {
-          uint32_t a[8], b[8];
-          ptx::tmem_ld8(s_col, a);
-          ptx::tmem_ld8(s_col + NR, b);
-          ptx::tmem_wait_ld();
+        uint32_t hi[8], lo[8];
+        ptx::tmem_ld16x256_x2(s_col, hi);
+        ptx::tmem_ld16x256_x2(s_col + NR, lo);
+        ptx::tmem_wait_ld();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&aux->s_empty[k2]);
+        float s[2][4];                                   // [token of the two][column]
 #pragma unroll
-          for (int j = 0; j < 8; ++j) s[j] = (__uint_as_float(a[j]) + __uint_as_float(b[j])) * p.scale_log2;
-        }
-        if (edge) {
+        for (int e = 0; e < 8; ++e)
+          s[(e >> 1) & 1][(e >> 2) * 2 + (e & 1)] = (__uint_as_float(hi[e]) + __uint_as_float(lo[e])) * p.scale_log2;
+        // a tile every row sees whole needs no masks; otherwise row j sees t < len + off
+        if ((sg.t0 + i) * kTok + kTok > sg.len - (p.n_tok - 1)) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) s[j] = t < sg.len + aux->off_s[8 * g + j] ? s[j] : -INFINITY;
+          for (int k = 0; k < 4; ++k) {
+            s[0][k] = t < sg.len + off[k] ? s[0][k] : -INFINITY;
+            s[1][k] = t + 8 < sg.len + off[k] ? s[1][k] : -INFINITY;
+          }
         }
         bool ex = false;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ex |= s[j] > m[j] + kLazy;
-        ex = ptx::named_bar_or(bar, 128, ex);
-        if (gt > 0) {   // the value mix before has completed: P may be rewritten, O~ rescaled
-          (void)wait_w(&aux->p_empty, (gt - 1) & 1, aux, p.err);
-          ptx::tc_fence_after();
-        }
-        if (!kQuant && t >= sg.len) {
-          // rows behind the sequence hold whatever the page held: 0 weight times a stale
-          // infinity would still be NaN, so their values become 0 (the groups share the boxes)
-          for (int c = g; c < 2 * p.nch; c += NR / 8) {
-            const uint32_t base =
-                ptx::smem_u32(ring + ((gt * p.nch + (c >> 1)) % p.nslot) * kSlot + (c & 1) * kSub + row * 128);
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + v * 16), "r"(0) : "memory");
-          }
-        }
-        __syncwarp();
+        for (int k = 0; k < 4; ++k) ex |= fmaxf(s[0][k], s[1][k]) > m[k] + kLazy;
+        ex = ptx::named_bar_or(1 + g, 128, ex);
         if (ex) {
-          float top[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top[j] = s[j];
-          const float mt = reduce_cols<true>(top, lane);
-          if (lane < 8) aux->red[g][qd][lane] = mt;   // read by all before the next tile's vote
-          ptx::named_bar_sync(bar, 128);
-          float a[8];
-          bool need_o = false;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float mn = fmaxf(m[j], fmaxf(fmaxf(aux->red[g][0][j], aux->red[g][1][j]),
-                                               fmaxf(aux->red[g][2][j], aux->red[g][3][j])));
-            a[j] = ptx::ex2_approx(m[j] - mn);
-            m[j] = mn;
-            l[j] *= a[j];
-            need_o |= a[j] < 1.f;
+          for (int k = 0; k < 4; ++k) {
+            const float top = reduce_rows<true>(fmaxf(s[0][k], s[1][k]));
+            if (lane < 4) aux->red[g][qd][col0 - 16 * g + 8 * (k >> 1) + (k & 1)] = top;   // read by all before the next vote
           }
-          if (need_o && i > 0) {
-            for (int c = 0; c < p.nch; ++c) {
-              uint32_t v[8];
-              const uint32_t col = tmem + lane_off + kOCol + c * NR + 8 * g;
-              ptx::tmem_ld8(col, v);
+          ptx::named_bar_sync(1 + g, 128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = col0 - 16 * g + 8 * (k >> 1) + (k & 1);
+            const float mn = fmaxf(m[k], fmaxf(fmaxf(aux->red[g][0][c], aux->red[g][1][c]),
+                                               fmaxf(aux->red[g][2][c], aux->red[g][3][c])));
+            const float a = ptx::ex2_approx(m[k] - mn);
+            m[k] = mn;
+            l[k] *= a;
+            if (qd == 0 && lane < 4) aux->alpha[g][c] = a;
+          }
+          if (i > 0) {
+            // the value mixes before have completed, then the group's 16 columns of O~ are rescaled
+            ptx::named_bar_sync(1 + g, 128);
+            (void)wait_w(&aux->p_empty[k2 ^ 1], ((gt - 1) >> 1) & 1, aux, p.err);
+            ptx::tc_fence_after();
+            for (int c = 0; c < nch; ++c) {
+              uint32_t v[16];
+              const uint32_t col = tmem + lane_off + kOCol + c * NR + 16 * g;
+              ptx::tmem_ld16(col, v);
               ptx::tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * a[j]);
-              ptx::tmem_st8(col, v);
+              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * aux->alpha[g][j]);
+              ptx::tmem_st16(col, v);
             }
             ptx::tmem_wait_st();
           }
         }
-        uint32_t hw[4];
+        if (!kQuant && sg.len - (sg.t0 + i) * kTok < kTok) {
+          // rows behind the sequence hold whatever the page held: 0 weight times a stale
+          // infinity would still be NaN, so their values become 0
+          for (int c = warp - 4; c < nsub; c += 4 * NG)
+            for (int rr = lane; rr < kTok; rr += 32)
+              if ((sg.t0 + i) * kTok + rr >= sg.len) {
+                const uint32_t base = ptx::smem_u32(ring + w.slot * slot_bytes + c * kSub + rr * 128);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p0 = ptx::ex2_approx(s[2 * e] - m[2 * e]);
-          const float p1 = ptx::ex2_approx(s[2 * e + 1] - m[2 * e + 1]);
-          const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-          l[2 * e] += p0;
-          l[2 * e + 1] += p1;
-          hw[e] = *reinterpret_cast<const uint32_t*>(&h);
+                for (int v = 0; v < 8; ++v)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + v * 16), "r"(0) : "memory");
+              }
+          __syncwarp();
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(ptx::smem_u32(p_s + g * 2048 + row * 16)),
-                     "r"(hw[0]), "r"(hw[1]), "r"(hw[2]), "r"(hw[3])
-                     : "memory");
-        // every lane makes its own stores visible to the tensor core, then one arrival per warp
+        if (gt >= 2) (void)wait_w(&aux->p_empty[k2], ((gt >> 1) - 1) & 1, aux, p.err);   // this buffer's last use
+#pragma unroll
+        for (int tk = 0; tk < 2; ++tk)
+#pragma unroll
+          for (int cb = 0; cb < 2; ++cb) {
+            const float p0 = ptx::ex2_approx(s[tk][2 * cb] - m[2 * cb]);
+            const float p1 = ptx::ex2_approx(s[tk][2 * cb + 1] - m[2 * cb + 1]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+            l[2 * cb] += p0;
+            l[2 * cb + 1] += p1;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_at + k2 * kPBuf + cb * (kTok * 16) + tk * 128),
+                         "r"(*reinterpret_cast<const uint32_t*>(&h))
+                         : "memory");
+          }
+        // the weights become visible to the tensor core, then one arrival per warp
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&aux->s_empty[k2]);
-          ptx::mbar_arrive(&aux->p_full);
-        }
+        if (lane == 0) ptx::mbar_arrive(&aux->p_full[k2]);
       }
-      ok = ptx::named_bar_and(bar, 128, wait_b(&aux->o_full, nseg & 1, aux, p.err));
+      ok = ptx::named_bar_and(1 + g, 128, wait_b(&aux->o_full, nseg & 1, aux, p.err));
       if (!ok) break;
       ptx::tc_fence_after();
-      const size_t base = ((size_t)(x + sg.b) * p.HB + hb) * NR + 8 * g;
-      const float lt = reduce_cols<false>(l, lane);
-      if (lane < 8) aux->red[g][qd][lane] = lt;
-      ptx::named_bar_sync(bar, 128);
-      if (qd == 0 && lane < 8) {
-        float mj = m[0];
+      const size_t base = ((size_t)(x + sg.b) * p.HB + hb) * NR;
 #pragma unroll
-        for (int j = 1; j < 8; ++j) mj = lane == j ? m[j] : mj;
-        const float l4 = (aux->red[g][0][lane] + aux->red[g][1][lane]) + (aux->red[g][2][lane] + aux->red[g][3][lane]);
-        reinterpret_cast<float2*>(p.part_ml)[base + lane] = make_float2(mj, l4);
+      for (int k = 0; k < 4; ++k) {
+        const float lt = reduce_rows<false>(l[k]);
+        if (lane < 4) aux->red[g][qd][col0 - 16 * g + 8 * (k >> 1) + (k & 1)] = lt;
       }
-      for (int c = 0; c < p.nch; ++c) {
-        uint32_t o[8];
-        ptx::tmem_ld8(tmem + lane_off + kOCol + c * NR + 8 * g, o);
+      ptx::named_bar_sync(1 + g, 128);
+      if (qd == 0 && lane < 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = col0 - 16 * g + 8 * (k >> 1) + (k & 1);
+          const float l4 = (aux->red[g][0][c] + aux->red[g][1][c]) + (aux->red[g][2][c] + aux->red[g][3][c]);
+          reinterpret_cast<float2*>(p.part_ml)[base + 16 * g + c] = make_float2(m[k], l4);
+        }
+      }
+      __syncwarp();
+      for (int c = 0; c < nch; ++c) {                    // thread = rank row
+        const int e = c * 128 + qd * 32 + lane;
+        uint32_t o[16];
+        ptx::tmem_ld16(tmem + lane_off + kOCol + c * NR + 16 * g, o);
         ptx::tmem_wait_ld();
-        const int e = c * 128 + row;
         if (e < p.r) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (hb * NR + 8 * g + j < p.R) p.part_o[(base + j) * p.r + e] = __uint_as_float(o[j]);
+          for (int j = 0; j < 16; ++j)
+            if (hb * NR + 16 * g + j < p.R) p.part_o[(base + 16 * g + j) * p.r + e] = __uint_as_float(o[j]);
         }
         __syncwarp();
       }
@@ -418,32 +598,32 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       if (lane == 0) ptx::mbar_arrive(&aux->o_empty);
       ++nseg;
     }
-  } else if (kQuant) {
+    __syncwarp();
+  } else if (kQuant && warp >= 4 + 4 * NG) {
     // ------------------------------------------------------------- expansion of codes
-    const int tid = threadIdx.x - (64 + NR * 16);   // 0..255
-    int pos = 0;
+    const int tid = threadIdx.x - (128 + NR * 8), h = tid >> 7;   // each half takes every other chunk
+    Ring w;
     bool ok = true;
     while (ok && next_seg(&run, p, &sg)) {
-      for (int i = 0; i < sg.nt && ok; ++i) {
-        const int valid = sg.len - (sg.t0 + i) * 128;      // token rows of this tile (may exceed 128)
-        for (int c = 0; c < p.nch; ++c, ++pos) {
-          const int slot = pos % p.nslot;
-          if (!(ok = wait_w(&aux->raw_full[slot], (pos / p.nslot) & 1, aux, p.err))) break;
-          uint8_t* dst = ring + slot * kSlot;
-          const uint8_t* sc = sc_s + slot * kScaleBytes;
-          expand_chunk(dst, sc, tid, c * 128 + 64 < p.r, valid);
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&aux->slot_full[slot]);
-        }
+      for (int i = 0; i < sg.nt; ++i, w.next(p.nslot)) {
+        uint8_t* dst = ring + w.slot * slot_bytes;
+        if (!(ok = wait_w(&aux->raw_full[w.slot], w.ph, aux, p.err))) break;
+        const int valid = sg.len - (sg.t0 + i) * kTok;     // token rows of this tile (may exceed 64)
+        for (int c = h; c < nch; c += 2)
+          expand_chunk(dst + 2 * c * kSub, dst + (rope_box + 1) * kSub + c * kScaleBytes, tid & 127, c * 128 + 64 < p.r,
+                       valid);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&aux->full[w.slot]);
       }
     }
+    __syncwarp();
   }
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc(tmem, 256);
   }
 }
 
@@ -474,7 +654,7 @@ __global__ void __launch_bounds__(128)
     return;
   }
   uint8_t* w_s = smem_raw;                       // dn/64 blocks of 128 ranks x 128 B
-  uint8_t* q_s = smem_raw + (p.dn >> 6) * kSub;  // dn/64 blocks of ncols rows x 128 B
+  uint8_t* q_s = smem_raw + (p.dn >> 6) * kWSub;  // dn/64 blocks of ncols rows x 128 B
   QpAux& aux = *reinterpret_cast<QpAux*>(q_s + (p.dn >> 6) * p.ncols * 128);
   const int i0 = blockIdx.x * 128, h = blockIdx.y, bs0 = blockIdx.z * p.nb;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -486,8 +666,8 @@ __global__ void __launch_bounds__(128)
     ptx::mbar_init(&aux.done, 1);
     aux.abort_flag = 0;
     ptx::fence_mbar_init();
-    ptx::mbar_arrive_expect_tx(&aux.w_full, kb * kSub);
-    for (int k = 0; k < kb; ++k) ptx::tma_load_2d(w_s + k * kSub, &tm_w, &aux.w_full, h * p.dn + k * 64, i0);
+    ptx::mbar_arrive_expect_tx(&aux.w_full, kb * kWSub);
+    for (int k = 0; k < kb; ++k) ptx::tma_load_2d(w_s + k * kWSub, &tm_w, &aux.w_full, h * p.dn + k * 64, i0);
   }
   if (warp == 1) {
     ptx::tmem_alloc(&aux.tmem_base, 128);
@@ -517,7 +697,7 @@ __global__ void __launch_bounds__(128)
       for (int k = 0; k < kb; ++k)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_f16_elect(tmem, wd + (uint64_t)((k * kSub >> 4) + kk * 2),
+          ptx::mma_f16_elect(tmem, wd + (uint64_t)((k * kWSub >> 4) + kk * 2),
                              qd + (uint64_t)((k * qblk >> 4) + kk * 2), id, (k | kk) ? 1u : 0u);
     }
     ptx::mma_commit_elect(&aux.done);
@@ -623,7 +803,7 @@ __global__ void __launch_bounds__(kOutThreads)
   const int nrow = min(p.RB, p.rows - m0);               // rows m0 .. m0 + nrow - 1
   if (warp == 0) {
     // slots of the rows' sequences, from the same cut into runs as the decode's
-    auto tiles = [&](int b) { return (shared_len(p.row_len, b, p.cap) + 127) >> 7; };
+    auto tiles = [&](int b) { return (shared_len(p.row_len, b, p.cap) + kTok - 1) / kTok; };
     const int chunk = max(1, (tile_total(tiles, p.B) + p.X - 1) / p.X);
     int run = 0;
     for (int base = 0; base < p.B; base += 32) {
@@ -794,25 +974,23 @@ __global__ void __launch_bounds__(kOutThreads)
 // host side
 // ---------------------------------------------------------------------------
 
-// How R query rows per sequence are cut: NR per block, HB blocks, X runs of tiles.  A block of
-// 16 rows when a sequence has no more, else 32; pairs of CTAs (r > 256) also have blocks of 64.
+// How R query rows per sequence are cut: NR per block (16 when a sequence has no more, else 32),
+// HB blocks, X runs of tiles.  (64 rows a block leave room for one tile only at r = 512.)
 struct Cut {
   int NR, HB, X;
 };
 Cut cut_of(const lr_shared_desc& d, int n_tokens, int num_sms) {
   const int R = n_tokens * d.n_q_heads;
-  const bool pair = d.rank > 256;
   Cut c;
-  c.NR = R <= 16 ? 16 : (pair && R > 32 ? 64 : 32);
+  c.NR = R <= 16 ? 16 : 32;
   c.HB = (R + c.NR - 1) / c.NR;
-  c.X = std::max(1, std::min(num_sms, kMaxRuns) / (pair ? 2 : 1) / c.HB);
+  c.X = std::max(1, std::min(num_sms, kMaxRuns) / c.HB);
   return c;
 }
 
 size_t decode_smem(int r, int NR, int nslot, bool quant) {
-  const size_t head = (size_t)(r / 64) * 2 * NR * 128 + (size_t)NR * 128 + 128 * NR * 2;
-  return kAuxBytes + ((head + 1023) & ~(size_t)1023) + (size_t)nslot * kSlot + kSub +
-         (quant ? (size_t)nslot * kScaleBytes : 0);
+  return kAuxBytes + (size_t)(r / 64) * 2 * NR * 128 + (size_t)NR * 128 + 2 * kTok * NR * 2 +
+         (size_t)nslot * dec_slot(r, quant);
 }
 
 bool map2d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, uint64_t d0, uint64_t d1, uint64_t stride,
@@ -828,7 +1006,7 @@ cudaError_t launch_dec(const lr_shared* c, const CUtensorMap& tqr, const DecArgs
   cudaError_t e = smem_optin(k_shared_decode<NR, kQuant>, optin);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_shared_decode<NR, kQuant>, dim3(a.X, a.HB), dim3(dec_threads<NR, kQuant>()), smem, s,
-                    c->tm_qt[NR / 32], tqr, c->tm_c, c->tm_kr, a);
+                    c->tm_qt[NR / 32], tqr, c->tm_c64, c->tm_kr, a);
 }
 
 }  // namespace
@@ -858,13 +1036,13 @@ cudaError_t shared_decode_maps(lr_shared* c) {
   const uint64_t qrows = shared_qt_bytes(&d) / (r * 2);
   bool ok = map2d(&c->tm_w, bf, c->B, wk, r, (wk + wv) * 2, 64, 128) &&
             map2d(&c->tm_v, bf, static_cast<const __nv_bfloat16*>(c->B) + wk, wv, r, (wk + wv) * 2, 64, 64) &&
-            map2d(&c->tm_kr, bf, c->kr, d.dim_rope, rows, (uint64_t)d.dim_rope * 2, 64, 128) &&
+            map2d(&c->tm_kr, bf, c->kr, d.dim_rope, rows, (uint64_t)d.dim_rope * 2, 64, kTok) &&
             map2d(&c->tm_qt[0], bf, c->qt, r, qrows, r * 2, 64, 32) &&
-            map2d(&c->tm_qt[1], bf, c->qt, r, qrows, r * 2, 64, 64) &&
-            map2d(&c->tm_qt[2], bf, c->qt, r, qrows, r * 2, 64, 128);
+            map2d(&c->tm_qt[1], bf, c->qt, r, qrows, r * 2, 64, 64);
   // (8 bits: the codes are copied without a map; any valid one stands in)
-  if (ok && d.quant_bits) c->tm_c = c->tm_kr;
-  else if (ok) ok = map2d(&c->tm_c, bf, c->c, r, rows, r * 2, 64, 128);
+  if (ok && d.quant_bits) c->tm_c = c->tm_c64 = c->tm_kr;
+  else if (ok)
+    ok = map2d(&c->tm_c, bf, c->c, r, rows, r * 2, 64, 128) && map2d(&c->tm_c64, bf, c->c, r, rows, r * 2, 64, kTok);
   return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -903,7 +1081,7 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   static std::atomic<uint32_t> optin_q{0}, optin_o{0};
   cudaError_t e = smem_optin(k_shared_qproj, optin_q);
   if (e != cudaSuccess) return e;
-  const size_t smem_q = (size_t)(d.dim_nope / 64) * (kSub + qp.ncols * 128) + sizeof(QpAux);
+  const size_t smem_q = (size_t)(d.dim_nope / 64) * (kWSub + qp.ncols * 128) + sizeof(QpAux);
   e = launch_pdl(k_shared_qproj, dim3((r + 127) / 128, d.n_kv_heads, (BS + qp.nb - 1) / qp.nb), dim3(128), smem_q, s,
                  c->tm_w, tq, qp);
   if (e != cudaSuccess) return e;
@@ -916,17 +1094,31 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
     if (!tc::make_map(&tqr, bf, static_cast<const __nv_bfloat16*>(q) + d.dim_nope, 3, dims, st, box))
       return cudaErrorInvalidValue;
   }
-  if (r > 256) {
-    e = launch_shared_pair(c, tqr, row_len, n_tokens, R, NR, HB, X, s);
-  } else {
-    DecArgs a = dec_args(c, row_len, n_tokens, R, HB, X);
-    while (a.nslot < kMaxSlots && decode_smem(r, NR, a.nslot + 1, quant) <= (size_t)kSmemLimit) ++a.nslot;
-    const size_t smem = decode_smem(r, NR, a.nslot, quant);
-    if (NR == 16)
-      e = quant ? launch_dec<16, true>(c, tqr, a, smem, s) : launch_dec<16, false>(c, tqr, a, smem, s);
-    else
-      e = quant ? launch_dec<32, true>(c, tqr, a, smem, s) : launch_dec<32, false>(c, tqr, a, smem, s);
-  }
+  DecArgs a;
+  a.wait_ns = c->wait_ns;
+  a.row_len = row_len;
+  a.map = row_map(c);
+  a.B = d.batch;
+  a.cap = d.capacity;
+  a.r = r;
+  a.Hq = d.n_q_heads;
+  a.n_tok = n_tokens;
+  a.R = R;
+  a.HB = HB;
+  a.X = X;
+  a.scale_log2 = c->scale_log2;
+  a.codes = static_cast<const uint8_t*>(c->c);
+  a.scale = c->scale;
+  a.part_o = c->part_o;
+  a.part_ml = c->part_ml;
+  a.err = c->dev_err;
+  a.nslot = 1;
+  while (a.nslot < kMaxSlots && decode_smem(r, NR, a.nslot + 1, quant) <= (size_t)kSmemLimit) ++a.nslot;
+  const size_t smem = decode_smem(r, NR, a.nslot, quant);
+  if (NR == 16)
+    e = quant ? launch_dec<16, true>(c, tqr, a, smem, s) : launch_dec<16, false>(c, tqr, a, smem, s);
+  else
+    e = quant ? launch_dec<32, true>(c, tqr, a, smem, s) : launch_dec<32, false>(c, tqr, a, smem, s);
   if (e != cudaSuccess) return e;
 
   // join and output projection

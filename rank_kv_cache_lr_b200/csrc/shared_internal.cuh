@@ -31,10 +31,11 @@ struct lr_shared {
   int* dev_err = nullptr;
 
   // tensor maps of the cache's own storage, made once
-  CUtensorMap tm_c, tm_kr;    // latents (bf16 caches) and rotary keys by stored row
+  CUtensorMap tm_c, tm_c64;   // latents (bf16 caches) by stored row, in boxes of 128 and 64 tokens
+  CUtensorMap tm_kr;          // rotary keys, 64 tokens
   CUtensorMap tm_w, tm_v;     // B_k: 128 ranks x 64 columns; B_v: 64 ranks x 64 columns
   CUtensorMap tm_bt;          // Bt: 128 columns x 64 ranks
-  CUtensorMap tm_qt[3];       // query latents, hi | lo blocks of 2 x 16, 2 x 32 and 2 x 64 rows
+  CUtensorMap tm_qt[2];       // query latents, hi | lo blocks of 2 x 16 and 2 x 32 rows
 };
 
 inline RowMap row_map(const lr_shared* c) {
@@ -67,8 +68,7 @@ __device__ __forceinline__ float shared_pow2(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7FC00000u : byte << 23);
 }
 
-// Work of the paged kernels: the 128-token tiles of all sequences in order, cut into equal
-// runs, run x for CTA column x of X.  A run may span several sequences, and a sequence
+// Work of the paged kernels: the tiles of all sequences in order, cut into equal runs, run x for CTA column x of X.  A run may span several sequences, and a sequence
 // several runs; (x, b) pairs form a staircase, so x + b numbers them without gaps in use.
 struct TileRun {
   int b, tile, left;   // first sequence, first tile in it, tiles in the run
@@ -140,10 +140,6 @@ cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t*
 cudaError_t launch_shared_attn(lr_shared* c, const void* q, const void* k, const void* kr, const void* v,
                                const int32_t* cu_q, const int32_t* cu_k, int nseq, int total_q, int total_k,
                                int causal, void* out, float* lse, cudaStream_t s);
-// the decode of r > 256 by pairs of CTAs (k_shared_pair.cu): query rows per block for R rows, and
-// the attention launch
-cudaError_t launch_shared_pair(const lr_shared* c, const CUtensorMap& tqr, const int32_t* row_len, int n_tokens,
-                               int R, int NR, int HB, int X, cudaStream_t s);
 // tensor maps of the cache's storage (host only)
 cudaError_t shared_decode_maps(lr_shared* c);
 cudaError_t shared_expand_maps(lr_shared* c);

@@ -49,43 +49,6 @@ __device__ __forceinline__ bool wait_b(uint64_t* bar, uint32_t parity, int* abor
   }
 }
 
-// wait_b in fewer instructions (one try_wait in the loop, no separate first test): for roles whose
-// code is walked once per step, where the instruction fetch itself sets the pace.
-__device__ __forceinline__ bool wait_small(uint64_t* bar, uint32_t parity, int* abort_flag, int* err,
-                                           uint64_t limit_ns) {
-  const uint32_t hint = limit_ns < kSuspendNs ? (uint32_t)limit_ns : kSuspendNs;
-  uint64_t t0 = 0;
-#pragma unroll 1
-  while (!ptx::mbar_try_wait_hint(bar, parity, hint)) {
-    const uint64_t now = ptx::globaltimer();
-    if (t0 == 0) t0 = now;
-    const bool late = now - t0 > limit_ns;
-    if (late) {
-      *(volatile int*)abort_flag = 1;
-      atomicExch(err, (int)LR_ERR_TIMEOUT);
-    }
-    if (late || *(volatile int*)abort_flag) return false;
-  }
-  return true;
-}
-
-// As wait_b, for phases that another CTA of the cluster completes: what it wrote before its
-// arrival is visible afterwards.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* abort_flag, int* err,
-                                             uint64_t limit_ns) {
-  const uint64_t t0 = ptx::globaltimer();
-  const uint32_t hint = limit_ns < kSuspendNs ? (uint32_t)limit_ns : kSuspendNs;
-  for (;;) {
-    if (ptx::mbar_try_wait_cluster(bar, parity, hint)) return true;
-    if (*(volatile int*)abort_flag) return false;
-    if (ptx::globaltimer() - t0 > limit_ns) {
-      *(volatile int*)abort_flag = 1;
-      atomicExch(err, (int)LR_ERR_TIMEOUT);
-      return false;
-    }
-  }
-}
-
 // Wait that ignores the abort flag (used to drain in-flight copies and MMAs after an
 // abort); still bounded, always by kTimeoutNs (a short test limit applies only to the
 // waits above).
