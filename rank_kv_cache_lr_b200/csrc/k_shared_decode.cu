@@ -41,7 +41,6 @@ using tc::kSmemLimit;
 constexpr int kTok = 64;               // tokens of a tile
 constexpr int kSub = kTok * 128;       // 64 tokens x 64 ranks x 2 B (one TMA box)
 constexpr int kWSub = 128 * 128;       // 128 rows x 64 columns x 2 B (the projections' operands)
-constexpr int kScaleBytes = kTok * 4;  // 8 bits: exponent bytes of 64 tokens x 4 groups, per 128 ranks
 constexpr int kAuxBytes = 2048;
 constexpr int kMaxSlots = 4;
 constexpr float kNoMax = -1e30f;       // running max before any visible token (finite: no inf - inf)
@@ -98,28 +97,27 @@ __device__ __forceinline__ __nv_bfloat162 place2(uint32_t w) {
 }
 // Sixteen codes of one token (their words in the order in which they are stored), times 2^e, to
 // two 16-byte columns of a swizzled row: w.x, w.y to address a0 and w.z, w.w to a1.  e <= 7
-// (exponent byte at most 134): 2^(120 + e) is a bf16, so one exact product; kTwo: two products.
-template <bool kTwo>
+// (exponent byte at most 134): 2^(120 + e) is a bf16, so one exact product; above, two products
+// 2^(b1 - 127) 2^(b2 - 127) with 120 folded into the first; byte 255 (a group that held a NaN or an
+// infinity) is NaN.
 __device__ __forceinline__ void expand16(const uint4& w, uint32_t eb, uint32_t a0, uint32_t a1) {
-  // 2^e = 2^(b1 - 127) 2^(b2 - 127) with 120 folded into the first; byte 255 (a group that held a
-  // NaN or an infinity) is NaN
-  const uint32_t b1 = kTwo ? min(eb + 120u, 254u) : eb + 120u;
-  const uint32_t h1 = kTwo && eb == 255u ? 0x7FC07FC0u : b1 * 0x00800080u;
-  const uint32_t h2 = (eb + 247u - b1) * 0x00800080u;
+  const uint32_t b1 = min(eb + 120u, 254u);
+  const uint32_t h1 = eb == 255u ? 0x7FC07FC0u : b1 * 0x00800080u;
   const __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162*>(&h1);
-  const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&h2);
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  uint32_t o[8];
+  __nv_bfloat162 x[8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    __nv_bfloat162 x = __hmul2(place2<0x9180>(in[k]), s1), y = __hmul2(place2<0xB3A2>(in[k]), s1);
-    if (kTwo) {
-      x = __hmul2(x, s2);
-      y = __hmul2(y, s2);
-    }
-    o[2 * k] = *reinterpret_cast<const uint32_t*>(&x);
-    o[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&y);
+    x[2 * k] = __hmul2(place2<0x9180>(in[k]), s1);
+    x[2 * k + 1] = __hmul2(place2<0xB3A2>(in[k]), s1);
   }
+  if (__any_sync(0xffffffffu, eb > 134u)) {
+    const uint32_t h2 = (eb + 247u - b1) * 0x00800080u;
+    const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&h2);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = __hmul2(x[k], s2);
+  }
+  const uint32_t* o = reinterpret_cast<const uint32_t*>(x);
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                : "memory");
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
@@ -129,60 +127,34 @@ __device__ __forceinline__ void expand16(const uint4& w, uint32_t eb, uint32_t a
 // (an MMA issues at the tensor core's pace; without, every ~160 cycles).
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// Expand one 128-rank chunk of a tile by 128 threads (tid): codes in the second of the chunk's two
-// boxes at `dst`, exponent bytes `sc` [64][4], to bf16 boxes; `full`: 128 ranks (else 64); token
-// rows at `valid` and beyond, which hold whatever the page held, become 0.
-__device__ __forceinline__ void expand_chunk(uint8_t* dst, const uint8_t* sc, int tid, bool full, int valid) {
-  // 16 codes a thread and step: 8 (a last chunk of 64 ranks: 4) threads per token row
-  const int sh = full ? 3 : 2, steps = full ? 4 : 2;
-  const int col = tid & ((1 << sh) - 1), tok0 = tid >> sh, dtok = 128 >> sh;
-  uint4 w[4];
-  uint32_t eb[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    eb[k] = 127u;
-    if (k < steps) {
-      w[k] = reinterpret_cast<const uint4*>(dst + kSub)[k * 128 + tid];
-      eb[k] = sc[(k * dtok + tok0) * 4 + (col >> 1)];
-    }
-  }
-  // A whole chunk's codes of a token lie where its second box row goes, and a warp holds
-  // whole tokens: once its lanes have read, it may write.
-  __syncwarp();
-  // 128-byte swizzle: 16-byte column v of row tok sits at v ^ (tok % 8), and tok % 8 is
-  // the same in every step; the lanes of the second box take their two columns in the
-  // other order, so that the eight lanes of a row store to eight different columns
-  const bool swap = col >= 4;
-  const uint32_t base = ptx::smem_u32(dst + (col >> 2) * kSub + tok0 * 128);
-  const uint32_t a0 = base + ((((col & 3) * 2 + swap) ^ (tok0 & 7)) << 4);
-  const uint32_t a1 = base + ((((col & 3) * 2 + !swap) ^ (tok0 & 7)) << 4);
-  const bool two = __any_sync(0xffffffffu, max(max(eb[0], eb[1]), max(eb[2], eb[3])) > 134u);
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k < steps) {
-      const uint32_t off = k * dtok * 128;
-      uint4 x = w[k];
-      if (swap) x = make_uint4(w[k].z, w[k].w, w[k].x, w[k].y);
-      if (two) expand16<true>(x, eb[k], a0 + off, a1 + off);
-      else expand16<false>(x, eb[k], a0 + off, a1 + off);
-    }
-  if (valid < kTok) {
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k < steps && k * dtok + tok0 >= valid) {
-        const uint32_t off = k * dtok * 128;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a0 + off), "r"(0) : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a1 + off), "r"(0) : "memory");
-      }
-  }
+// Sixteen codes of one token row of a 128-rank chunk, per thread of 256: 8 threads a row, so 32 rows
+// a step; in a last chunk of 64 ranks 4 threads a row, one step.
+struct CodePlace {
+  uint32_t off, sc_off;    // of the codes in the chunk's rows, of their exponent byte
+  uint32_t a0, a1;         // of the two 16-byte columns in the chunk's bf16 boxes
+  int tok;
+};
+__device__ __forceinline__ CodePlace code_place(int tid, int sh) {
+  const int col = tid & ((1 << sh) - 1);
+  CodePlace x;
+  x.tok = tid >> sh;
+  x.off = (uint32_t)tid * 16;
+  x.sc_off = (uint32_t)(x.tok * 4 + (col >> 1));
+  // 128-byte swizzle: 16-byte column v of row tok sits at v ^ (tok % 8); the lanes of the second
+  // box take their two columns in the other order, so that the eight lanes of a row store to eight
+  // different columns
+  const int swap = col >> 2;
+  const uint32_t base = (uint32_t)(swap * kSub + x.tok * 128);
+  x.a0 = base + ((((col & 3) * 2 + swap) ^ (x.tok & 7)) << 4);
+  x.a1 = base + ((((col & 3) * 2 + 1 - swap) ^ (x.tok & 7)) << 4);
+  return x;
 }
 
 // Barriers (arrival count; who arrives -> who waits); phase k is waited with parity k & 1.  NG =
 // NR / 16 groups of four softmax warps.
-//   raw_full[s]     1 + tx   8 bits: producer's codes, scales and rotary keys -> expansion warps
-//   full[s]         1 + tx (8 bits: 8)   producer's boxes (expansion warps) -> GEMM1 issuer
-//   empty[s]        1        GEMM2's commit -> producer
+//   full[s][h]      1 + tx   producer's boxes -> GEMM1 issuer; half h of the ranks, the rotary box with
+//                            the second (8 bits: 16 expansion warps, + 1 + tx with the rotary box)
+//   empty[s]        1        GEMM2's commit -> producer, expansion warps
 //   q_full/q_empty  1 + tx / 1   per sequence of the run
 //   s_full[2]       1        GEMM1's commit -> softmax warps
 //   s_empty[2]      4 NG     softmax warps (scores read) -> GEMM1 issuer
@@ -192,7 +164,7 @@ __device__ __forceinline__ void expand_chunk(uint8_t* dst, const uint8_t* sc, in
 //   o_empty         4 NG     softmax warps (O~ read) -> GEMM2 issuer
 //   done            2        final commits of both issuers: every MMA complete before TMEM is freed
 struct Aux {
-  uint64_t raw_full[kMaxSlots], full[kMaxSlots], empty[kMaxSlots];
+  uint64_t full[kMaxSlots][2], empty[kMaxSlots];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], p_empty[2], o_full, o_empty, done;
   uint32_t tmem_base;
   int abort_flag;
@@ -236,20 +208,22 @@ __device__ __forceinline__ float reduce_rows(float v) {
 
 // Warps: 0 TMA producer, 1 GEMM1 issuer, 2 GEMM2 issuer (a warp each: what stands between two MMAs
 // of one warp, a barrier test or a commit, would leave the tensor pipe idle), 3 idle; then NG groups
-// of four softmax warps, 16 query rows each; (8 bits) 8 warps that expand codes to bf16.
+// of four softmax warps, 16 query rows each; (8 bits) 16 warps that expand codes to bf16.
 template <int NR, bool kQuant>
 constexpr int dec_threads() {
-  return 128 + NR * 8 + (kQuant ? 256 : 0);
+  return 128 + NR * 8 + (kQuant ? 512 : 0);
 }
-__host__ __device__ constexpr int dec_boxes(int r, bool quant) {   // of a tile, its rotary box last
-  return (quant ? (r + 127) / 128 * 2 : r / 64) + 1;
-}
-__host__ __device__ constexpr int dec_slot(int r, bool quant) {
-  return dec_boxes(r, quant) * kSub + (quant ? ((r + 127) / 128 * kScaleBytes + 1023) & ~1023 : 0);
-}
+// 8 bits: registers a thread at launch, and how the warpgroups share them then
+template <int NR>
+struct Split {
+  static constexpr int kThreads = 128 + NR * 8 + 512, kLaunch = 65536 / kThreads / 8 * 8, kExpand = 64,
+                       kOther = (kThreads * kLaunch - 512 * kExpand) / (kThreads - 512) / 8 * 8;
+  static_assert(512 * kExpand + (kThreads - 512) * kOther <= kThreads * kLaunch, "register split exceeds the launch");
+};
+__host__ __device__ constexpr int dec_slot(int r) { return (r / 64 + 1) * kSub; }   // a tile, its rotary box last
 
 // Shared memory: [aux][q~: r/64 blocks of (2 NR rows hi | lo) x 128 B][q_rope: NR rows x 128 B]
-// [P: 2 x 64 tokens x NR][slots: boxes, 8 bits: scales].
+// [P: 2 x 64 tokens x NR][slots].
 template <int NR, bool kQuant>
 __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     k_shared_decode(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
@@ -262,7 +236,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
   }
   constexpr int NG = NR / 16, kQSub = 2 * NR * 128, kPBuf = kTok * NR * 2;
   const int nsub = p.r >> 6, nch = (p.r + 127) >> 7;
-  const int rope_box = dec_boxes(p.r, kQuant) - 1, slot_bytes = dec_slot(p.r, kQuant);
+  const int slot_bytes = dec_slot(p.r), nsub0 = min(nsub, (nch + 1) / 2 * 2);   // boxes of a tile's first half
   Aux* aux = reinterpret_cast<Aux*>(smem_raw);
   uint8_t* q_s = smem_raw + kAuxBytes;
   uint8_t* qr_s = q_s + nsub * kQSub;
@@ -274,8 +248,8 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nslot; ++s) {
-      ptx::mbar_init(&aux->raw_full[s], 1);
-      ptx::mbar_init(&aux->full[s], kQuant ? 8 : 1);
+      ptx::mbar_init(&aux->full[s][0], kQuant ? 16 : 1);
+      ptx::mbar_init(&aux->full[s][1], kQuant ? 17 : 1);
       ptx::mbar_init(&aux->empty[s], 1);
     }
     ptx::mbar_init(&aux->q_full, 1);
@@ -322,6 +296,8 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
   TileRun run = aux->run;
   Seg sg;
 
+  if (warp < 4) {
+  if constexpr (kQuant) ptx::setmaxnreg_inc<Split<NR>::kOther>();
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer
     if (lane == 0) {
@@ -335,21 +311,24 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
           if (gt >= p.nslot && !(ok = wait_b(&aux->empty[w.slot], w.ph ^ 1, aux, p.err))) break;
           uint8_t* dst = ring + w.slot * slot_bytes;
           const int row = (int)page * 128 + half;
-          uint64_t* load = kQuant ? &aux->raw_full[w.slot] : &aux->full[w.slot];
+          uint64_t* const full = aux->full[w.slot];
           if (kQuant) {
-            ptx::mbar_arrive_expect_tx(load, (uint32_t)(nsub * (kSub / 2) + nch * kScaleBytes + kSub));
-            for (int c = 0; c < nch; ++c) {
-              const int width = min(128, p.r - c * 128);       // bytes of a token's codes
-              ptx::bulk_load(dst + (2 * c + 1) * kSub, p.codes + page * 128 * p.r + c * 16384 + half * width,
-                             (uint32_t)(kTok * width), load);
-              ptx::bulk_load(dst + (rope_box + 1) * kSub + c * kScaleBytes,
-                             p.scale + (page * nch + c) * 512 + half * 4, kScaleBytes, load);
+            // the expansion warps read the codes one tile ahead; this far ahead they come into L2
+            if (i + 3 < sg.nt) {
+              const int tok3 = tok + 3 * kTok, half3 = tok3 & 64;
+              const long long page3 = p.map.page(sg.b, tok3);
+              for (int c = 0; c < nch; ++c) {
+                const int width = min(128, p.r - c * 128);     // bytes of a token's codes
+                ptx::bulk_prefetch(p.codes + page3 * 128 * p.r + c * 16384 + half3 * width, (uint32_t)(kTok * width));
+              }
             }
+            ptx::mbar_arrive_expect_tx(&full[1], kSub);
           } else {
-            ptx::mbar_arrive_expect_tx(load, (uint32_t)((nsub + 1) * kSub));
-            for (int s = 0; s < nsub; ++s) ptx::tma_load_2d(dst + s * kSub, &tm_c, load, s * 64, row);
+            ptx::mbar_arrive_expect_tx(&full[0], (uint32_t)(nsub0 * kSub));
+            ptx::mbar_arrive_expect_tx(&full[1], (uint32_t)((nsub - nsub0 + 1) * kSub));
+            for (int s = 0; s < nsub; ++s) ptx::tma_load_2d(dst + s * kSub, &tm_c, &full[s >= nsub0], s * 64, row);
           }
-          ptx::tma_load_2d(dst + rope_box * kSub, &tm_kr, load, 0, row);
+          ptx::tma_load_2d(dst + nsub * kSub, &tm_kr, &full[1], 0, row);
           ++gt;
           w.next(p.nslot);
           if (i > 0) continue;
@@ -367,7 +346,8 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       for (int k = min(gt, p.nslot); k > 0; --k) {
         if (w.slot == 0) w.ph ^= 1;
         w.slot = w.slot ? w.slot - 1 : p.nslot - 1;
-        drain_wait(kQuant ? &aux->raw_full[w.slot] : &aux->full[w.slot], w.ph);
+        if (!kQuant) drain_wait(&aux->full[w.slot][0], w.ph);
+        drain_wait(&aux->full[w.slot][1], w.ph);
       }
     }
     __syncwarp();
@@ -385,19 +365,27 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       if (!(ok = wait_w(&aux->q_full, nseg & 1, aux, p.err))) break;
       for (int i = 0; i < sg.nt; ++i, ++gt, w.next(p.nslot)) {
         const uint64_t kd = kd0 + uniform((uint32_t)(w.slot * slot_bytes) >> 4);
-        const uint64_t rd = kd + uniform((uint32_t)(rope_box * kSub) >> 4);
+        const uint64_t rd = kd + uniform((uint32_t)(nsub * kSub) >> 4);
         const uint32_t d_s = uniform(tmem + kSCol + 64 * (gt & 1));
         if (gt >= 2 && !(ok = wait_w(&aux->s_empty[gt & 1], ((gt >> 1) - 1) & 1, aux, p.err))) break;
-        if (!(ok = wait_w(&aux->full[w.slot], w.ph, aux, p.err))) break;
+        if (!(ok = wait_w(&aux->full[w.slot][0], w.ph, aux, p.err))) break;
         ptx::tc_fence_after();
+        uint64_t a = kd, b = qd;
+#pragma unroll 1
+        for (int s = 0; s < nsub0; ++s, a += kSub >> 4, b += kQSub >> 4) {
+          const uint32_t more = s ? 1u : 0u;
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          if (s < nsub) {
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_f16_elect(d_s, a + (uint64_t)(kk * 2), b + (uint64_t)(kk * 2), id1, kk ? 1u : more);
+        }
+        if (!(ok = wait_w(&aux->full[w.slot][1], w.ph, aux, p.err))) break;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int s = nsub0; s < nsub; ++s, a += kSub >> 4, b += kQSub >> 4) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              ptx::mma_f16_elect(d_s, kd + (uint64_t)((s * kSub >> 4) + kk * 2), qd + (uint64_t)((s * kQSub >> 4) + kk * 2),
-                                 id1, s + kk ? 1u : 0u);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_f16_elect(d_s, a + (uint64_t)(kk * 2), b + (uint64_t)(kk * 2), id1, 1u);
+        }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)       // columns past dim_rope are 0 on both sides
           ptx::mma_f16_elect(d_s, rd + (uint64_t)(kk * 2), qrd + (uint64_t)(kk * 2), idr, 1u);
@@ -443,7 +431,9 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     ptx::mma_commit_elect(&aux->done);
     drain_wait(&aux->done, 0);
     __syncwarp();
-  } else if (warp >= 4 && warp < 4 + 4 * NG) {
+  }
+  } else if (warp < 4 + 4 * NG) {
+    if constexpr (kQuant) ptx::setmaxnreg_inc<Split<NR>::kOther>();
     // ------------------------------------------------------------- softmax / epilogue
     // Scores of 64 tokens stand in lanes 0..15 of each lane quarter; the fragment load spreads 16
     // lanes x 16 columns over the warp: lane l has tokens l / 4 and l / 4 + 8 of the quarter's 16,
@@ -599,22 +589,86 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       ++nseg;
     }
     __syncwarp();
-  } else if (kQuant && warp >= 4 + 4 * NG) {
+  } else if constexpr (kQuant) {
+    ptx::setmaxnreg_dec<Split<NR>::kExpand>();
     // ------------------------------------------------------------- expansion of codes
-    const int tid = threadIdx.x - (128 + NR * 8), h = tid >> 7;   // each half takes every other chunk
+    // Two groups of 8 warps take the even and the odd chunks.  The codes come straight to registers,
+    // fetched anew as soon as a chunk is expanded, so neither their latency nor their copy holds up a
+    // free slot.  The code is kept short: the roles of this kernel share the instruction caches, and
+    // with addresses made anew for each step its warps waited for instructions more than for anything.
+    const int tid = (threadIdx.x - (128 + NR * 8)) & 255, g = (warp - 4 - 4 * NG) >> 3;
+    const CodePlace wide = code_place(tid, 3), last = code_place(tid, 2);
+    const bool odd = (nsub & 1) != 0, swap = (lane & 4) != 0;
+    TileRun run_n = run;                               // the next tile to fetch, and its page's table entry
+    Seg sn;
+    int in = 0, page_n = 0;
+    bool more = next_seg(&run_n, p, &sn);
+    auto peek = [&]() { page_n = __ldg(p.map.table + (long long)sn.b * p.map.pps + ((sn.t0 + in) * kTok >> 7)); };
+    if (more) peek();
+    const uint8_t* codes = p.codes;                    // the tile to fetch: its page's, and its half of the page
+    const uint8_t* scale = p.scale;
+    int half = 0;
+    // (past the run's end the last tile is fetched again: loads under a condition were waited for
+    // where they were issued)
+    auto advance = [&]() {
+      if (!more) return;
+      const long long page = min(max(page_n, 0), p.map.n_pages - 1);
+      half = (sn.t0 + in) * kTok & 64;
+      codes = p.codes + page * 128 * p.r;
+      scale = p.scale + page * nch * 512 + half * 4;
+      if (++in == sn.nt) {
+        in = 0;
+        more = next_seg(&run_n, p, &sn);
+      }
+      if (more) peek();
+    };
+    uint4 x[2][2];                                     // [chunk of the group][step]
+    uint32_t eb[2][2];
+    auto fetch = [&](int k) {                          // (a chunk that is not there: the group's first again)
+      const int c = g + 2 * k < nch ? g + 2 * k : min(g, nch - 1);
+      const bool l = odd && c == nch - 1;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        // (each byte is used once: it has no place in the little L1 that is left)
+        x[k][r] = ptx::ld_nc_stream(codes + (c * 16384 + (l ? half * 64 + last.off : half * 128 + r * 4096 + wide.off)));
+        eb[k][r] = __ldg(scale + (c * 512 + (l ? last.sc_off : r * 128 + wide.sc_off)));
+      }
+    };
+    advance();
+    fetch(0);
+    fetch(1);
+    advance();
     Ring w;
+    int gt = 0;
     bool ok = true;
     while (ok && next_seg(&run, p, &sg)) {
-      for (int i = 0; i < sg.nt; ++i, w.next(p.nslot)) {
-        uint8_t* dst = ring + w.slot * slot_bytes;
-        if (!(ok = wait_w(&aux->raw_full[w.slot], w.ph, aux, p.err))) break;
+      for (int i = 0; i < sg.nt; ++i, ++gt, w.next(p.nslot)) {
+        const uint32_t dst = ptx::smem_u32(ring + w.slot * slot_bytes);
         const int valid = sg.len - (sg.t0 + i) * kTok;     // token rows of this tile (may exceed 64)
-        for (int c = h; c < nch; c += 2)
-          expand_chunk(dst + 2 * c * kSub, dst + (rope_box + 1) * kSub + c * kScaleBytes, tid & 127, c * 128 + 64 < p.r,
-                       valid);
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&aux->full[w.slot]);
+        if (gt >= p.nslot && !(ok = wait_w(&aux->empty[w.slot], w.ph ^ 1, aux, p.err))) break;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = g + 2 * k;
+          const bool l = odd && c == nch - 1;
+          if (c < nch) {
+            const uint32_t box = dst + 2 * c * kSub;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (r == 0 || !l) {
+                const int tok = (l ? last.tok : wide.tok) + r * 32;
+                uint4 y = x[k][r];
+                if (swap && !l) y = make_uint4(y.z, y.w, y.x, y.y);
+                if (tok >= valid) y = make_uint4(0, 0, 0, 0);        // rows behind the sequence hold whatever the page held
+                expand16(y, tok >= valid ? 127u : eb[k][r], box + r * 4096 + (l ? last.a0 : wide.a0),
+                         box + r * 4096 + (l ? last.a1 : wide.a1));
+              }
+          }
+          fetch(k);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&aux->full[w.slot][k]);
+        }
+        advance();
       }
     }
     __syncwarp();
@@ -988,9 +1042,9 @@ Cut cut_of(const lr_shared_desc& d, int n_tokens, int num_sms) {
   return c;
 }
 
-size_t decode_smem(int r, int NR, int nslot, bool quant) {
+size_t decode_smem(int r, int NR, int nslot) {
   return kAuxBytes + (size_t)(r / 64) * 2 * NR * 128 + (size_t)NR * 128 + 2 * kTok * NR * 2 +
-         (size_t)nslot * dec_slot(r, quant);
+         (size_t)nslot * dec_slot(r);
 }
 
 bool map2d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, uint64_t d0, uint64_t d1, uint64_t stride,
@@ -1005,6 +1059,15 @@ cudaError_t launch_dec(const lr_shared* c, const CUtensorMap& tqr, const DecArgs
   static std::atomic<uint32_t> optin{0};
   cudaError_t e = smem_optin(k_shared_decode<NR, kQuant>, optin);
   if (e != cudaSuccess) return e;
+  if (kQuant) {
+    // the register split was sized for exactly this launch allocation (an increase beyond it waits)
+    static std::atomic<int> regs{-1};
+    if (regs.load() < 0) {
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, k_shared_decode<NR, kQuant>) == cudaSuccess) regs.store(fa.numRegs);
+    }
+    if (regs.load() != Split<NR>::kLaunch) return cudaErrorInvalidConfiguration;
+  }
   return launch_pdl(k_shared_decode<NR, kQuant>, dim3(a.X, a.HB), dim3(dec_threads<NR, kQuant>()), smem, s,
                     c->tm_qt[NR / 32], tqr, c->tm_c64, c->tm_kr, a);
 }
@@ -1113,8 +1176,8 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   a.part_ml = c->part_ml;
   a.err = c->dev_err;
   a.nslot = 1;
-  while (a.nslot < kMaxSlots && decode_smem(r, NR, a.nslot + 1, quant) <= (size_t)kSmemLimit) ++a.nslot;
-  const size_t smem = decode_smem(r, NR, a.nslot, quant);
+  while (a.nslot < kMaxSlots && decode_smem(r, NR, a.nslot + 1) <= (size_t)kSmemLimit) ++a.nslot;
+  const size_t smem = decode_smem(r, NR, a.nslot);
   if (NR == 16)
     e = quant ? launch_dec<16, true>(c, tqr, a, smem, s) : launch_dec<16, false>(c, tqr, a, smem, s);
   else
