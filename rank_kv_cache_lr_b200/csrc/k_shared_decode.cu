@@ -127,27 +127,15 @@ __device__ __forceinline__ void expand16(const uint4& w, uint32_t eb, uint32_t a
 // (an MMA issues at the tensor core's pace; without, every ~160 cycles).
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// Sixteen codes of one token row of a 128-rank chunk, per thread of 256: 8 threads a row, so 32 rows
-// a step; in a last chunk of 64 ranks 4 threads a row, one step.
-struct CodePlace {
-  uint32_t off, sc_off;    // of the codes in the chunk's rows, of their exponent byte
-  uint32_t a0, a1;         // of the two 16-byte columns in the chunk's bf16 boxes
-  int tok;
-};
-__device__ __forceinline__ CodePlace code_place(int tid, int sh) {
-  const int col = tid & ((1 << sh) - 1);
-  CodePlace x;
-  x.tok = tid >> sh;
-  x.off = (uint32_t)tid * 16;
-  x.sc_off = (uint32_t)(x.tok * 4 + (col >> 1));
-  // 128-byte swizzle: 16-byte column v of row tok sits at v ^ (tok % 8); the lanes of the second
-  // box take their two columns in the other order, so that the eight lanes of a row store to eight
-  // different columns
-  const int swap = col >> 2;
-  const uint32_t base = (uint32_t)(swap * kSub + x.tok * 128);
-  x.a0 = base + ((((col & 3) * 2 + swap) ^ (x.tok & 7)) << 4);
-  x.a1 = base + ((((col & 3) * 2 + 1 - swap) ^ (x.tok & 7)) << 4);
-  return x;
+// Sixteen codes of one token row of a 128-rank chunk, per thread of 256: 1 << sh = 8 threads a row, so
+// 32 rows a step; in a last chunk of 64 ranks 4 threads a row, one step.  The codes lie at 16 tid in
+// the chunk's rows; this is where the first of their two 16-byte bf16 columns goes in the chunk's
+// boxes (the second is at ^ 16).  128-byte swizzle: column v of row tok sits at v ^ (tok % 8); the
+// lanes of the second box take their two columns in the other order, so that the eight lanes of a row
+// store to eight different columns.
+__device__ __forceinline__ uint32_t code_place(int tid, int sh) {
+  const int col = tid & ((1 << sh) - 1), tok = tid >> sh, swap = col >> 2;
+  return (uint32_t)(swap * kSub + tok * 128) + ((((col & 3) * 2 + swap) ^ (tok & 7)) << 4);
 }
 
 // Barriers (arrival count; who arrives -> who waits); phase k is waited with parity k & 1.  NG =
@@ -177,7 +165,19 @@ struct Aux {
 static_assert(sizeof(Aux) <= kAuxBytes, "aux block");
 
 __device__ __forceinline__ bool wait_b(uint64_t* bar, uint32_t parity, Aux* aux, int* err) {
-  return tc::wait_b(bar, parity, &aux->abort_flag, err, aux->wait_ns);
+  // (tc::wait_b with the barrier's own suspend time: with a longer hint a waiting warp takes part in
+  // a software loop of short sleeps, and 27 warps wait here at times)
+  if (ptx::mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  for (;;) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (*(volatile int*)&aux->abort_flag) return false;
+    if (ptx::globaltimer() - t0 > aux->wait_ns) {
+      *(volatile int*)&aux->abort_flag = 1;
+      atomicExch(err, (int)LR_ERR_TIMEOUT);
+      return false;
+    }
+  }
 }
 __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, Aux* aux, int* err) {
   return __all_sync(0xffffffffu, wait_b(bar, parity, aux, err));
@@ -213,13 +213,6 @@ template <int NR, bool kQuant>
 constexpr int dec_threads() {
   return 128 + NR * 8 + (kQuant ? 512 : 0);
 }
-// 8 bits: registers a thread at launch, and how the warpgroups share them then
-template <int NR>
-struct Split {
-  static constexpr int kThreads = 128 + NR * 8 + 512, kLaunch = 65536 / kThreads / 8 * 8, kExpand = 64,
-                       kOther = (kThreads * kLaunch - 512 * kExpand) / (kThreads - 512) / 8 * 8;
-  static_assert(512 * kExpand + (kThreads - 512) * kOther <= kThreads * kLaunch, "register split exceeds the launch");
-};
 __host__ __device__ constexpr int dec_slot(int r) { return (r / 64 + 1) * kSub; }   // a tile, its rotary box last
 
 // Shared memory: [aux][q~: r/64 blocks of (2 NR rows hi | lo) x 128 B][q_rope: NR rows x 128 B]
@@ -296,8 +289,6 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
   TileRun run = aux->run;
   Seg sg;
 
-  if (warp < 4) {
-  if constexpr (kQuant) ptx::setmaxnreg_inc<Split<NR>::kOther>();
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer
     if (lane == 0) {
@@ -414,14 +405,14 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
         if (!(ok = wait_w(&aux->p_full[gt & 1], (gt >> 1) & 1, aux, p.err))) break;
         ptx::tc_fence_after();
         // a last block of 64 ranks mixes the box behind it into rows that nobody reads
+        uint64_t a = vd;
+        uint32_t d = d_o;
+#pragma unroll 1
+        for (int c = 0; c < nch; ++c, a += 2 * kSub >> 4, d += NR) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < nch) {
-#pragma unroll
-            for (int kt = 0; kt < 4; ++kt)
-              ptx::mma_f16_elect(d_o + c * NR, vd + (uint64_t)((2 * c * kSub >> 4) + kt * 128), pd + (uint64_t)(kt * 16),
-                                 id2, kt ? 1u : first);
-          }
+          for (int kt = 0; kt < 4; ++kt)
+            ptx::mma_f16_elect(d, a + (uint64_t)(kt * 128), pd + (uint64_t)(kt * 16), id2, kt ? 1u : first);
+        }
         ptx::mma_commit_elect(&aux->empty[w.slot]);
         ptx::mma_commit_elect(&aux->p_empty[gt & 1]);
         if (i == sg.nt - 1) ptx::mma_commit_elect(&aux->o_full);
@@ -431,9 +422,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     ptx::mma_commit_elect(&aux->done);
     drain_wait(&aux->done, 0);
     __syncwarp();
-  }
-  } else if (warp < 4 + 4 * NG) {
-    if constexpr (kQuant) ptx::setmaxnreg_inc<Split<NR>::kOther>();
+  } else if (warp >= 4 && warp < 4 + 4 * NG) {
     // ------------------------------------------------------------- softmax / epilogue
     // Scores of 64 tokens stand in lanes 0..15 of each lane quarter; the fragment load spreads 16
     // lanes x 16 columns over the warp: lane l has tokens l / 4 and l / 4 + 8 of the quarter's 16,
@@ -442,9 +431,6 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     const int tok0 = qd * 16 + (lane >> 2), col0 = 16 * g + 2 * (lane & 3);
     const uint32_t p_at = ptx::smem_u32(p_s + 2 * g * (kTok * 16) + tok0 * 16 + (lane & 3) * 4);
-    int off[4];                                          // visibility of the thread's columns
-#pragma unroll
-    for (int k = 0; k < 4; ++k) off[k] = aux->off_s[col0 + 8 * (k >> 1) + (k & 1)];
     int gt = 0, nseg = 0;
     Ring w;
     bool ok = true;
@@ -477,8 +463,9 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
         if ((sg.t0 + i) * kTok + kTok > sg.len - (p.n_tok - 1)) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            s[0][k] = t < sg.len + off[k] ? s[0][k] : -INFINITY;
-            s[1][k] = t + 8 < sg.len + off[k] ? s[1][k] : -INFINITY;
+            const int end = sg.len + aux->off_s[col0 + 8 * (k >> 1) + (k & 1)];
+            s[0][k] = t < end ? s[0][k] : -INFINITY;
+            s[1][k] = t + 8 < end ? s[1][k] : -INFINITY;
           }
         }
         bool ex = false;
@@ -507,14 +494,16 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
             ptx::named_bar_sync(1 + g, 128);
             (void)wait_w(&aux->p_empty[k2 ^ 1], ((gt - 1) >> 1) & 1, aux, p.err);
             ptx::tc_fence_after();
-            for (int c = 0; c < nch; ++c) {
-              uint32_t v[16];
-              const uint32_t col = tmem + lane_off + kOCol + c * NR + 16 * g;
-              ptx::tmem_ld16(col, v);
+#pragma unroll 1
+            for (int c = 0; c < 2 * nch; ++c) {            // 8 columns at a time
+              uint32_t v[8];
+              const int j0 = 8 * (c & 1);
+              const uint32_t col = tmem + lane_off + kOCol + (c >> 1) * NR + 16 * g + j0;
+              ptx::tmem_ld8(col, v);
               ptx::tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * aux->alpha[g][j]);
-              ptx::tmem_st16(col, v);
+              for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * aux->alpha[g][j0 + j]);
+              ptx::tmem_st8(col, v);
             }
             ptx::tmem_wait_st();
           }
@@ -589,87 +578,86 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       ++nseg;
     }
     __syncwarp();
-  } else if constexpr (kQuant) {
-    ptx::setmaxnreg_dec<Split<NR>::kExpand>();
+  } else if (kQuant && warp >= 4 + 4 * NG) {
     // ------------------------------------------------------------- expansion of codes
     // Two groups of 8 warps take the even and the odd chunks.  The codes come straight to registers,
     // fetched anew as soon as a chunk is expanded, so neither their latency nor their copy holds up a
     // free slot.  The code is kept short: the roles of this kernel share the instruction caches, and
     // with addresses made anew for each step its warps waited for instructions more than for anything.
     const int tid = (threadIdx.x - (128 + NR * 8)) & 255, g = (warp - 4 - 4 * NG) >> 3;
-    const CodePlace wide = code_place(tid, 3), last = code_place(tid, 2);
+    const uint32_t wide = code_place(tid, 3);
     const bool odd = (nsub & 1) != 0, swap = (lane & 4) != 0;
-    TileRun run_n = run;                               // the next tile to fetch, and its page's table entry
-    Seg sn;
-    int in = 0, page_n = 0;
-    bool more = next_seg(&run_n, p, &sn);
-    auto peek = [&]() { page_n = __ldg(p.map.table + (long long)sn.b * p.map.pps + ((sn.t0 + in) * kTok >> 7)); };
+    // the next tile to fetch, its page's table entry, and the rows of the sequence in it
+    int i = 0, page_n = 0, valid_n = 0;
+    bool more = next_seg(&run, p, &sg);
+    auto peek = [&]() { page_n = __ldg(p.map.table + (long long)sg.b * p.map.pps + ((sg.t0 + i) * kTok >> 7)); };
     if (more) peek();
-    const uint8_t* codes = p.codes;                    // the tile to fetch: its page's, and its half of the page
-    const uint8_t* scale = p.scale;
-    int half = 0;
+    int page = 0, half = 0;                            // of the tile being fetched
     // (past the run's end the last tile is fetched again: loads under a condition were waited for
     // where they were issued)
     auto advance = [&]() {
-      if (!more) return;
-      const long long page = min(max(page_n, 0), p.map.n_pages - 1);
-      half = (sn.t0 + in) * kTok & 64;
-      codes = p.codes + page * 128 * p.r;
-      scale = p.scale + page * nch * 512 + half * 4;
-      if (++in == sn.nt) {
-        in = 0;
-        more = next_seg(&run_n, p, &sn);
+      if (!more) return false;
+      page = min(max(page_n, 0), p.map.n_pages - 1);
+      half = (sg.t0 + i) * kTok & 64;
+      valid_n = sg.len - (sg.t0 + i) * kTok;           // (may exceed 64)
+      if (++i == sg.nt) {
+        i = 0;
+        more = next_seg(&run, p, &sg);
       }
       if (more) peek();
+      return true;
     };
     uint4 x[2][2];                                     // [chunk of the group][step]
     uint32_t eb[2][2];
     auto fetch = [&](int k) {                          // (a chunk that is not there: the group's first again)
       const int c = g + 2 * k < nch ? g + 2 * k : min(g, nch - 1);
       const bool l = odd && c == nch - 1;
+      const int sh = l ? 2 : 3;
+      const uint8_t* codes = p.codes + ((long long)page * 128 * p.r + (c * 16384 + half * (16 << sh) + tid * 16));
+      const uint8_t* scale = p.scale + ((long long)page * nch * 512 +
+                                        (c * 512 + (half + (tid >> sh)) * 4 + ((tid & ((1 << sh) - 1)) >> 1)));
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         // (each byte is used once: it has no place in the little L1 that is left)
-        x[k][r] = ptx::ld_nc_stream(codes + (c * 16384 + (l ? half * 64 + last.off : half * 128 + r * 4096 + wide.off)));
-        eb[k][r] = __ldg(scale + (c * 512 + (l ? last.sc_off : r * 128 + wide.sc_off)));
+        x[k][r] = ptx::ld_nc_stream(codes + (l ? 0 : r * 4096));
+        eb[k][r] = __ldg(scale + (l ? 0 : r * 128));
       }
     };
-    advance();
+    bool got = advance();                              // x holds a tile to expand
+    int valid = valid_n;
     fetch(0);
     fetch(1);
-    advance();
     Ring w;
     int gt = 0;
-    bool ok = true;
-    while (ok && next_seg(&run, p, &sg)) {
-      for (int i = 0; i < sg.nt; ++i, ++gt, w.next(p.nslot)) {
-        const uint32_t dst = ptx::smem_u32(ring + w.slot * slot_bytes);
-        const int valid = sg.len - (sg.t0 + i) * kTok;     // token rows of this tile (may exceed 64)
-        if (gt >= p.nslot && !(ok = wait_w(&aux->empty[w.slot], w.ph ^ 1, aux, p.err))) break;
+    while (got) {
+      got = advance();
+      const uint32_t dst = ptx::smem_u32(ring + w.slot * slot_bytes);
+      if (gt >= p.nslot && !wait_w(&aux->empty[w.slot], w.ph ^ 1, aux, p.err)) break;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int c = g + 2 * k;
+      for (int k = 0; k < 2; ++k) {
+        const int c = g + 2 * k;
+        if (c < nch) {
           const bool l = odd && c == nch - 1;
-          if (c < nch) {
-            const uint32_t box = dst + 2 * c * kSub;
+          const uint32_t box = dst + 2 * c * kSub + (l ? code_place(tid, 2) : wide);
+          const int tok = tid >> (l ? 2 : 3);
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if (r == 0 || !l) {
-                const int tok = (l ? last.tok : wide.tok) + r * 32;
-                uint4 y = x[k][r];
-                if (swap && !l) y = make_uint4(y.z, y.w, y.x, y.y);
-                if (tok >= valid) y = make_uint4(0, 0, 0, 0);        // rows behind the sequence hold whatever the page held
-                expand16(y, tok >= valid ? 127u : eb[k][r], box + r * 4096 + (l ? last.a0 : wide.a0),
-                         box + r * 4096 + (l ? last.a1 : wide.a1));
-              }
-          }
-          fetch(k);
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&aux->full[w.slot][k]);
+          for (int r = 0; r < 2; ++r)
+            if (r == 0 || !l) {
+              uint4 y = x[k][r];
+              if (swap && !l) y = make_uint4(y.z, y.w, y.x, y.y);
+              const bool in = tok + r * 32 < valid;        // rows behind the sequence hold whatever the page held
+              if (!in) y = make_uint4(0, 0, 0, 0);
+              expand16(y, in ? eb[k][r] : 127u, box + r * 4096, (box + r * 4096) ^ 16);
+            }
         }
-        advance();
+        fetch(k);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&aux->full[w.slot][k]);
       }
+      valid = valid_n;
+      ++gt;
+      w.next(p.nslot);
     }
     __syncwarp();
   }
@@ -1059,15 +1047,6 @@ cudaError_t launch_dec(const lr_shared* c, const CUtensorMap& tqr, const DecArgs
   static std::atomic<uint32_t> optin{0};
   cudaError_t e = smem_optin(k_shared_decode<NR, kQuant>, optin);
   if (e != cudaSuccess) return e;
-  if (kQuant) {
-    // the register split was sized for exactly this launch allocation (an increase beyond it waits)
-    static std::atomic<int> regs{-1};
-    if (regs.load() < 0) {
-      cudaFuncAttributes fa;
-      if (cudaFuncGetAttributes(&fa, k_shared_decode<NR, kQuant>) == cudaSuccess) regs.store(fa.numRegs);
-    }
-    if (regs.load() != Split<NR>::kLaunch) return cudaErrorInvalidConfiguration;
-  }
   return launch_pdl(k_shared_decode<NR, kQuant>, dim3(a.X, a.HB), dim3(dec_threads<NR, kQuant>()), smem, s,
                     c->tm_qt[NR / 32], tqr, c->tm_c64, c->tm_kr, a);
 }
