@@ -44,8 +44,8 @@ constexpr int kWSub = 128 * 128;       // 128 rows x 64 columns x 2 B (the proje
 constexpr int kAuxBytes = 2048;
 constexpr int kMaxSlots = 4;
 constexpr float kNoMax = -1e30f;       // running max before any visible token (finite: no inf - inf)
-constexpr int kSCol = 0;               // TMEM: S of tile t in columns [64 (t % 2), + 2 NR)
-constexpr int kOCol = 128;             // TMEM: O~ of 128-rank block k in columns [128 + k NR, + NR)
+constexpr int kSCol = 0;               // TMEM: S of tile t and rank half h in columns [128 (t % 2) + 64 h, + 2 NR)
+constexpr int kOCol = 256;             // TMEM: O~ of 128-rank block k in columns [256 + k NR, + NR)
 
 struct DecArgs {
   unsigned long long wait_ns;
@@ -143,14 +143,14 @@ __device__ __forceinline__ uint32_t code_place(int tid, int sh) {
 //   full[s][h]      1 + tx   producer's boxes -> GEMM1 issuer; half h of the ranks, the rotary box with
 //                            the second (8 bits: 16 expansion warps, + 1 + tx with the rotary box)
 //   empty[s]        1        GEMM2's commit -> producer, expansion warps
-//   q_full/q_empty  1 + tx / 1   per sequence of the run
-//   s_full[2]       1        GEMM1's commit -> softmax warps
+//   q_full/q_empty  1 + tx / 2   per sequence of the run
+//   s_full[2]       2        GEMM1's commits (one a half) -> softmax warps
 //   s_empty[2]      4 NG     softmax warps (scores read) -> GEMM1 issuer
 //   p_full[2]       4 NG     softmax warps -> GEMM2 issuer
 //   p_empty[2]      1        GEMM2's commit -> softmax warps (P may be rewritten, O~ rescaled)
 //   o_full          1        GEMM2's commit, last tile of a sequence -> softmax warps
 //   o_empty         4 NG     softmax warps (O~ read) -> GEMM2 issuer
-//   done            2        final commits of both issuers: every MMA complete before TMEM is freed
+//   done            3        final commits of the issuers: every MMA complete before TMEM is freed
 struct Aux {
   uint64_t full[kMaxSlots][2], empty[kMaxSlots];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], p_empty[2], o_full, o_empty, done;
@@ -206,9 +206,10 @@ __device__ __forceinline__ float reduce_rows(float v) {
   return v;
 }
 
-// Warps: 0 TMA producer, 1 GEMM1 issuer, 2 GEMM2 issuer (a warp each: what stands between two MMAs
-// of one warp, a barrier test or a commit, would leave the tensor pipe idle), 3 idle; then NG groups
-// of four softmax warps, 16 query rows each; (8 bits) 16 warps that expand codes to bf16.
+// Warps: 0 TMA producer, 1 and 3 GEMM1 issuers, one for each half of the ranks (an MMA and what
+// prepares it take a warp ~85 clocks here, 33 in the pipe, so two warps fill it better; each half
+// has its own accumulator, as nothing orders the MMAs of two warps), 2 GEMM2 issuer; then NG groups of
+// four softmax warps, 16 query rows each; (8 bits) 16 warps that expand codes to bf16.
 template <int NR, bool kQuant>
 constexpr int dec_threads() {
   return 128 + NR * 8 + (kQuant ? 512 : 0);
@@ -246,22 +247,22 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       ptx::mbar_init(&aux->empty[s], 1);
     }
     ptx::mbar_init(&aux->q_full, 1);
-    ptx::mbar_init(&aux->q_empty, 1);
+    ptx::mbar_init(&aux->q_empty, 2);
     for (int k = 0; k < 2; ++k) {
-      ptx::mbar_init(&aux->s_full[k], 1);
+      ptx::mbar_init(&aux->s_full[k], 2);
       ptx::mbar_init(&aux->s_empty[k], 4 * NG);
       ptx::mbar_init(&aux->p_full[k], 4 * NG);
       ptx::mbar_init(&aux->p_empty[k], 1);
     }
     ptx::mbar_init(&aux->o_full, 1);
     ptx::mbar_init(&aux->o_empty, 4 * NG);
-    ptx::mbar_init(&aux->done, 2);
+    ptx::mbar_init(&aux->done, 3);
     aux->abort_flag = 0;
     aux->wait_ns = tc::wait_limit(p.wait_ns);
     ptx::fence_mbar_init();
   }
-  if (threadIdx.x >= 96 && threadIdx.x < 96 + NR) {   // query row j of this block belongs to token (hb NR + j) / Hq
-    const int j = threadIdx.x - 96;
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + NR) {   // query row j of this block belongs to token (hb NR + j) / Hq
+    const int j = threadIdx.x - 64;
     aux->off_s[j] = min((hb * NR + j) / p.Hq, p.n_tok - 1) - (p.n_tok - 1);
   }
   if (warp == 0 && lane == 0) {
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     ptx::prefetch_tmap(&tm_kr);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&aux->tmem_base, 256);
+    ptx::tmem_alloc(&aux->tmem_base, 512);
     ptx::tmem_relinquish();
   }
   pdl_wait();       // lengths, pages, rows and q~ may come from the work just before
@@ -342,12 +343,13 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------- GEMM1 issuer (warp-wide)
     const uint32_t id1 = ptx::idesc_f16(1, 0, 0, kTok, 2 * NR);  // K-major x K-major (hi | lo)
     const uint32_t idr = ptx::idesc_f16(1, 0, 0, kTok, NR);      // rotary part, into the hi columns
     const uint64_t kd0 = ptx::smem_desc(ptx::smem_u32(ring), 16, 1024, 2);
-    const uint64_t qd = ptx::smem_desc(ptx::smem_u32(q_s), 16, 1024, 2);
+    const int h = warp == 3, s0 = h ? nsub0 : 0, s1 = h ? nsub : nsub0;   // half of the ranks, its boxes
+    const uint64_t qb = ptx::smem_desc(ptx::smem_u32(q_s + s0 * kQSub), 16, 1024, 2);
     const uint64_t qrd = ptx::smem_desc(ptx::smem_u32(qr_s), 16, 1024, 2);
     int gt = 0, nseg = 0;
     Ring w;
@@ -355,31 +357,24 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     while (ok && next_seg(&run, p, &sg)) {
       if (!(ok = wait_w(&aux->q_full, nseg & 1, aux, p.err))) break;
       for (int i = 0; i < sg.nt; ++i, ++gt, w.next(p.nslot)) {
-        const uint64_t kd = kd0 + uniform((uint32_t)(w.slot * slot_bytes) >> 4);
-        const uint64_t rd = kd + uniform((uint32_t)(nsub * kSub) >> 4);
-        const uint32_t d_s = uniform(tmem + kSCol + 64 * (gt & 1));
+        uint64_t a = kd0 + uniform((uint32_t)(w.slot * slot_bytes + s0 * kSub) >> 4), b = qb;
+        const uint32_t d_s = uniform(tmem + kSCol + 128 * (gt & 1) + 64 * h);
         if (gt >= 2 && !(ok = wait_w(&aux->s_empty[gt & 1], ((gt >> 1) - 1) & 1, aux, p.err))) break;
-        if (!(ok = wait_w(&aux->full[w.slot][0], w.ph, aux, p.err))) break;
+        if (!(ok = wait_w(&aux->full[w.slot][h], w.ph, aux, p.err))) break;
         ptx::tc_fence_after();
-        uint64_t a = kd, b = qd;
 #pragma unroll 1
-        for (int s = 0; s < nsub0; ++s, a += kSub >> 4, b += kQSub >> 4) {
-          const uint32_t more = s ? 1u : 0u;
+        for (int s = s0; s < s1; ++s, a += kSub >> 4, b += kQSub >> 4) {
+          const uint32_t more = s > s0 ? 1u : 0u;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             ptx::mma_f16_elect(d_s, a + (uint64_t)(kk * 2), b + (uint64_t)(kk * 2), id1, kk ? 1u : more);
         }
-        if (!(ok = wait_w(&aux->full[w.slot][1], w.ph, aux, p.err))) break;
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int s = nsub0; s < nsub; ++s, a += kSub >> 4, b += kQSub >> 4) {
+        if (h == 1) {                        // the rotary box follows the ranks' boxes
+          const uint32_t more = s1 > s0 ? 1u : 0u;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            ptx::mma_f16_elect(d_s, a + (uint64_t)(kk * 2), b + (uint64_t)(kk * 2), id1, 1u);
+          for (int kk = 0; kk < 4; ++kk)     // columns past dim_rope are 0 on both sides
+            ptx::mma_f16_elect(d_s, a + (uint64_t)(kk * 2), qrd + (uint64_t)(kk * 2), idr, kk ? 1u : more);
         }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)       // columns past dim_rope are 0 on both sides
-          ptx::mma_f16_elect(d_s, rd + (uint64_t)(kk * 2), qrd + (uint64_t)(kk * 2), idr, 1u);
         ptx::mma_commit_elect(&aux->s_full[gt & 1]);
         if (i == sg.nt - 1) ptx::mma_commit_elect(&aux->q_empty);
       }
@@ -443,14 +438,16 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       }
       for (int i = 0; i < sg.nt; ++i, ++gt, w.next(p.nslot)) {
         const int k2 = gt & 1, t = (sg.t0 + i) * kTok + tok0;
-        const uint32_t s_col = tmem + lane_off + kSCol + 64 * k2 + 16 * g;
+        const uint32_t s_col = tmem + lane_off + kSCol + 128 * k2 + 16 * g;
         // after an abort every wait returns at once: the warps finish the sequence in step (their
         // barriers stay matched) and leave at the verdict below
         (void)wait_w(&aux->s_full[k2], (gt >> 1) & 1, aux, p.err);
         ptx::tc_fence_after();
-        uint32_t hi[8], lo[8];
+        uint32_t hi[8], lo[8], hi1[8], lo1[8];
         ptx::tmem_ld16x256_x2(s_col, hi);
         ptx::tmem_ld16x256_x2(s_col + NR, lo);
+        ptx::tmem_ld16x256_x2(s_col + 64, hi1);
+        ptx::tmem_ld16x256_x2(s_col + 64 + NR, lo1);     // (nothing there if all ranks are in the first half)
         ptx::tmem_wait_ld();
         ptx::tc_fence_before();
         __syncwarp();
@@ -458,7 +455,10 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
         float s[2][4];                                   // [token of the two][column]
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          s[(e >> 1) & 1][(e >> 2) * 2 + (e & 1)] = (__uint_as_float(hi[e]) + __uint_as_float(lo[e])) * p.scale_log2;
+          s[(e >> 1) & 1][(e >> 2) * 2 + (e & 1)] =
+              ((__uint_as_float(hi[e]) + __uint_as_float(hi1[e])) +
+               (__uint_as_float(lo[e]) + (nsub > nsub0 ? __uint_as_float(lo1[e]) : 0.f))) *
+              p.scale_log2;
         // a tile every row sees whole needs no masks; otherwise row j sees t < len + off
         if ((sg.t0 + i) * kTok + kTok > sg.len - (p.n_tok - 1)) {
 #pragma unroll
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 256);
+    ptx::tmem_dealloc(tmem, 512);
   }
 }
 
