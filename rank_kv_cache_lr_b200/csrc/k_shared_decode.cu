@@ -678,6 +678,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
 struct QpArgs {
   unsigned long long wait_ns;
   int r, dn, g, nb, BS, n_tok, Hq, HB, NR, ncols;   // ncols: MMA N (nb g rounded up to 16)
+  uint32_t tcols;        // TMEM columns (a power of two)
   __nv_bfloat16* qt;     // [B][HB][2 NR][r]
   int* err;
 };
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(128)
     for (int k = 0; k < kb; ++k) ptx::tma_load_2d(w_s + k * kWSub, &tm_w, &aux.w_full, h * p.dn + k * 64, i0);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&aux.tmem_base, 128);
+    ptx::tmem_alloc(&aux.tmem_base, p.tcols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -775,14 +776,14 @@ __global__ void __launch_bounds__(128)
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 128);
+    ptx::tmem_dealloc(tmem, p.tcols);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Join of the split partials and output projection, per KV head and block of RB (<= 16) query
+// Join of the split partials and output projection, per KV head and block of RB (<= 32) query
 // rows: o~ = sum_k w_k o~_k / sum_k w_k l_k with w_k = 2^(m_k - max m), then
-// out = o~ B_v,h with M = dim_v (A: B_v,h columns, MN-major), N = 32 rows (bf16 hi | lo of o~,
+// out = o~ B_v,h with M = dim_v (A: B_v,h columns, MN-major), N = 2 x 16 or 2 x 32 rows (bf16 hi | lo of o~,
 // so that the projection adds no rounding of its own), K = r.  B_v,h is copied before the
 // grid-dependency wait; partials come from L2.
 struct OutArgs {
@@ -801,9 +802,9 @@ struct OutAux {
   uint64_t w_full, done;
   uint32_t tmem_base;
   int abort_flag;
-  int first[16], count[16], row[16];   // per row: first slot, slots, row of its sequence
-  float inv[16];
-  float w[16][kMaxRuns];
+  int first[32], count[32], row[32];   // per row: first slot, slots, row of its sequence
+  float inv[32];
+  float w[32][kMaxRuns];
   float4 part[kOutThreads];            // sums over subsets of a row's slots
 };
 
@@ -815,8 +816,10 @@ __global__ void __launch_bounds__(kOutThreads)
     return;
   }
   const int nsub = p.r >> 6;
-  uint8_t* o_s = smem_raw;                               // nsub blocks of 32 rows x 128 B
-  uint8_t* w_s = o_s + nsub * 4096;                      // 2 column halves of r rows x 128 B
+  const int half = p.RB <= 16 ? 16 : 32;                 // rows of o~'s hi half, then its lo half
+  const int oblk = 2 * half * 128;
+  uint8_t* o_s = smem_raw;                               // nsub blocks of 2 half rows x 128 B
+  uint8_t* w_s = o_s + nsub * oblk;                      // 2 column halves of r rows x 128 B
   OutAux* aux = reinterpret_cast<OutAux*>(w_s + 2 * p.r * 128);
   const int h = blockIdx.y, m0 = blockIdx.x * p.RB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -832,10 +835,10 @@ __global__ void __launch_bounds__(kOutThreads)
         ptx::tma_load_2d(w_s + v * p.r * 128 + k * 64 * 128, &tm_w, &aux->w_full, h * p.dv + v * 64, k * 64);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&aux->tmem_base, 32);
+    ptx::tmem_alloc(&aux->tmem_base, 64);
     ptx::tmem_relinquish();
   }
-  if (threadIdx.x < 16) aux->count[threadIdx.x] = 0;
+  if (threadIdx.x < 32) aux->count[threadIdx.x] = 0;
   pdl_wait();
   pdl_trigger();
   ptx::tc_fence_before();
@@ -911,16 +914,37 @@ __global__ void __launch_bounds__(kOutThreads)
   const int r4 = p.r >> 2, parts = kOutThreads / r4;
   const int part = (int)threadIdx.x / r4, e = ((int)threadIdx.x % r4) * 4;
   const int subs = max(1, parts / nrow);
-  const int sub = subs > 1 ? part / nrow : 0;
-  for (int k0 = 0; k0 < nrow; k0 += parts) {
-    const int k = subs > 1 ? part % nrow : k0 + part;
-    const bool in = part < parts && k < nrow && sub < subs;
+  auto put = [&](int k, float4 acc) {                    // a row's sum, divided, as hi and lo
+    const float inv = aux->inv[k];
+    acc.x *= inv;
+    acc.y *= inv;
+    acc.z *= inv;
+    acc.w *= inv;
+    const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x, acc.y), h1 = __floats2bfloat162_rn(acc.z, acc.w);
+    const __nv_bfloat162 l0 = __floats2bfloat162_rn(acc.x - __low2float(h0), acc.y - __high2float(h0));
+    const __nv_bfloat162 l1 = __floats2bfloat162_rn(acc.z - __low2float(h1), acc.w - __high2float(h1));
+    // K-major, 128-byte swizzle: row k (hi) and half + k (lo; half % 8 = 0, the same swizzle)
+    uint8_t* d = o_s + (e >> 6) * oblk + k * 128 + ((((e & 63) >> 3) ^ (k & 7)) << 4) + (e & 4) * 2;
+    *reinterpret_cast<uint2*>(d) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+    *reinterpret_cast<uint2*>(d + half * 128) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&l0), *reinterpret_cast<const uint32_t*>(&l1));
+  };
+  auto add = [](float4& acc, float f, const float4& v) {
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  };
+  const size_t step = srow * p.r;
+  auto src_of = [&](int k) { return p.part_o + ((size_t)aux->first[k] * srow + aux->row[k]) * p.r + e; };
+  if (nrow <= parts) {
+    const int k = part % nrow, sub = part / nrow;
+    const bool in = part < parts && sub < subs;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (in) {
       const int n = aux->count[k];
-      const float* src = p.part_o + ((size_t)aux->first[k] * srow + aux->row[k]) * p.r + e;
-      const float* w = aux->w[k];
-      const size_t step = srow * p.r;
+      const float* src = src_of(k);
       for (int s = sub; s < n; s += 8 * subs) {
         float4 v[8];
 #pragma unroll
@@ -928,42 +952,44 @@ __global__ void __launch_bounds__(kOutThreads)
           if (s + q * subs < n) v[q] = *reinterpret_cast<const float4*>(src + (s + q * subs) * step);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (s + q * subs < n) {
-            const float f = w[s + q * subs];
-            acc.x += f * v[q].x;
-            acc.y += f * v[q].y;
-            acc.z += f * v[q].z;
-            acc.w += f * v[q].w;
-          }
+          if (s + q * subs < n) add(acc, aux->w[k][s + q * subs], v[q]);
       }
     }
     if (subs > 1) {
       aux->part[threadIdx.x] = acc;
       __syncthreads();
-      if (in && sub == 0)
-        for (int q = 1; q < subs; ++q) {
-          const float4 v = aux->part[threadIdx.x + q * nrow * r4];
-          acc.x += v.x;
-          acc.y += v.y;
-          acc.z += v.z;
-          acc.w += v.w;
-        }
     }
     if (in && sub == 0) {
-      const float inv = aux->inv[k];
-      acc.x *= inv;
-      acc.y *= inv;
-      acc.z *= inv;
-      acc.w *= inv;
-      const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x, acc.y), h1 = __floats2bfloat162_rn(acc.z, acc.w);
-      const __nv_bfloat162 l0 = __floats2bfloat162_rn(acc.x - __low2float(h0), acc.y - __high2float(h0));
-      const __nv_bfloat162 l1 = __floats2bfloat162_rn(acc.z - __low2float(h1), acc.w - __high2float(h1));
-      // K-major, 128-byte swizzle: row k (hi) and 16 + k (lo; 16 % 8 = 0, the same swizzle)
-      uint8_t* d = o_s + (e >> 6) * 4096 + k * 128 + ((((e & 63) >> 3) ^ (k & 7)) << 4) + (e & 4) * 2;
-      *reinterpret_cast<uint2*>(d) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-      *reinterpret_cast<uint2*>(d + 16 * 128) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&l0), *reinterpret_cast<const uint32_t*>(&l1));
+      for (int q = 1; q < subs; ++q) add(acc, 1.f, aux->part[threadIdx.x + q * nrow * r4]);
+      put(k, acc);
+    }
+  } else if (part < parts) {
+    // four rows at a time, two slots of each: eight loads in flight, as many rows have few slots
+    for (int k0 = part; k0 < nrow; k0 += 4 * parts) {
+      float4 acc[4];
+      int n[4], most = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        n[q] = k0 + q * parts < nrow ? aux->count[k0 + q * parts] : 0;
+        most = max(most, n[q]);
+      }
+      for (int s = 0; s < most; s += 2) {
+        float4 v[4][2];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (s + u < n[q]) v[q][u] = *reinterpret_cast<const float4*>(src_of(k0 + q * parts) + (s + u) * step);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (s + u < n[q]) add(acc[q], aux->w[k0 + q * parts][s + u], v[q][u]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (k0 + q * parts < nrow) put(k0 + q * parts, acc[q]);
     }
   }
   ptx::fence_proxy_async_smem();
@@ -973,14 +999,17 @@ __global__ void __launch_bounds__(kOutThreads)
         0xffffffffu, tc::wait_b(&aux->w_full, 0, &aux->abort_flag, p.err, tc::wait_limit(p.wait_ns)));
     if (ok) {
       ptx::tc_fence_after();
-      const uint32_t id = ptx::idesc_f16(1, 1, 0, 128, 32);   // A MN-major, B K-major
+      const uint32_t id = ptx::idesc_f16(1, 1, 0, 128, 2 * half);   // A MN-major, B K-major
       const uint64_t wd = ptx::smem_desc(ptx::smem_u32(w_s), (uint32_t)p.r * 128, 1024, 2);
       const uint64_t od = ptx::smem_desc(ptx::smem_u32(o_s), 16, 1024, 2);
-      for (int k = 0; k < nsub; ++k)
+      const uint32_t d = uniform(tmem), idu = uniform(id);
+      for (int k = 0; k < nsub; ++k) {
+        const uint64_t a = wd + uniform((uint32_t)(k * 64 * 128) >> 4), b = od + uniform((uint32_t)(k * oblk) >> 4);
+        const uint32_t more = uniform(k ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_f16_elect(tmem, wd + (uint64_t)((k * 64 + kk * 16) * 128 >> 4),
-                             od + (uint64_t)((k * 4096 >> 4) + kk * 2), id, (k | kk) ? 1u : 0u);
+          ptx::mma_f16_elect(d, a + (uint64_t)(kk * 16 * 128 >> 4), b + (uint64_t)(kk * 2), idu, kk ? 1u : more);
+      }
     }
     ptx::mma_commit_elect(&aux->done);
     drain_wait(&aux->w_full, 0);
@@ -990,25 +1019,29 @@ __global__ void __launch_bounds__(kOutThreads)
   __syncthreads();
   ptx::tc_fence_after();
   if (warp < 4 && !aux->abort_flag) {
-    uint32_t v[32];
-    ptx::tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16), v);
-    ptx::tmem_wait_ld();
     const int d = warp * 32 + lane;
-    if (d < p.dv) {
+    for (int k0 = 0; k0 < half; k0 += 16) {
+      uint32_t hi[16], lo[16];
+      ptx::tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + k0, hi);
+      ptx::tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + half + k0, lo);
+      ptx::tmem_wait_ld();
+      if (d < p.dv) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (k < nrow) {
-          const int bs = (m0 + k) / p.g;
-          const size_t o = (size_t)(bs / p.n_tok) * p.n_tok * p.Hq + aux->row[k];
-          p.out[o * p.dv + d] = __float2bfloat16_rn(__uint_as_float(v[k]) + __uint_as_float(v[16 + k]));
-        }
+        for (int k = 0; k < 16; ++k)
+          if (k0 + k < nrow) {
+            const int bs = (m0 + k0 + k) / p.g;
+            const size_t o = (size_t)(bs / p.n_tok) * p.n_tok * p.Hq + aux->row[k0 + k];
+            p.out[o * p.dv + d] = __float2bfloat16_rn(__uint_as_float(hi[k]) + __uint_as_float(lo[k]));
+          }
+      }
+      __syncwarp();
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 32);
+    ptx::tmem_dealloc(tmem, 64);
   }
 }
 
@@ -1111,6 +1144,7 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   qp.HB = HB;
   qp.NR = NR;
   qp.ncols = (qp.nb * g + 15) / 16 * 16;
+  qp.tcols = qp.ncols <= 32 ? 32 : (qp.ncols <= 64 ? 64 : 128);
   qp.qt = static_cast<__nv_bfloat16*>(c->qt);
   qp.err = c->dev_err;
   CUtensorMap tq, tqr;
@@ -1174,7 +1208,7 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   o.g = g;
   o.rows = BS * g;
   // the fewest rows a block whose grid still is one wave (each block reads B_v,h once more)
-  o.RB = 16;
+  o.RB = 32;
   while (o.RB > 1 && (o.rows + o.RB / 2 - 1) / (o.RB / 2) * d.n_kv_heads <= c->num_sms) o.RB /= 2;
   o.n_tok = n_tokens;
   o.Hq = d.n_q_heads;
@@ -1188,7 +1222,7 @@ cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, cons
   o.err = c->dev_err;
   e = smem_optin(k_shared_out, optin_o);
   if (e != cudaSuccess) return e;
-  const size_t smem_o = (size_t)(r / 64) * 4096 + (size_t)2 * r * 128 + sizeof(OutAux);
+  const size_t smem_o = (size_t)(r / 64) * (o.RB <= 16 ? 4096 : 8192) + (size_t)2 * r * 128 + sizeof(OutAux);
   return launch_pdl(k_shared_out, dim3((o.rows + o.RB - 1) / o.RB, d.n_kv_heads), dim3(kOutThreads), smem_o, s, c->tm_v,
                     o);
 }
