@@ -305,15 +305,6 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
           const int row = (int)page * 128 + half;
           uint64_t* const full = aux->full[w.slot];
           if (kQuant) {
-            // the expansion warps read the codes one tile ahead; this far ahead they come into L2
-            if (i + 3 < sg.nt) {
-              const int tok3 = tok + 3 * kTok, half3 = tok3 & 64;
-              const long long page3 = p.map.page(sg.b, tok3);
-              for (int c = 0; c < nch; ++c) {
-                const int width = min(128, p.r - c * 128);     // bytes of a token's codes
-                ptx::bulk_prefetch(p.codes + page3 * 128 * p.r + c * 16384 + half3 * width, (uint32_t)(kTok * width));
-              }
-            }
             ptx::mbar_arrive_expect_tx(&full[1], kSub);
           } else {
             ptx::mbar_arrive_expect_tx(&full[0], (uint32_t)(nsub0 * kSub));

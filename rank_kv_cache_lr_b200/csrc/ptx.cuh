@@ -101,10 +101,6 @@ __device__ __forceinline__ uint4 ld_nc_stream(const void* p) {
                : "l"(p));
   return v;
 }
-// A bulk copy's source into L2 only.
-__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
-}
 // Tiled TMA store shared -> global (bulk group); the coordinates are non-negative.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
