@@ -1,16 +1,17 @@
 // Stored tokens of a shared-latent cache as per-head keys and values: K = C B_k, V = C B_v,
 // with C the latents read back from their pages, and the rotary keys copied along.
 //
-// One GEMM whose A operand is gathered by page: M = 128 tokens (a page), N = 256 columns of
+// One GEMM whose A operand is gathered by page: M = 256 tokens (two pages), N = 256 columns of
 // [K | V], K = rank.  The tensor pipe bounds it (2 r flop per 2-byte output element: 512 flop
-// per byte written at r = 512).  A CTA keeps a page's whole latent tile in shared memory
-// (r <= 512: 128 KB) and streams the bases past it (from a copy transposed at creation, so both
-// operands are K-major rows of 64 ranks), so per 128 x 256 output block only the bases cross
-// L2 (64 B per SM and clock at full rate, what a 256 x 256 tile pair would need too).  The
-// (page, column block) units of all sequences are cut into equal consecutive runs, one per SM:
-// a run changes its tile once or twice, and each 64-rank part of the next tile is fetched as
-// soon as the last block has used the old one.  Two TMEM accumulators let the epilogue of one
-// block run under the MMAs of the next; it stores 32 bytes per lane, whole sectors.
+// per byte written at r = 512).  Two CTAs form a pair (cta_group::2): each keeps one page's whole
+// latent tile in shared memory (r <= 512: 128 KB) and streams half of the bases' columns past both
+// (from a copy transposed at creation, so both operands are K-major rows of 64 ranks).  So per 256 x
+// 256 block only the bases cross L2, half by each: 32 B per SM and clock at full rate, where a single
+// CTA's 128 x 256 blocks need 64 and an SM gets ~38.  The (page pair, column block) units of all
+// sequences are cut into equal consecutive runs, one per pair: a run changes its tiles once or twice,
+// and each 64-rank part of the next is fetched as soon as the last block has used the old one.
+// Two TMEM accumulators let the epilogue of one block run under the MMAs of the next; it stores 32
+// bytes per lane, whole sectors.
 //
 // 8-bit latents are expanded to bf16 (exactly) by eight warps straight from global memory into
 // the swizzled tile, once per tile; the MMAs then run as for bf16.
@@ -26,11 +27,11 @@ namespace {
 using tc::drain_wait;
 
 constexpr int kSub = 128 * 128;        // 128 tokens x 64 ranks x 2 B
-constexpr int kStage = 2 * kSub;       // 256 columns x 64 ranks x 2 B: two boxes of 128 columns
-constexpr int kStages = 3;
+constexpr int kStage = kSub;           // 128 columns x 64 ranks x 2 B (this CTA's half of 256 columns)
+constexpr int kStages = 6;
 constexpr int kAuxBytes = 2048;
 
-constexpr int kMaxTiles = 60;          // tiles of one CTA's run
+constexpr int kMaxTiles = 60;          // tiles of one CTA in a run
 
 struct ExpArgs {
   unsigned long long wait_ns;
@@ -49,11 +50,12 @@ struct Tile {
   int lo, hi;
 };
 
-// Barriers (arrival count; who arrives -> who waits):
-//   a_full[s]   1 + tx / 8   producer (bf16) or expansion warps (8 bits) -> MMA; 64 ranks of the tile
-//   a_empty[s]  1        MMA commit in the tile's last block -> producer / expansion warps
+// Barriers (arrival count; who arrives -> who waits).  CTA 0 issues all MMAs, so what they wait for is
+// counted there, for both CTAs; what they free is announced in both:
+//   a_full[s]   1 + tx / 16   producers (bf16) or expansion warps (8 bits) -> MMA; 64 ranks of the tiles
+//   a_empty[s]  1        MMA commit in the tiles' last block -> producer / expansion warps
 //   b_full/b_empty[s]    1 + tx / 1   basis stages (64 ranks)
-//   d_full/d_empty[2]    1 / 4        accumulators
+//   d_full/d_empty[2]    1 / 8        accumulators
 struct Aux {
   uint64_t a_full[8], a_empty[8], b_full[kStages], b_empty[kStages], d_full[2], d_empty[2], done;
   unsigned long long wait_ns;
@@ -69,6 +71,24 @@ __device__ __forceinline__ bool wait_b(uint64_t* bar, uint32_t parity, Aux* aux,
 }
 __device__ __forceinline__ bool wait_w(uint64_t* bar, uint32_t parity, Aux* aux, int* err) {
   return __all_sync(0xffffffffu, wait_b(bar, parity, aux, err));
+}
+// As wait_w, for phases that the other CTA takes part in: what its threads did before is visible.
+__device__ __forceinline__ bool wait_x(uint64_t* bar, uint32_t parity, Aux* aux, int* err) {
+  const uint64_t t0 = ptx::globaltimer();
+  bool ok = false;
+  for (;;) {
+    if (ptx::mbar_try_wait_cluster(bar, parity)) {
+      ok = true;
+      break;
+    }
+    if (*(volatile int*)&aux->abort_flag) break;
+    if (ptx::globaltimer() - t0 > aux->wait_ns) {
+      *(volatile int*)&aux->abort_flag = 1;
+      atomicExch(err, (int)LR_ERR_TIMEOUT);
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // Positions [lo, hi) of sequence b to expand, inside the cache; position t goes to row t + off.
@@ -121,10 +141,11 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
   const int nsub = p.r >> 6;
   uint8_t* b_s = a_s + nsub * kSub;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cr = ptx::cluster_rank();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
-      ptx::mbar_init(&aux->a_full[s], kQuant ? 8 : 1);
+      ptx::mbar_init(&aux->a_full[s], kQuant ? 16 : 1);
       ptx::mbar_init(&aux->a_empty[s], 1);
     }
     for (int s = 0; s < kStages; ++s) {
@@ -133,7 +154,7 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
     }
     for (int k = 0; k < 2; ++k) {
       ptx::mbar_init(&aux->d_full[k], 1);
-      ptx::mbar_init(&aux->d_empty[k], 4);
+      ptx::mbar_init(&aux->d_empty[k], 8);
     }
     ptx::mbar_init(&aux->done, 1);
     aux->abort_flag = 0;
@@ -143,8 +164,8 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
     ptx::prefetch_tmap(&tm_w);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&aux->tmem_base, 512);
-    ptx::tmem_relinquish();
+    ptx::tmem_alloc_pair(&aux->tmem_base, 512);
+    ptx::tmem_relinquish_pair();
   }
   pdl_wait();
   pdl_trigger();
@@ -152,9 +173,9 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
     // this CTA's run of units, and its tiles
     auto tiles = [&](int b) { return span_tiles(p, b); };
     const int total = tile_total(tiles, p.B);
-    const unsigned G = gridDim.x;
-    const unsigned units = (unsigned)total * (unsigned)p.NB;      // < 2^31 (host)
-    const unsigned chunk = (units + G - 1) / G, first = chunk * (unsigned)blockIdx.x;
+    const unsigned G = gridDim.x / 2;                             // pairs
+    const unsigned units = ((unsigned)total + 1) / 2 * (unsigned)p.NB;      // < 2^31 (host)
+    const unsigned chunk = (units + G - 1) / G, first = chunk * (unsigned)(blockIdx.x >> 1);
     int n = 0, blk0 = 0;
     if (first < units) {
       n = (int)min(chunk, units - first);
@@ -163,7 +184,12 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
       const int t0 = (int)(first / (unsigned)p.NB), nt = (blk0 + n + p.NB - 1) / p.NB;
       for (int k = 0; k < nt; ++k) {
         int b, tile;
-        tile_find(tiles, p.B, t0 + k, &b, &tile);
+        const int t = 2 * (t0 + k) + (int)cr;
+        if (t >= total) {            // an odd number of tiles: the last pair's second is any page, and not stored
+          if (lane == 0) aux->tiles[k] = Tile{0, 0, 0, 0};
+          continue;
+        }
+        tile_find(tiles, p.B, t, &b, &tile);
         if (lane == 0) {
           const Span s = span_at(p, b);
           const int tok = ((s.lo >> 7) + tile) << 7;
@@ -183,6 +209,7 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
+  ptx::cluster_sync();      // both CTAs' barriers are ready before any copy or arrival counts there
   ptx::tc_fence_after();
   const uint32_t tmem = aux->tmem_base;
   const int units = aux->units;
@@ -195,7 +222,7 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
       int a_boxes = 0;                      // boxes issued of tile nt - 1
       bool ok = true;
       for (; ok && w.u < units; w.next(p.NB)) {
-        const int c0 = w.blk * 256, nb = p.W - c0 > 128 ? 2 : 1;
+        const int c0 = w.blk * 256, n2 = min(256, p.W - c0) / 2;   // this CTA's columns of the block
         const bool fresh = w.fresh();
         const int row = (int)aux->tiles[w.k].pool;
         if (fresh) {
@@ -205,27 +232,30 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
         for (int h = 0; h < nsub; ++h) {
           if (!kQuant && fresh) {
             if (nt > 1 && !(ok = wait_b(&aux->a_empty[h], nt & 1, aux, p.err))) break;   // tile nt - 2's use
-            ptx::mbar_arrive_expect_tx(&aux->a_full[h], kSub);
-            ptx::tma_load_2d(a_s + h * kSub, &tm_c, &aux->a_full[h], h * 64, row);
+            if (cr == 0) ptx::mbar_arrive_expect_tx(&aux->a_full[h], 2 * kSub);
+            ptx::tma_load_2d_pair(a_s + h * kSub, &tm_c, ptx::map_rank(ptx::smem_u32(&aux->a_full[h]), 0), h * 64, row);
             ++a_boxes;
           }
           const int st = pos % kStages;
           if (pos >= kStages && !(ok = wait_b(&aux->b_empty[st], (pos / kStages - 1) & 1, aux, p.err))) break;
-          ptx::mbar_arrive_expect_tx(&aux->b_full[st], (uint32_t)(nb * kSub));
-          ptx::tma_load_2d(b_s + st * kStage, &tm_w, &aux->b_full[st], h * 64, c0);   // rows past W read as 0
-          if (nb == 2) ptx::tma_load_2d(b_s + st * kStage + kSub, &tm_w, &aux->b_full[st], h * 64, c0 + 128);
+          if (cr == 0) ptx::mbar_arrive_expect_tx(&aux->b_full[st], 2 * kStage);
+          ptx::tma_load_2d_pair(b_s + st * kStage, &tm_w, ptx::map_rank(ptx::smem_u32(&aux->b_full[st]), 0), h * 64,
+                                c0 + (int)cr * n2);        // rows past W read as 0
           ++pos;
         }
       }
-      // every copy this thread issued has landed before the CTA can exit
-      for (int k = max(0, pos - kStages); k < pos; ++k) drain_wait(&aux->b_full[k % kStages], (k / kStages) & 1);
-      if (!kQuant)
-        for (int s = 0; s < nsub; ++s) {
-          const int n = s < a_boxes ? nt : nt - 1;      // tiles whose box s was issued
-          if (n > 0) drain_wait(&aux->a_full[s], (n - 1) & 1);
-        }
+      // every copy of either CTA has landed before the pair's last barrier (after an abort the other
+      // CTA may not have issued its own: time to land is given there instead)
+      if (cr == 0 && ok) {
+        for (int k = max(0, pos - kStages); k < pos; ++k) drain_wait(&aux->b_full[k % kStages], (k / kStages) & 1);
+        if (!kQuant)
+          for (int s = 0; s < nsub; ++s) {
+            const int n = s < a_boxes ? nt : nt - 1;      // tiles whose box s was issued
+            if (n > 0) drain_wait(&aux->a_full[s], (n - 1) & 1);
+          }
+      }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && cr == 0) {
     // ------------------------------------------------------------- MMA issuer (warp-wide)
     const uint64_t ad0 = ptx::smem_desc(ptx::smem_u32(a_s), 16, 1024, 2);
     const uint64_t bd0 = ptx::smem_desc(ptx::smem_u32(b_s), 16, 1024, 2);
@@ -233,14 +263,14 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
     uint32_t ph = 0;
     bool ok = true;
     for (; ok && w.u < units; w.next(p.NB)) {
-      const uint32_t id = uniform(ptx::idesc_f16(1, 0, 0, 128, (uint32_t)min(256, p.W - w.blk * 256)));
+      const uint32_t id = uniform(ptx::idesc_f16(1, 0, 0, 256, (uint32_t)min(256, p.W - w.blk * 256)));
       const bool fresh = w.fresh(), last = w.last(units, p.NB);
       const int u = w.u;
       if (fresh) ++nt;
       const uint32_t d = uniform(tmem + (uint32_t)(u & 1) * 256);
-      if (u >= 2 && !(ok = wait_w(&aux->d_empty[u & 1], ((u >> 1) - 1) & 1, aux, p.err))) break;
+      if (u >= 2 && !(ok = wait_x(&aux->d_empty[u & 1], ((u >> 1) - 1) & 1, aux, p.err))) break;
       for (int h = 0; h < nsub; ++h) {
-        if (fresh && !(ok = wait_w(&aux->a_full[h], (nt - 1) & 1, aux, p.err))) break;
+        if (fresh && !(ok = wait_x(&aux->a_full[h], (nt - 1) & 1, aux, p.err))) break;
         if (!(ok = wait_w(&aux->b_full[st], ph, aux, p.err))) break;
         ptx::tc_fence_after();
         const uint64_t ad = ad0 + uniform((uint32_t)(h * kSub) >> 4);
@@ -248,20 +278,20 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
         const uint32_t more = uniform(h ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_f16_elect(d, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), id, kk ? 1u : more);
-        ptx::mma_commit_elect(&aux->b_empty[st]);
-        if (last) ptx::mma_commit_elect(&aux->a_empty[h]);
+          ptx::mma_f16_pair_elect(d, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), id, kk ? 1u : more);
+        ptx::mma_commit_pair_elect(&aux->b_empty[st]);
+        if (last) ptx::mma_commit_pair_elect(&aux->a_empty[h]);
         if (++st == kStages) {
           st = 0;
           ph ^= 1;
         }
       }
-      if (ok) ptx::mma_commit_elect(&aux->d_full[u & 1]);
+      if (ok) ptx::mma_commit_pair_elect(&aux->d_full[u & 1]);
     }
-    ptx::mma_commit_elect(&aux->done);
+    ptx::mma_commit_pair_elect(&aux->done);
     drain_wait(&aux->done, 0);
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp >= 2 && warp < 6) {
     // ------------------------------------------------------------- epilogue: thread = token row
     const int qd = warp & 3, row = qd * 32 + lane;
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
@@ -279,7 +309,7 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
         if (c + 32 >= n) {             // all read: the accumulator is free before the last stores
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&aux->d_empty[u & 1]);
+          if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_rank(ptx::smem_u32(&aux->d_empty[u & 1]), 0));
         }
         // 32 columns lie in K or in V (both widths are multiples of 64)
         const int col = c0 + c;
@@ -298,7 +328,7 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
         __syncwarp();                  // the next TMEM load wants the whole warp
       }
     }
-  } else if (kQuant) {
+  } else if (kQuant && warp >= 6) {
     // ------------------------------------------------------------- expansion of codes
     const int tid = threadIdx.x - 192;
     int nt = 0;
@@ -350,15 +380,19 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
-          for (int q = 0; q < ns; ++q) ptx::mbar_arrive(&aux->a_full[s0 + q]);
+          for (int q = 0; q < ns; ++q) ptx::mbar_arrive_cluster(ptx::map_rank(ptx::smem_u32(&aux->a_full[s0 + q]), 0));
       }
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
+  // neither CTA leaves while the other's MMAs, copies or arrivals may still reach it (after an abort,
+  // those that nobody waited for have time to land)
+  if (aux->abort_flag) __nanosleep(1000000);
+  ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -397,10 +431,10 @@ cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t*
   a.v = static_cast<__nv_bfloat16*>(v);
   a.err = c->dev_err;
   const bool quant = d.quant_bits != 0;
-  // One run per SM, no more runs than units there can be, and no run longer than its tile table
-  // holds (beyond 60 tiles an SM, over a million tokens, the runs queue up).
-  const long long tiles = (long long)total / 128 + 2 * std::min<long long>(d.batch, total);
-  const long long grid = std::max(std::min<long long>(c->num_sms, tiles * a.NB), (tiles + kMaxTiles - 3) / (kMaxTiles - 2));
+  // One run per pair of SMs, no more runs than units there can be, and no run longer than its tile
+  // table holds (beyond 60 tiles an SM, over a million tokens, the runs queue up).
+  const long long tiles = (long long)total / 128 + 2 * std::min<long long>(d.batch, total), two = (tiles + 1) / 2;
+  const long long grid = 2 * std::max(std::min<long long>(c->num_sms / 2, two * a.NB), (two + kMaxTiles - 3) / (kMaxTiles - 2));
   if (tiles * a.NB > 0x7FFFFFFF) return cudaErrorNotSupported;
   const size_t smem = kAuxBytes + (size_t)(a.r / 64) * kSub + (size_t)kStages * kStage;
   static std::atomic<uint32_t> optin[2] = {{0}, {0}};
@@ -408,6 +442,6 @@ cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t*
   if (e != cudaSuccess) return e;
   e = launch_shared_read(c, cu, start, total, nullptr, kr, s);   // the rotary keys
   if (e != cudaSuccess) return e;
-  return quant ? launch_pdl(k_shared_expand<true>, dim3((unsigned)grid), dim3(448), smem, s, c->tm_c, c->tm_bt, a)
-               : launch_pdl(k_shared_expand<false>, dim3((unsigned)grid), dim3(192), smem, s, c->tm_c, c->tm_bt, a);
+  return quant ? launch_pdl_cluster(k_shared_expand<true>, dim3((unsigned)grid), dim3(448), 2, smem, s, c->tm_c, c->tm_bt, a)
+               : launch_pdl_cluster(k_shared_expand<false>, dim3((unsigned)grid), dim3(192), 2, smem, s, c->tm_c, c->tm_bt, a);
 }
