@@ -38,8 +38,10 @@ struct ExpArgs {
   const int32_t* cu; const int32_t* start;
   RowMap map;
   int B, cap, total, r, Wk, W, NB;   // columns: [0, Wk) of K, [Wk, W) of V; NB blocks of 256
+  int dr;
   const uint8_t* codes; const uint8_t* scale;
-  __nv_bfloat16* k; __nv_bfloat16* v;
+  const __nv_bfloat16* kr_pool;
+  __nv_bfloat16* k; __nv_bfloat16* v; __nv_bfloat16* kr;
   int* err;
 };
 
@@ -127,8 +129,14 @@ struct Place {
   }
 };
 
+// Warps: 0 TMA producer, 1 MMA issuer (CTA 0), 2..5 epilogue, (8 bits) 6..13 expansion of codes; the
+// last copies the rotary keys.
 template <bool kQuant>
-__global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
+constexpr int exp_threads() {
+  return kQuant ? 480 : 224;
+}
+template <bool kQuant>
+__global__ void __launch_bounds__(exp_threads<kQuant>(), 1)
     k_shared_expand(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_w,
                     const ExpArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -328,6 +336,26 @@ __global__ void __launch_bounds__(kQuant ? 448 : 192, 1)
         __syncwarp();                  // the next TMEM load wants the whole warp
       }
     }
+  } else if (warp == exp_threads<kQuant>() / 32 - 1) {
+    // ------------------------------------------------------------- rotary keys, with a tile's first block
+    const int sh = p.dr == 64 ? 3 : 2;                 // 16-byte parts of a row
+    for (; w.u < units; w.next(p.NB)) {
+      if (w.blk != 0) continue;
+      const Tile t = aux->tiles[w.k];
+      const uint4* src = reinterpret_cast<const uint4*>(p.kr_pool + (t.pool + t.lo) * p.dr);
+      uint4* dst = reinterpret_cast<uint4*>(p.kr + (t.out + t.lo) * p.dr);
+      const int n = (t.hi - t.lo) << sh;
+      for (int i0 = lane; i0 < n; i0 += 8 * 32) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i0 + k * 32 < n) v[k] = __ldg(src + i0 + k * 32);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i0 + k * 32 < n) dst[i0 + k * 32] = v[k];
+      }
+    }
+    __syncwarp();
   } else if (kQuant && warp >= 6) {
     // ------------------------------------------------------------- expansion of codes
     const int tid = threadIdx.x - 192;
@@ -427,6 +455,9 @@ cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t*
   a.NB = (a.W + 255) / 256;
   a.codes = static_cast<const uint8_t*>(c->c);
   a.scale = c->scale;
+  a.dr = d.dim_rope;
+  a.kr_pool = static_cast<const __nv_bfloat16*>(c->kr);
+  a.kr = static_cast<__nv_bfloat16*>(kr);
   a.k = static_cast<__nv_bfloat16*>(k);
   a.v = static_cast<__nv_bfloat16*>(v);
   a.err = c->dev_err;
@@ -440,8 +471,6 @@ cudaError_t launch_shared_expand(lr_shared* c, const int32_t* cu, const int32_t*
   static std::atomic<uint32_t> optin[2] = {{0}, {0}};
   cudaError_t e = quant ? smem_optin(k_shared_expand<true>, optin[1]) : smem_optin(k_shared_expand<false>, optin[0]);
   if (e != cudaSuccess) return e;
-  e = launch_shared_read(c, cu, start, total, nullptr, kr, s);   // the rotary keys
-  if (e != cudaSuccess) return e;
-  return quant ? launch_pdl_cluster(k_shared_expand<true>, dim3((unsigned)grid), dim3(448), 2, smem, s, c->tm_c, c->tm_bt, a)
-               : launch_pdl_cluster(k_shared_expand<false>, dim3((unsigned)grid), dim3(192), 2, smem, s, c->tm_c, c->tm_bt, a);
+  return quant ? launch_pdl_cluster(k_shared_expand<true>, dim3((unsigned)grid), dim3(exp_threads<true>()), 2, smem, s, c->tm_c, c->tm_bt, a)
+               : launch_pdl_cluster(k_shared_expand<false>, dim3((unsigned)grid), dim3(exp_threads<false>()), 2, smem, s, c->tm_c, c->tm_bt, a);
 }

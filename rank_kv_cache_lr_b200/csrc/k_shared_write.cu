@@ -9,14 +9,18 @@
 //
 // Both directions move each byte once and are bound by HBM (one decode step: by latency).  A
 // warp owns a token: its lanes hold 8 consecutive elements each (16 bytes in, 16 or 8 out), so
-// every access is a full coalesced run and a group's maximum is two shuffles within 4 lanes.
+// every access is a full coalesced run and a group's maximum is two shuffles within 4 lanes.  With
+// many tokens a warp owns two of them, all loads first (65536 tokens of r = 512 in 8 bits, written and
+// read back: 59 us with one token a warp, 53 with two, 55 with four or eight; 4.4 TB/s).
 #include "shared_internal.cuh"
 
 #include <cuda_fp8.h>
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8, kMany = 2;
+// Tokens a warp: kMany once that still fills the SMs (64 warps each), else 1, for the shortest way.
+inline int per_warp(int n, int num_sms) { return n >= kMany * 64 * num_sms ? kMany : 1; }
 
 __device__ __forceinline__ uint32_t warp_max4(uint32_t v) {   // over the 4 lanes of a group
   v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -43,71 +47,84 @@ struct AppendArgs {
   void* c; uint8_t* scale; __nv_bfloat16* kr_pool;
 };
 
-template <bool kQuant>
+template <bool kQuant, int T>
 __global__ void __launch_bounds__(32 * kWarps) k_shared_append(const AppendArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (i >= a.n) return;
-  const int b = __ldg(a.seq + i), t = __ldg(a.pos + i);
-  if (b < 0 || b >= a.B || t < 0 || t >= a.cap) return;   // a padded row: writes nothing
-  const long long row = a.map.row(b, t);
+  const int i0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * T;
   const int nv = a.r >> 3;                                // 8-element runs, a multiple of 8
-  const uint4* src = reinterpret_cast<const uint4*>(a.z + (long long)i * a.z_stride);
-  uint4 w[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (k * 32 + lane < nv) w[k] = __ldg(src + k * 32 + lane);
-  // rotary part: lane j holds the pair (j, j + dr/2)
-  const int half = a.dr >> 1;
+  const int half = a.dr >> 1;                             // rotary part: lane j holds the pair (j, j + dr/2)
   const bool has = lane < half;
-  float x0 = 0.f, x1 = 0.f;
-  if (has) {
-    const __nv_bfloat16* kr = a.kr + (long long)i * a.kr_stride;
-    x0 = __bfloat162float(kr[lane]);
-    x1 = __bfloat162float(kr[half + lane]);
-    if (a.rope_cs) {
-      const float2 cs = __ldg(a.rope_cs + (long long)t * half + lane);
-      const float y0 = x0 * cs.x - x1 * cs.y, y1 = x0 * cs.y + x1 * cs.x;
-      x0 = y0;
-      x1 = y1;
+  int b[T], t[T];
+  uint4 w[T][2];
+  __nv_bfloat16 x[T][2];
+#pragma unroll
+  for (int u = 0; u < T; ++u) {
+    const int i = i0 + u;
+    b[u] = t[u] = -1;
+    if (i >= a.n) continue;
+    b[u] = __ldg(a.seq + i);
+    t[u] = __ldg(a.pos + i);
+    const uint4* src = reinterpret_cast<const uint4*>(a.z + (long long)i * a.z_stride);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (k * 32 + lane < nv) w[u][k] = __ldg(src + k * 32 + lane);
+    if (has) {
+      const __nv_bfloat16* kr = a.kr + (long long)i * a.kr_stride;
+      x[u][0] = kr[lane];
+      x[u][1] = kr[half + lane];
     }
-    __nv_bfloat16* dst = a.kr_pool + row * a.dr;
-    dst[lane] = __float2bfloat16_rn(x0);
-    dst[half + lane] = __float2bfloat16_rn(x1);
   }
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int v = k * 32 + lane;
-    const bool in = v < nv;
-    if (!kQuant) {
-      if (in) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.c) + row * a.r)[v] = w[k];
-      continue;
-    }
-    const uint32_t ww[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-    uint32_t top = 0;
-    if (in) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, max(ww[e] & 0x7FFFu, (ww[e] >> 16) & 0x7FFFu));
-    }
-    top = warp_max4(top);
-    const uint32_t eb = shared_quant_exp(top);
-    const float inv = __uint_as_float((254u - min(eb, 247u)) << 23);   // 2^-e
-    if (in) {
-      uint32_t o[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float2 p = make_float2(__uint_as_float(ww[2 * h] << 16) * inv,
-                                     __uint_as_float(ww[2 * h] & 0xFFFF0000u) * inv);
-        const float2 q = make_float2(__uint_as_float(ww[2 * h + 1] << 16) * inv,
-                                     __uint_as_float(ww[2 * h + 1] & 0xFFFF0000u) * inv);
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-        o[h] = lo | (hi << 16);
+  for (int u = 0; u < T; ++u) {
+    if (b[u] < 0 || b[u] >= a.B || t[u] < 0 || t[u] >= a.cap) continue;   // a padded row: writes nothing
+    const long long row = a.map.row(b[u], t[u]);
+    if (has) {
+      float x0 = __bfloat162float(x[u][0]), x1 = __bfloat162float(x[u][1]);
+      if (a.rope_cs) {
+        const float2 cs = __ldg(a.rope_cs + (long long)t[u] * half + lane);
+        const float y0 = x0 * cs.x - x1 * cs.y, y1 = x0 * cs.y + x1 * cs.x;
+        x0 = y0;
+        x1 = y1;
       }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.c) + shared_code_index(row, a.r, v * 8)) = make_uint2(o[0], o[1]);
-      if ((lane & 3) == 0) a.scale[shared_scale_index(row, a.r, v >> 2)] = (uint8_t)eb;
+      __nv_bfloat16* dst = a.kr_pool + row * a.dr;
+      dst[lane] = __float2bfloat16_rn(x0);
+      dst[half + lane] = __float2bfloat16_rn(x1);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int v = k * 32 + lane;
+      const bool in = v < nv;
+      if (!kQuant) {
+        if (in) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.c) + row * a.r)[v] = w[u][k];
+        continue;
+      }
+      const uint32_t ww[4] = {w[u][k].x, w[u][k].y, w[u][k].z, w[u][k].w};
+      uint32_t top = 0;
+      if (in) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(ww[e] & 0x7FFFu, (ww[e] >> 16) & 0x7FFFu));
+      }
+      top = warp_max4(top);
+      const uint32_t eb = shared_quant_exp(top);
+      const float inv = __uint_as_float((254u - min(eb, 247u)) << 23);   // 2^-e
+      if (in) {
+        uint32_t o[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 p = make_float2(__uint_as_float(ww[2 * h] << 16) * inv,
+                                       __uint_as_float(ww[2 * h] & 0xFFFF0000u) * inv);
+          const float2 q = make_float2(__uint_as_float(ww[2 * h + 1] << 16) * inv,
+                                       __uint_as_float(ww[2 * h + 1] & 0xFFFF0000u) * inv);
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+          o[h] = lo | (hi << 16);
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.c) + shared_code_index(row, a.r, v * 8)) =
+            make_uint2(o[0], o[1]);
+        if ((lane & 3) == 0) a.scale[shared_scale_index(row, a.r, v >> 2)] = (uint8_t)eb;
+      }
     }
   }
 }
@@ -122,7 +139,7 @@ struct ReadArgs {
 
 // Row i of the packed output belongs to the sequence b with cu[b] <= i < cu[b + 1] and holds
 // its token start[b] + i - cu[b].  Each warp finds b by bisection of cu in shared memory.
-template <bool kQuant>
+template <bool kQuant, int T>
 __global__ void __launch_bounds__(32 * kWarps) k_shared_read(const ReadArgs a) {
   extern __shared__ int32_t cu_s[];
   pdl_wait();
@@ -130,44 +147,71 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_read(const ReadArgs a) {
   for (int k = threadIdx.x; k <= a.B; k += blockDim.x) cu_s[k] = __ldg(a.cu + k);
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (i >= a.total || i < cu_s[0]) return;
-  int lo = 0, hi = a.B;                       // the last b in [0, B] with cu[b] <= i
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu_s[mid] <= i) lo = mid;
-    else hi = mid - 1;
+  const int i0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * T;
+  long long found = -1;                         // lane u: the stored row of output row i0 + u, or none
+  if (lane < T) {
+    const int i = i0 + lane;
+    int lo = 0, hi = a.B;                       // the last b in [0, B] with cu[b] <= i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cu_s[mid] <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    if (i < a.total && i >= cu_s[0] && lo < a.B) {      // (behind the last sequence: left as it is)
+      const long long t = (long long)(a.start ? __ldg(a.start + lo) : 0) + ((long long)i - cu_s[lo]);
+      if (t >= 0 && t < a.cap) found = a.map.row(lo, (int)t);
+    }
   }
-  if (lo >= a.B) return;                      // behind the last sequence: left as it is
-  const long long t = (long long)(a.start ? __ldg(a.start + lo) : 0) + ((long long)i - cu_s[lo]);
-  if (t < 0 || t >= a.cap) return;
-  const long long row = a.map.row(lo, (int)t);
   const int nv = a.r >> 3;
-  uint4* dst = reinterpret_cast<uint4*>(a.z + (long long)i * a.r);
+  long long row[T];
+  uint4 w[T][2], y[T];                          // latents (bf16) or their codes (x, y) and exponent bytes (z)
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int v = k * 32 + lane;
-    if (!a.z || v >= nv) continue;     // a.z null: the rotary keys only
-    if (!kQuant) {
-      dst[v] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.c) + row * a.r) + v);
-      continue;
-    }
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.c) + shared_code_index(row, a.r, v * 8)));
-    const float sc = shared_pow2(__ldg(a.scale + shared_scale_index(row, a.r, v >> 2)));
-    uint32_t o[4];
+  for (int u = 0; u < T; ++u) {
+    row[u] = __shfl_sync(0xffffffffu, found, u);
+    if (row[u] < 0) continue;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const uint32_t two = ((h < 2 ? q.x : q.y) >> (16 * (h & 1))) & 0xFFFFu;
-      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-      const float2 f = __half22float2(__half2(hr));
-      const __nv_bfloat162 bb = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-      o[h] = *reinterpret_cast<const uint32_t*>(&bb);
+    for (int k = 0; k < 2; ++k) {
+      const int v = k * 32 + lane;
+      if (v >= nv) continue;
+      if (!kQuant) {
+        w[u][k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.c) + row[u] * a.r) + v);
+      } else {
+        const uint2 q =
+            __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.c) + shared_code_index(row[u], a.r, v * 8)));
+        w[u][k].x = q.x;
+        w[u][k].y = q.y;
+        w[u][k].z = __ldg(a.scale + shared_scale_index(row[u], a.r, v >> 2));
+      }
     }
-    dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
+    if (lane < (a.dr >> 3)) y[u] = __ldg(reinterpret_cast<const uint4*>(a.kr_pool + row[u] * a.dr) + lane);
   }
-  if (lane < (a.dr >> 3))
-    reinterpret_cast<uint4*>(a.kr + (long long)i * a.dr)[lane] =
-        __ldg(reinterpret_cast<const uint4*>(a.kr_pool + row * a.dr) + lane);
+#pragma unroll
+  for (int u = 0; u < T; ++u) {
+    if (row[u] < 0) continue;
+    const long long i = i0 + u;
+    uint4* dst = reinterpret_cast<uint4*>(a.z + i * a.r);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int v = k * 32 + lane;
+      if (v >= nv) continue;
+      if (!kQuant) {
+        dst[v] = w[u][k];
+        continue;
+      }
+      const float sc = shared_pow2(w[u][k].z);
+      uint32_t o[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const uint32_t two = ((h < 2 ? w[u][k].x : w[u][k].y) >> (16 * (h & 1))) & 0xFFFFu;
+        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+        const float2 f = __half22float2(__half2(hr));
+        const __nv_bfloat162 bb = __floats2bfloat162_rn(f.x * sc, f.y * sc);
+        o[h] = *reinterpret_cast<const uint32_t*>(&bb);
+      }
+      dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (lane < (a.dr >> 3)) reinterpret_cast<uint4*>(a.kr + i * a.dr)[lane] = y[u];
+  }
 }
 
 __global__ void k_shared_rope(float2* cs, int cap, int half, double log_theta) {
@@ -222,9 +266,14 @@ cudaError_t launch_shared_append(lr_shared* c, const void* z, long long z_stride
   a.c = c->c;
   a.scale = c->scale;
   a.kr_pool = static_cast<__nv_bfloat16*>(c->kr);
-  const dim3 grid((n + kWarps - 1) / kWarps);
-  return c->desc.quant_bits ? launch_pdl(k_shared_append<true>, grid, dim3(32 * kWarps), 0, s, a)
-                            : launch_pdl(k_shared_append<false>, grid, dim3(32 * kWarps), 0, s, a);
+  const bool many = per_warp(n, c->num_sms) > 1;
+  const int per = kWarps * (many ? kMany : 1);
+  const dim3 grid((n + per - 1) / per);
+  if (many)
+    return c->desc.quant_bits ? launch_pdl(k_shared_append<true, kMany>, grid, dim3(32 * kWarps), 0, s, a)
+                              : launch_pdl(k_shared_append<false, kMany>, grid, dim3(32 * kWarps), 0, s, a);
+  return c->desc.quant_bits ? launch_pdl(k_shared_append<true, 1>, grid, dim3(32 * kWarps), 0, s, a)
+                            : launch_pdl(k_shared_append<false, 1>, grid, dim3(32 * kWarps), 0, s, a);
 }
 
 cudaError_t launch_shared_read(lr_shared* c, const int32_t* cu, const int32_t* start, int total, void* z, void* kr,
@@ -243,8 +292,13 @@ cudaError_t launch_shared_read(lr_shared* c, const int32_t* cu, const int32_t* s
   a.kr_pool = static_cast<const __nv_bfloat16*>(c->kr);
   a.z = static_cast<__nv_bfloat16*>(z);
   a.kr = static_cast<__nv_bfloat16*>(kr);
-  const dim3 grid((total + kWarps - 1) / kWarps);
+  const bool many = per_warp(total, c->num_sms) > 1;
+  const int per = kWarps * (many ? kMany : 1);
+  const dim3 grid((total + per - 1) / per);
   const size_t smem = (size_t)(a.B + 1) * sizeof(int32_t);
-  return c->desc.quant_bits ? launch_pdl(k_shared_read<true>, grid, dim3(32 * kWarps), smem, s, a)
-                            : launch_pdl(k_shared_read<false>, grid, dim3(32 * kWarps), smem, s, a);
+  if (many)
+    return c->desc.quant_bits ? launch_pdl(k_shared_read<true, kMany>, grid, dim3(32 * kWarps), smem, s, a)
+                              : launch_pdl(k_shared_read<false, kMany>, grid, dim3(32 * kWarps), smem, s, a);
+  return c->desc.quant_bits ? launch_pdl(k_shared_read<true, 1>, grid, dim3(32 * kWarps), smem, s, a)
+                            : launch_pdl(k_shared_read<false, 1>, grid, dim3(32 * kWarps), smem, s, a);
 }

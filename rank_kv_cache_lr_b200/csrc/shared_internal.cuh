@@ -130,7 +130,6 @@ cudaError_t launch_shared_transpose(lr_shared* c, cudaStream_t s);
 cudaError_t launch_shared_rope_table(lr_shared* c, cudaStream_t s);
 cudaError_t launch_shared_append(lr_shared* c, const void* z, long long z_stride, const void* kr, long long kr_stride,
                                  const int32_t* seq, const int32_t* pos, int n, cudaStream_t s);
-// z null: only the rotary keys are read back
 cudaError_t launch_shared_read(lr_shared* c, const int32_t* cu, const int32_t* start, int total, void* z, void* kr,
                                cudaStream_t s);
 cudaError_t launch_shared_decode(lr_shared* c, const void* q, int n_tokens, const int32_t* row_len, void* out,
