@@ -677,6 +677,7 @@ struct QpAux {
   uint64_t w_full, q_full, done;
   uint32_t tmem_base;
   int abort_flag;
+  long long at[128];     // element of qt where column m's hi half starts (rank 0), or -1: no such row
 };
 
 __global__ void __launch_bounds__(128)
@@ -706,6 +707,15 @@ __global__ void __launch_bounds__(128)
   if (warp == 1) {
     ptx::tmem_alloc(&aux.tmem_base, p.tcols);
     ptx::tmem_relinquish();
+  }
+  {
+    const int m = threadIdx.x, bs = bs0 + m / p.g;
+    long long o = -1;
+    if (m < p.nb * p.g && bs < p.BS) {
+      const int b = bs / p.n_tok, row = (bs % p.n_tok) * p.Hq + h * p.g + m % p.g;
+      o = (((long long)b * p.HB + row / p.NR) * 2 * p.NR + row % p.NR) * p.r;
+    }
+    aux.at[m] = o;
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -751,15 +761,13 @@ __global__ void __launch_bounds__(128)
       ptx::tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const int m = c0 + j, bs = bs0 + m / p.g;
-        if (m >= p.nb * p.g || bs >= p.BS || i >= p.r) continue;
-        const int b = bs / p.n_tok, row = (bs % p.n_tok) * p.Hq + h * p.g + m % p.g;
+        const long long at = aux.at[c0 + j];
+        if (at < 0 || i >= p.r) continue;
         const float f = __uint_as_float(v[j]);
         const __nv_bfloat16 hi = __float2bfloat16_rn(f);
         const __nv_bfloat16 lo = __float2bfloat16_rn(f - __bfloat162float(hi));
-        const size_t o = (((size_t)b * p.HB + row / p.NR) * 2 * p.NR + row % p.NR) * p.r + i;
-        p.qt[o] = hi;
-        p.qt[o + (size_t)p.NR * p.r] = lo;
+        p.qt[at + i] = hi;
+        p.qt[at + (long long)p.NR * p.r + i] = lo;
       }
     }
   }
@@ -793,7 +801,8 @@ struct OutAux {
   uint64_t w_full, done;
   uint32_t tmem_base;
   int abort_flag;
-  int first[32], count[32], row[32];   // per row: first slot, slots, row of its sequence
+  int first[32], count[32], row[32];   // per row: first slot, slots, row of its sequence,
+  long long orow[32];                  // row of the outputs
   float inv[32];
   float w[32][kMaxRuns];
   float4 part[kOutThreads];            // sums over subsets of a row's slots
@@ -842,6 +851,7 @@ __global__ void __launch_bounds__(kOutThreads)
     auto tiles = [&](int b) { return (shared_len(p.row_len, b, p.cap) + kTok - 1) / kTok; };
     const int chunk = max(1, (tile_total(tiles, p.B) + p.X - 1) / p.X);
     int run = 0;
+    const int bk = (m0 + lane) / p.g / p.n_tok;          // the sequence of row m0 + lane
     for (int base = 0; base < p.B; base += 32) {
       const int b = base + lane;
       const int v = b < p.B ? tiles(b) : 0;
@@ -852,13 +862,12 @@ __global__ void __launch_bounds__(kOutThreads)
         if (lane >= o) inc += u;
       }
       const int t0 = run + inc - v;
-      if (v > 0) {
-        const int x0 = t0 / chunk, x1 = (t0 + v - 1) / chunk;
-        for (int k = 0; k < nrow; ++k)
-          if ((m0 + k) / p.g / p.n_tok == b) {
-            aux->first[k] = x0 + b;
-            aux->count[k] = min(x1 - x0 + 1, kMaxRuns);
-          }
+      // lane k: row k's sequence, if it is one of these 32
+      const int tk = __shfl_sync(0xffffffffu, t0, (bk - base) & 31), vk = __shfl_sync(0xffffffffu, v, (bk - base) & 31);
+      if (lane < nrow && bk >= base && bk < base + 32 && vk > 0) {
+        const int x0 = tk / chunk, x1 = (tk + vk - 1) / chunk;
+        aux->first[lane] = x0 + bk;
+        aux->count[lane] = min(x1 - x0 + 1, kMaxRuns);
       }
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
@@ -866,6 +875,7 @@ __global__ void __launch_bounds__(kOutThreads)
     if (lane < nrow) {
       const int bs = (m0 + lane) / p.g;
       aux->row[lane] = (bs % p.n_tok) * p.Hq + h * p.g + (m0 + lane) % p.g;
+      aux->orow[lane] = (long long)(bs / p.n_tok) * p.n_tok * p.Hq + aux->row[lane];
     }
   }
   __syncthreads();
@@ -891,11 +901,7 @@ __global__ void __launch_bounds__(kOutThreads)
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
       aux->inv[k] = l == 0.f ? 0.f : 1.f / l;
-      if (p.lse) {
-        const int bs = (m0 + k) / p.g;
-        p.lse[(size_t)(bs / p.n_tok) * p.n_tok * p.Hq + aux->row[k]] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * LR_LN2;
-      }
+      if (p.lse) p.lse[aux->orow[k]] = l == 0.f ? -INFINITY : (m + log2f(l)) * LR_LN2;
     }
   }
   __syncthreads();
@@ -1020,9 +1026,7 @@ __global__ void __launch_bounds__(kOutThreads)
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           if (k0 + k < nrow) {
-            const int bs = (m0 + k0 + k) / p.g;
-            const size_t o = (size_t)(bs / p.n_tok) * p.n_tok * p.Hq + aux->row[k0 + k];
-            p.out[o * p.dv + d] = __float2bfloat16_rn(__uint_as_float(hi[k]) + __uint_as_float(lo[k]));
+            p.out[aux->orow[k0 + k] * p.dv + d] = __float2bfloat16_rn(__uint_as_float(hi[k]) + __uint_as_float(lo[k]));
           }
       }
       __syncwarp();
