@@ -142,7 +142,7 @@ __device__ __forceinline__ uint32_t code_place(int tid, int sh) {
 // NR / 16 groups of four softmax warps.
 //   full[s][h]      1 + tx   producer's boxes -> GEMM1 issuer; half h of the ranks, the rotary box with
 //                            the second (8 bits: 16 expansion warps, + 1 + tx with the rotary box)
-//   empty[s]        1        GEMM2's commit -> producer, expansion warps
+//   empty[s][h]     1        GEMM2's commit on half h -> producer, expansion warps
 //   q_full/q_empty  1 + tx / 2   per sequence of the run
 //   s_full[2]       2        GEMM1's commits (one a half) -> softmax warps
 //   s_empty[2]      4 NG     softmax warps (scores read) -> GEMM1 issuer
@@ -152,7 +152,7 @@ __device__ __forceinline__ uint32_t code_place(int tid, int sh) {
 //   o_empty         4 NG     softmax warps (O~ read) -> GEMM2 issuer
 //   done            3        final commits of the issuers: every MMA complete before TMEM is freed
 struct Aux {
-  uint64_t full[kMaxSlots][2], empty[kMaxSlots];
+  uint64_t full[kMaxSlots][2], empty[kMaxSlots][2];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], p_empty[2], o_full, o_empty, done;
   uint32_t tmem_base;
   int abort_flag;
@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     for (int s = 0; s < p.nslot; ++s) {
       ptx::mbar_init(&aux->full[s][0], kQuant ? 16 : 1);
       ptx::mbar_init(&aux->full[s][1], kQuant ? 17 : 1);
-      ptx::mbar_init(&aux->empty[s], 1);
+      ptx::mbar_init(&aux->empty[s][0], 1);
+      ptx::mbar_init(&aux->empty[s][1], 1);
     }
     ptx::mbar_init(&aux->q_full, 1);
     ptx::mbar_init(&aux->q_empty, 2);
@@ -300,20 +301,29 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
         for (int i = 0; i < sg.nt; ++i) {
           const int tok = (sg.t0 + i) * kTok, half = tok & 64;
           const long long page = p.map.page(sg.b, tok);
-          if (gt >= p.nslot && !(ok = wait_b(&aux->empty[w.slot], w.ph ^ 1, aux, p.err))) break;
           uint8_t* dst = ring + w.slot * slot_bytes;
           const int row = (int)page * 128 + half;
           uint64_t* const full = aux->full[w.slot];
-          if (kQuant) {
-            ptx::mbar_arrive_expect_tx(&full[1], kSub);
-          } else {
+          // (an abort between the halves leaves the first one's copies to the drain below, whose wait for
+          // the second half then runs into its limit)
+          bool begun = false;
+          if (!kQuant) {
+            if (gt >= p.nslot && !(ok = wait_b(&aux->empty[w.slot][0], w.ph ^ 1, aux, p.err))) break;
+            begun = true;
             ptx::mbar_arrive_expect_tx(&full[0], (uint32_t)(nsub0 * kSub));
-            ptx::mbar_arrive_expect_tx(&full[1], (uint32_t)((nsub - nsub0 + 1) * kSub));
-            for (int s = 0; s < nsub; ++s) ptx::tma_load_2d(dst + s * kSub, &tm_c, &full[s >= nsub0], s * 64, row);
+            for (int s = 0; s < nsub0; ++s) ptx::tma_load_2d(dst + s * kSub, &tm_c, &full[0], s * 64, row);
           }
-          ptx::tma_load_2d(dst + nsub * kSub, &tm_kr, &full[1], 0, row);
+          if (gt < p.nslot || (ok = wait_b(&aux->empty[w.slot][1], w.ph ^ 1, aux, p.err))) {
+            begun = true;
+            ptx::mbar_arrive_expect_tx(&full[1], (uint32_t)((kQuant ? 1 : nsub - nsub0 + 1) * kSub));
+            if (!kQuant)
+              for (int s = nsub0; s < nsub; ++s) ptx::tma_load_2d(dst + s * kSub, &tm_c, &full[1], s * 64, row);
+            ptx::tma_load_2d(dst + nsub * kSub, &tm_kr, &full[1], 0, row);
+          }
+          if (!begun) break;
           ++gt;
           w.next(p.nslot);
+          if (!ok) break;
           if (i > 0) continue;
           // the query latents, behind the first tile: it has further to come
           if (nseg > 0 && !(ok = wait_b(&aux->q_empty, (nseg - 1) & 1, aux, p.err))) break;
@@ -398,8 +408,9 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
 #pragma unroll
           for (int kt = 0; kt < 4; ++kt)
             ptx::mma_f16_elect(d, a + (uint64_t)(kt * 128), pd + (uint64_t)(kt * 16), id2, kt ? 1u : first);
+          if (2 * c + 2 == (nsub0 + 1) / 2 * 2) ptx::mma_commit_elect(&aux->empty[w.slot][0]);
         }
-        ptx::mma_commit_elect(&aux->empty[w.slot]);
+        ptx::mma_commit_elect(&aux->empty[w.slot][1]);
         ptx::mma_commit_elect(&aux->p_empty[gt & 1]);
         if (i == sg.nt - 1) ptx::mma_commit_elect(&aux->o_full);
       }
@@ -623,9 +634,10 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     while (got) {
       got = advance();
       const uint32_t dst = ptx::smem_u32(ring + w.slot * slot_bytes);
-      if (gt >= p.nslot && !wait_w(&aux->empty[w.slot], w.ph ^ 1, aux, p.err)) break;
+      bool ok = true;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
+        if (gt >= p.nslot && !(ok = wait_w(&aux->empty[w.slot][k], w.ph ^ 1, aux, p.err))) break;
         const int c = g + 2 * k;
         if (c < nch) {
           const bool l = odd && c == nch - 1;
@@ -646,6 +658,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&aux->full[w.slot][k]);
       }
+      if (!ok) break;
       valid = valid_n;
       ++gt;
       w.next(p.nslot);
