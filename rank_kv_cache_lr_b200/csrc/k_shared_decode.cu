@@ -19,6 +19,11 @@
 // tiles cost the tensor pipe 1.4 times the time per token, ~1800 clocks a tile at r = 512, still
 // below the 3300 that a bf16 tile takes from HBM.
 //
+// Measured (r = 512, 28 heads): a bf16 tile every ~3000 clocks (of its chain, fetch 2100, scores
+// 1200, softmax 1000, value mix 1000, two tiles are under way); 16 x 4096 tokens 25 us, of which the
+// first tile's way through the SM takes 6.  An 8-bit tile every ~3800 clocks: its codes' expansion
+// (3000 clocks by 16 warps) takes the fetch's place in the chain; 16 x 32768 tokens 131 us, 2.6 TB/s.
+//
 // Roundings: q~ enters GEMM1 as two bf16 halves, hi and lo = q~ - hi, stacked on N and added in
 // fp32: the scores, and so lse, carry ~16 bits of q~.  The rotary query is bf16 as given.  p enters
 // GEMM2 as one bf16 (2^-8 relative at most, at random over the tokens, below the output's own
@@ -272,12 +277,13 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     ptx::prefetch_tmap(&tm_c);
     ptx::prefetch_tmap(&tm_kr);
   }
+  pdl_wait();       // lengths, pages, rows and q~ may come from the work just before
+  // TMEM is taken after this wait, and dependents are let in once it is held: a CTA that held some
+  // while it waited for this grid could keep this grid from the rest
   if (warp == 1) {
     ptx::tmem_alloc(&aux->tmem_base, 512);
     ptx::tmem_relinquish();
   }
-  pdl_wait();       // lengths, pages, rows and q~ may come from the work just before
-  pdl_trigger();
   if (warp == 0) {
     int chunk;
     const TileRun run = tile_run([&](int b) { return (shared_len(p.row_len, b, p.cap) + kTok - 1) / kTok; }, p.B,
@@ -287,6 +293,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  pdl_trigger();
   const uint32_t tmem = aux->tmem_base;
   TileRun run = aux->run;
   Seg sg;
@@ -717,10 +724,6 @@ __global__ void __launch_bounds__(128)
     ptx::mbar_arrive_expect_tx(&aux.w_full, kb * kWSub);
     for (int k = 0; k < kb; ++k) ptx::tma_load_2d(w_s + k * kWSub, &tm_w, &aux.w_full, h * p.dn + k * 64, i0);
   }
-  if (warp == 1) {
-    ptx::tmem_alloc(&aux.tmem_base, p.tcols);
-    ptx::tmem_relinquish();
-  }
   {
     const int m = threadIdx.x, bs = bs0 + m / p.g;
     long long o = -1;
@@ -730,12 +733,16 @@ __global__ void __launch_bounds__(128)
     }
     aux.at[m] = o;
   }
+  pdl_wait();
+  if (warp == 1) {            // (after the wait, as in k_shared_decode)
+    ptx::tmem_alloc(&aux.tmem_base, p.tcols);
+    ptx::tmem_relinquish();
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = aux.tmem_base;
-  pdl_wait();
   pdl_trigger();
+  const uint32_t tmem = aux.tmem_base;
   const uint64_t limit = tc::wait_limit(p.wait_ns);
   if (warp == 0) {
     if (lane == 0) {
@@ -847,16 +854,16 @@ __global__ void __launch_bounds__(kOutThreads)
       for (int k = 0; k < nsub; ++k)
         ptx::tma_load_2d(w_s + v * p.r * 128 + k * 64 * 128, &tm_w, &aux->w_full, h * p.dv + v * 64, k * 64);
   }
-  if (warp == 1) {
+  if (threadIdx.x < 32) aux->count[threadIdx.x] = 0;
+  pdl_wait();
+  if (warp == 1) {            // (after the wait, as in k_shared_decode)
     ptx::tmem_alloc(&aux->tmem_base, 64);
     ptx::tmem_relinquish();
   }
-  if (threadIdx.x < 32) aux->count[threadIdx.x] = 0;
-  pdl_wait();
-  pdl_trigger();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  pdl_trigger();
   const uint32_t tmem = aux->tmem_base;
   const int nrow = min(p.RB, p.rows - m0);               // rows m0 .. m0 + nrow - 1
   if (warp == 0) {

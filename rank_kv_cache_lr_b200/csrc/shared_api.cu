@@ -84,7 +84,6 @@ lr_status lr_shared_create(const lr_shared_desc* desc, const void* B_k, const vo
   if (!c) return LR_ERR_OOM;
   c->desc = *desc;
   const lr_shared_desc& d = c->desc;
-  c->R_max = d.max_queries * d.n_q_heads;
   c->pps = d.capacity / kPageTokens;
   c->n_pages = d.n_pages ? d.n_pages : d.batch * c->pps;
   const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt((float)(d.dim_nope + d.dim_rope));

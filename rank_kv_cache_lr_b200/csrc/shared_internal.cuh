@@ -9,7 +9,6 @@
 // Rows of the stored arrays are page * 128 + token % 128, page = table[b][token / 128].
 struct lr_shared {
   lr_shared_desc desc;
-  int R_max;             // query rows per sequence at max_queries (max_queries * Hq)
   int pps, n_pages;      // pages per sequence, pages in the pool
   float scale_log2;      // softmax_scale * log2(e)
   int num_sms = 148, device = 0;

@@ -117,15 +117,14 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A tiled map, 128-byte swizzled unless told otherwise.
+// A tiled map with 128-byte swizzle over 16-bit elements.
 inline bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, int rank, const cuuint64_t* dims,
-                     const cuuint64_t* strides, const cuuint32_t* box,
-                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                     const cuuint64_t* strides, const cuuint32_t* box) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = fn(m, type, rank, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

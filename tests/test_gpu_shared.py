@@ -385,6 +385,25 @@ def test_waits_that_give_up_are_reported_and_the_cache_recovers(lib, r, bits):
     m.check_decode(q, *m.decode(q))
 
 
+def test_decodes_of_two_caches_at_once(lib):
+    """Caches own their scratch: decodes of two of them may overlap, on two streams."""
+    import torch
+    ms = [Layer(lib, lens, hq=28, hkv=28, r=r, bits=bits) for lens, r, bits in (([900, 31, 400], 512, 0), ([700, 1200], 320, 8))]
+    qs, streams = [m.query(1) for m in ms], [torch.cuda.Stream() for _ in ms]
+    want = [m.decode(q) for m, q in zip(ms, qs)]
+    lens = [i32(m.lens) for m in ms]
+    got = [[(torch.zeros_like(w[0]), torch.zeros_like(w[1])) for _ in range(8)] for w in want]
+    torch.cuda.synchronize()
+    for n in range(8):
+        for m, q, s, l, g in zip(ms, qs, streams, lens, got):
+            lib.lr_shared_decode(m.cache, q, l, *g[n], stream=s)
+    torch.cuda.synchronize()
+    for m, q, w, g in zip(ms, qs, want, got):
+        assert lib.lr_shared_device_error(m.cache) == 0
+        m.check_decode(q, *w)
+        assert all(torch.equal(o, w[0]) and torch.equal(e, w[1]) for o, e in g)
+
+
 # ---------------------------------------------------------------------------
 # expansion
 # ---------------------------------------------------------------------------
@@ -446,6 +465,54 @@ def test_expand_outside_the_cache_writes_nothing(lib):
     want = m.c64[[0, 1, 254, 255]] @ m.Bk64
     assert np.allclose(got[3:7].reshape(4, -1), want, atol=0.02)
     assert np.array_equal(f64(kr)[3:7], m.kr64[[0, 1, 254, 255]])
+
+
+@pytest.mark.parametrize("bits", [0, 8])
+def test_expand_captured_and_replayed_with_other_parts(lib, bits):
+    import torch
+    m = Layer(lib, [300, 513, 40], hq=3, hkv=3, r=192, bits=bits)
+    cu, start = i32([0, 0, 0, 0]), i32([0, 0, 0])
+    k, v, kr = (torch.zeros((600, *x), dtype=torch.bfloat16, device="cuda") for x in ((3, 128), (3, 128), (64,)))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lib.lr_shared_expand(m.cache, cu, k, v, kr, start=start)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.lr_shared_expand(m.cache, cu, k, v, kr, start=start)
+    for first, lens in (([0, 0, 0], [300, 260, 40]), ([299, 100, 39], [1, 400, 1]), ([0, 0, 5], [0, 0, 3])):
+        start.copy_(i32(first)), cu.copy_(i32(np.concatenate([[0], np.cumsum(lens)])))
+        for x in (k, v, kr):
+            x.fill_(55.0)
+        g.replay()
+        check_expand(m, first, lens, k, v, kr)
+
+
+@pytest.mark.parametrize("bits", [0, 8])
+def test_expansions_at_once_and_one_that_gives_up(lib, bits):
+    """Two caches expanded on two streams again and again; then waits that give up are reported, and
+    the cache recovers."""
+    import torch
+    ms = [Layer(lib, lens, hq=4, hkv=4, r=r, dn=64, dv=64, bits=bits) for lens, r in (([700, 300], 64), ([1, 129, 500], 512))]
+    outs = [run_expand(m, None, m.lens) for m in ms]
+    streams = [torch.cuda.Stream() for _ in ms]
+    got = [[torch.zeros_like(x) for x in o[:3]] for o in outs]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for m, s, o, g in zip(ms, streams, outs, got):
+            lib.lr_shared_expand(m.cache, o[3], *g, stream=s)
+    torch.cuda.synchronize()
+    for m, o, g in zip(ms, outs, got):
+        check_expand(m, [0] * len(m.lens), m.lens, *o[:3])
+        assert all(torch.equal(x[:sum(m.lens)], y[:sum(m.lens)]) for x, y in zip(g, o))
+    m = ms[1]
+    lib.lr_shared_set_wait_limit(m.cache, 4)
+    lib.lr_shared_expand(m.cache, outs[1][3], *got[1])
+    assert lib.lr_shared_device_error(m.cache) == lib.LR_ERR_TIMEOUT
+    assert lib.lr_shared_device_error(m.cache) == 0
+    lib.lr_shared_set_wait_limit(m.cache, 0)
+    check_expand(m, [0] * 3, m.lens, *run_expand(m, None, m.lens)[:3])
 
 
 # ---------------------------------------------------------------------------
@@ -589,6 +656,18 @@ def test_attn_captured_and_replayed_with_other_lengths(lib):
         out.fill_(33.0), lse.fill_(33.0)
         g.replay()
         check_attn(q, k, kr, v, nq, nk, True, 192 ** -0.5, out, lse)
+
+
+def test_attn_waits_that_give_up_are_reported(lib):
+    nq, nk = [300, 40], [700, 129]
+    cache, q, k, kr, v, cu = attn_case(lib, nq, nk)
+    import torch
+    out = torch.zeros((q.shape[0], 4, 128), dtype=torch.bfloat16, device="cuda")
+    lib.lr_shared_set_wait_limit(cache, 4)
+    lib.lr_shared_attn(cache, q, k, kr, v, cu[0], cu[1], out)
+    assert lib.lr_shared_device_error(cache) == lib.LR_ERR_TIMEOUT
+    lib.lr_shared_set_wait_limit(cache, 0)
+    check_attn(q, k, kr, v, nq, nk, True, 192 ** -0.5, *run_attn(lib, cache, q, k, kr, v, cu, True))
 
 
 # ---------------------------------------------------------------------------
