@@ -277,10 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (j == ntt) break;
         // S(j): the query boxes are dn, then the rotary columns (dn and dn + 64 are box borders).
-        // Tile 1 starts when tile 0 is half through its softmax: in step, both would want the
-        // tensor pipe at one time and the exponentials at another.
+        // Over many key tiles, tile 1 starts when tile 0 is half through its softmax: in step, both would
+        // want the tensor pipe at one time and the exponentials at another (2 x 8192: 4% slower).  Over a
+        // few the later start costs more (seven prompts of up to 400 tokens: 28.8 us against 26.7).
         if (!k_in && !(ok = wait_w(&aux->k_full[s], ph, aux, p.err))) break;
-        if (t == 1 && j < nt[0] && !(ok = wait_w(&aux->p_full[0][0][s], ph, aux, p.err))) break;
+        if (t == 1 && ntk > 4 && j < nt[0] && !(ok = wait_w(&aux->p_full[0][0][s], ph, aux, p.err))) break;
         ptx::tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 3; ++c)
