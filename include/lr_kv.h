@@ -385,7 +385,8 @@ lr_status lr_shared_read(lr_shared* cache, const int32_t* cu, const int32_t* sta
  *   tokens of each sequence, the new ones included (clamped to [0, capacity]).  Query token s
  *   sees tokens t < row_len[b] - (n_tokens - 1 - s).  out [B][n_tokens][Hq][dv] bf16, lse
  *   [B][n_tokens][Hq] fp32 (natural log) or NULL.  A query that sees no token gets out = 0,
- *   lse = -inf.  What pages hold behind row_len has no influence.  n_tokens > max_queries:
+ *   lse = -inf.  What pages hold behind row_len has no influence; a visible token's infinity or
+ *   NaN also reaches the call's query tokens that do not see it.  n_tokens > max_queries:
  *   LR_ERR_CAPACITY. */
 lr_status lr_shared_decode(lr_shared* cache, const void* q, int32_t n_tokens, const int32_t* row_len, void* out,
                            float* lse, void* stream);
@@ -401,7 +402,8 @@ lr_status lr_shared_decode(lr_shared* cache, const void* q, int32_t n_tokens, co
  *   causal = 1: query i of n sees keys j <= i + m - n of its m keys (the queries are the last n
  *   tokens); 0: all m.  out [total_q][Hq][dv] bf16 (32-byte aligned), lse [total_q][Hq] fp32 or
  *   NULL; a query that sees no key gets out = 0, lse = -inf; rows past cu_q[n_seq] are left as
- *   they are.  Partial results over several key ranges join by their lse. */
+ *   they are.  Partial results over several key ranges join by their lse.  An infinity or NaN in
+ *   a value also reaches queries of its sequence that do not see that key. */
 lr_status lr_shared_expand(lr_shared* cache, const int32_t* cu, const int32_t* start, int32_t total, void* k, void* v,
                            void* kr, void* stream);
 lr_status lr_shared_attn(lr_shared* cache, const void* q, const void* k, const void* kr, const void* v,

@@ -90,39 +90,12 @@ __device__ __forceinline__ bool next_seg(TileRun* run, const DecArgs& p, Seg* s)
   return false;
 }
 
-// Two e4m3 codes as bf16 before their scale: a code's sign, exponent and mantissa bits placed in
-// a bf16 stand for its value times 2^-120 (subnormals included).  sel picks bytes (i, j) as
-// halves with the sign replicated above each (selector bit 3).
-template <uint32_t kSel>
-__device__ __forceinline__ __nv_bfloat162 place2(uint32_t w) {
-  uint32_t a;
-  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(a) : "r"(w), "n"(kSel));
-  a = (a << 4) & 0x87F087F0u;
-  return *reinterpret_cast<const __nv_bfloat162*>(&a);
-}
 // Sixteen codes of one token (their words in the order in which they are stored), times 2^e, to
-// two 16-byte columns of a swizzled row: w.x, w.y to address a0 and w.z, w.w to a1.  e <= 7
-// (exponent byte at most 134): 2^(120 + e) is a bf16, so one exact product; above, two products
-// 2^(b1 - 127) 2^(b2 - 127) with 120 folded into the first; byte 255 (a group that held a NaN or an
-// infinity) is NaN.
+// two 16-byte columns of a swizzled row: w.x, w.y to address a0 and w.z, w.w to a1.
 __device__ __forceinline__ void expand16(const uint4& w, uint32_t eb, uint32_t a0, uint32_t a1) {
-  const uint32_t b1 = min(eb + 120u, 254u);
-  const uint32_t h1 = eb == 255u ? 0x7FC07FC0u : b1 * 0x00800080u;
-  const __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162*>(&h1);
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  __nv_bfloat162 x[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x[2 * k] = __hmul2(place2<0x9180>(in[k]), s1);
-    x[2 * k + 1] = __hmul2(place2<0xB3A2>(in[k]), s1);
-  }
-  if (__any_sync(0xffffffffu, eb > 134u)) {
-    const uint32_t h2 = (eb + 247u - b1) * 0x00800080u;
-    const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&h2);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = __hmul2(x[k], s2);
-  }
-  const uint32_t* o = reinterpret_cast<const uint32_t*>(x);
+  uint32_t o[8];
+  shared_expand<4>(in, eb, o);
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                : "memory");
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])

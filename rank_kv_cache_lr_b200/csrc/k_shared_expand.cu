@@ -19,7 +19,6 @@
 #include "shared_internal.cuh"
 #include "tc_common.cuh"
 
-#include <cuda_fp8.h>
 
 #include <algorithm>
 
@@ -387,18 +386,12 @@ __global__ void __launch_bounds__(exp_threads<kQuant>(), 1)
         for (int k = 0; k < 4; ++k) {
           const int idx = k * 256 + tid, tok = (idx >> 2) & 127, s = s0 + (idx >> 9), col = idx & 3;
           if ((idx >> 9) < ns) {
-            const float sc = shared_pow2(eb[k]);
             const uint32_t cw[4] = {cd[k].x, cd[k].y, cd[k].z, cd[k].w};
+            uint32_t all[8];
+            shared_expand<4>(cw, eb[k], all);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              uint32_t o[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t two = (cw[2 * h + (e >> 1)] >> (16 * (e & 1))) & 0xFFFFu;
-                const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-                o[e] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
+              const uint32_t* o = all + 4 * h;
               const uint32_t a = ptx::smem_u32(a_s + s * kSub + tok * 128) + (((col * 2 + h) ^ (tok & 7)) << 4);
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(o[0]), "r"(o[1]), "r"(o[2]),
                            "r"(o[3])

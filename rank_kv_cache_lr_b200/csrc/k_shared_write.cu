@@ -27,6 +27,11 @@ __device__ __forceinline__ uint32_t warp_max4(uint32_t v) {   // over the 4 lane
   return max(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
+__device__ __forceinline__ __nv_bfloat162 magnitudes(uint32_t two) {
+  two &= 0x7FFF7FFFu;
+  return *reinterpret_cast<const __nv_bfloat162*>(&two);
+}
+
 // Exponent byte of a group whose largest |element| has the bf16 magnitude bits `top`.
 // 448 = 1.75 * 2^8: a maximum m * 2^x takes e = x - 8 while m <= 1.75 (mantissa bits <= 96).
 // e >= -100 keeps 2^-e and every product inside fp32's and bf16's normal range.
@@ -103,20 +108,23 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_append(const AppendArgs 
       const uint32_t ww[4] = {w[u][k].x, w[u][k].y, w[u][k].z, w[u][k].w};
       uint32_t top = 0;
       if (in) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, max(ww[e] & 0x7FFFu, (ww[e] >> 16) & 0x7FFFu));
+        // magnitudes compared as pairs of bf16 (NaN wins)
+        const __nv_bfloat162 m =
+            __hmax2_nan(__hmax2_nan(magnitudes(ww[0]), magnitudes(ww[1])), __hmax2_nan(magnitudes(ww[2]), magnitudes(ww[3])));
+        const uint32_t mb = *reinterpret_cast<const uint32_t*>(&m);
+        top = max(mb & 0xFFFFu, mb >> 16);
       }
       top = warp_max4(top);
       const uint32_t eb = shared_quant_exp(top);
-      const float inv = __uint_as_float((254u - min(eb, 247u)) << 23);   // 2^-e
+      // 2^-e, twice: the products are exact in bf16, but for some below 2^-126, whose code is 0 anyway
+      const uint32_t ib = (254u - min(eb, 247u)) * 0x00800080u;
+      const __nv_bfloat162 inv = *reinterpret_cast<const __nv_bfloat162*>(&ib);
       if (in) {
         uint32_t o[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float2 p = make_float2(__uint_as_float(ww[2 * h] << 16) * inv,
-                                       __uint_as_float(ww[2 * h] & 0xFFFF0000u) * inv);
-          const float2 q = make_float2(__uint_as_float(ww[2 * h + 1] << 16) * inv,
-                                       __uint_as_float(ww[2 * h + 1] & 0xFFFF0000u) * inv);
+          const float2 p = __bfloat1622float2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&ww[2 * h]), inv));
+          const float2 q = __bfloat1622float2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&ww[2 * h + 1]), inv));
           const uint32_t lo = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
           const uint32_t hi = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
           o[h] = lo | (hi << 16);
@@ -198,16 +206,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_read(const ReadArgs a) {
         dst[v] = w[u][k];
         continue;
       }
-      const float sc = shared_pow2(w[u][k].z);
+      const uint32_t codes[2] = {w[u][k].x, w[u][k].y};
       uint32_t o[4];
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const uint32_t two = ((h < 2 ? w[u][k].x : w[u][k].y) >> (16 * (h & 1))) & 0xFFFFu;
-        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-        const float2 f = __half22float2(__half2(hr));
-        const __nv_bfloat162 bb = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-        o[h] = *reinterpret_cast<const uint32_t*>(&bb);
-      }
+      shared_expand<2>(codes, w[u][k].z, o);
       dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
     }
     if (lane < (a.dr >> 3)) reinterpret_cast<uint4*>(a.kr + i * a.dr)[lane] = y[u];

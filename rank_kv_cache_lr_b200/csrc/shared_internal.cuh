@@ -62,9 +62,38 @@ __host__ __device__ __forceinline__ long long shared_scale_index(long long row, 
   return ((((row >> 7) * ((r + 127) >> 7) + (g >> 2)) << 7) + (row & 127)) * 4 + (g & 3);
 }
 
-// 2^(byte - 127) as a float; NaN for 255.  Bytes are 27..247 (shared_quant).
-__device__ __forceinline__ float shared_pow2(uint32_t byte) {
-  return __uint_as_float(byte == 255u ? 0x7FC00000u : byte << 23);
+// Two e4m3 codes as bf16 before their scale: a code's sign, exponent and mantissa bits placed in
+// a bf16 stand for its value times 2^-120 (subnormals included).  sel picks bytes (i, j) as
+// halves with the sign replicated above each (selector bit 3).
+template <uint32_t kSel>
+__device__ __forceinline__ __nv_bfloat162 shared_place2(uint32_t w) {
+  uint32_t a;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(a) : "r"(w), "n"(kSel));
+  a = (a << 4) & 0x87F087F0u;
+  return *reinterpret_cast<const __nv_bfloat162*>(&a);
+}
+// 4 N codes of one group to bf16: times 2^e, byte eb (27..247, or 255).  e <= 7 (byte at most 134):
+// 2^(120 + e) is a bf16, so one exact product; above, two products 2^(b1 - 127) 2^(b2 - 127) with
+// 120 folded into the first; byte 255 (a group that held a NaN or an infinity) is NaN.
+template <int N>
+__device__ __forceinline__ void shared_expand(const uint32_t (&in)[N], uint32_t eb, uint32_t (&out)[2 * N]) {
+  const uint32_t b1 = min(eb + 120u, 254u);
+  const uint32_t h1 = eb == 255u ? 0x7FC07FC0u : b1 * 0x00800080u;
+  const __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162*>(&h1);
+  __nv_bfloat162 x[2 * N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    x[2 * k] = __hmul2(shared_place2<0x9180>(in[k]), s1);
+    x[2 * k + 1] = __hmul2(shared_place2<0xB3A2>(in[k]), s1);
+  }
+  if (eb > 134u) {
+    const uint32_t h2 = (eb + 247u - b1) * 0x00800080u;
+    const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&h2);
+#pragma unroll
+    for (int k = 0; k < 2 * N; ++k) x[k] = __hmul2(x[k], s2);
+  }
+#pragma unroll
+  for (int k = 0; k < 2 * N; ++k) out[k] = *reinterpret_cast<const uint32_t*>(&x[k]);
 }
 
 // Work of the paged kernels: the tiles of all sequences in order, cut into equal runs, run x for CTA column x of X.  A run may span several sequences, and a sequence
