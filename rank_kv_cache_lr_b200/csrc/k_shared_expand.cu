@@ -365,25 +365,26 @@ __global__ void __launch_bounds__(exp_threads<kQuant>(), 1)
       if (!w.fresh()) continue;
       ++nt;
       const long long row0 = aux->tiles[w.k].pool;
-      // two 64-rank parts at a time: a thread's 16-byte code runs are in flight together
-      for (int s0 = 0; s0 < nsub; s0 += 2) {
-        const int ns = min(2, nsub - s0);
-        uint4 cd[4];
-        uint32_t eb[4];
+      const uint8_t* const codes = p.codes + shared_code_page(row0 >> 7, p.r);
+      const uint8_t* const scale = p.scale + shared_scale_page(row0 >> 7, p.r);
+      // four 64-rank parts at a time: a thread's 16-byte code runs are in flight together
+      for (int s0 = 0; s0 < nsub; s0 += 4) {
+        const int ns = min(4, nsub - s0);
+        uint4 cd[8];
+        uint32_t eb[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const int idx = k * 256 + tid, tok = (idx >> 2) & 127, s = s0 + (idx >> 9), col = idx & 3;
           if ((idx >> 9) < ns) {
-            const long long row = row0 + tok;
-            cd[k] = __ldg(reinterpret_cast<const uint4*>(p.codes + shared_code_index(row, p.r, s * 64 + col * 16)));
-            eb[k] = __ldg(p.scale + shared_scale_index(row, p.r, s * 2 + (col >> 1)));
+            cd[k] = __ldg(reinterpret_cast<const uint4*>(codes + shared_code_index(tok, p.r, s * 64 + col * 16)));
+            eb[k] = __ldg(scale + shared_scale_index(tok, s * 2 + (col >> 1)));
           }
         }
         if (nt > 1)
           for (int q = 0; q < ns && ok; ++q) ok = wait_w(&aux->a_empty[s0 + q], nt & 1, aux, p.err);
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
           const int idx = k * 256 + tid, tok = (idx >> 2) & 127, s = s0 + (idx >> 9), col = idx & 3;
           if ((idx >> 9) < ns) {
             const uint32_t cw[4] = {cd[k].x, cd[k].y, cd[k].z, cd[k].w};

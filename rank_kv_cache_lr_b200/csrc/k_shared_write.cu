@@ -85,6 +85,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_append(const AppendArgs 
   for (int u = 0; u < T; ++u) {
     if (b[u] < 0 || b[u] >= a.B || t[u] < 0 || t[u] >= a.cap) continue;   // a padded row: writes nothing
     const long long row = a.map.row(b[u], t[u]);
+    const int tok = (int)(row & 127);
+    uint8_t* const codes = static_cast<uint8_t*>(a.c) + shared_code_page(row >> 7, a.r);
+    uint8_t* const scale = a.scale + shared_scale_page(row >> 7, a.r);
     if (has) {
       float x0 = __bfloat162float(x[u][0]), x1 = __bfloat162float(x[u][1]);
       if (a.rope_cs) {
@@ -129,9 +132,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_append(const AppendArgs 
           const uint32_t hi = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
           o[h] = lo | (hi << 16);
         }
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.c) + shared_code_index(row, a.r, v * 8)) =
-            make_uint2(o[0], o[1]);
-        if ((lane & 3) == 0) a.scale[shared_scale_index(row, a.r, v >> 2)] = (uint8_t)eb;
+        *reinterpret_cast<uint2*>(codes + shared_code_index(tok, a.r, v * 8)) = make_uint2(o[0], o[1]);
+        if ((lane & 3) == 0) scale[shared_scale_index(tok, v >> 2)] = (uint8_t)eb;
       }
     }
   }
@@ -177,6 +179,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_read(const ReadArgs a) {
   for (int u = 0; u < T; ++u) {
     row[u] = __shfl_sync(0xffffffffu, found, u);
     if (row[u] < 0) continue;
+    const int tok = (int)(row[u] & 127);
+    const uint8_t* const codes = static_cast<const uint8_t*>(a.c) + shared_code_page(row[u] >> 7, a.r);
+    const uint8_t* const scale = a.scale + shared_scale_page(row[u] >> 7, a.r);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int v = k * 32 + lane;
@@ -184,11 +189,10 @@ __global__ void __launch_bounds__(32 * kWarps) k_shared_read(const ReadArgs a) {
       if (!kQuant) {
         w[u][k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.c) + row[u] * a.r) + v);
       } else {
-        const uint2 q =
-            __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.c) + shared_code_index(row[u], a.r, v * 8)));
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(codes + shared_code_index(tok, a.r, v * 8)));
         w[u][k].x = q.x;
         w[u][k].y = q.y;
-        w[u][k].z = __ldg(a.scale + shared_scale_index(row[u], a.r, v >> 2));
+        w[u][k].z = __ldg(scale + shared_scale_index(tok, v >> 2));
       }
     }
     if (lane < (a.dr >> 3)) y[u] = __ldg(reinterpret_cast<const uint4*>(a.kr_pool + row[u] * a.dr) + lane);

@@ -50,16 +50,20 @@ inline RowMap row_map(const lr_shared* c) {
 // [128 tokens][128 codes] (a last chunk of 64 ranks: [128][64]), so that a tile's chunk is one
 // contiguous copy of 16 (8) KB.  (Boxes of 128 bytes from 512-byte rows took 1.0 us each with
 // four in flight, 16 GB/s an SM.)
-__host__ __device__ __forceinline__ long long shared_code_index(long long row, int r, int i) {
+__host__ __device__ __forceinline__ long long shared_code_page(long long page, int r) { return page * (128ll * r); }
+__host__ __device__ __forceinline__ uint32_t shared_code_index(int tok, int r, int i) {   // in its page
   const int c = i >> 7, left = r - (c << 7), w = left < 128 ? left : 128;
-  return (row >> 7) * (128ll * r) + ((long long)c << 14) + (row & 127) * w + (i & 127);
+  return (uint32_t)((c << 14) + tok * w + (i & 127));
 }
 
 // The exponent byte (2^(byte - 127); 255: a group that held a NaN or an infinity) of ranks
 // 32 g .. 32 g + 31 of a stored row.  A page's bytes of 128 ranks are contiguous, so that a
 // tile side's scales are one 512-byte copy.
-__host__ __device__ __forceinline__ long long shared_scale_index(long long row, int r, int g) {
-  return ((((row >> 7) * ((r + 127) >> 7) + (g >> 2)) << 7) + (row & 127)) * 4 + (g & 3);
+__host__ __device__ __forceinline__ long long shared_scale_page(long long page, int r) {
+  return page * ((r + 127) >> 7) * 512;
+}
+__host__ __device__ __forceinline__ uint32_t shared_scale_index(int tok, int g) {   // in its page
+  return (uint32_t)((g >> 2) * 512 + tok * 4 + (g & 3));
 }
 
 // Two e4m3 codes as bf16 before their scale: a code's sign, exponent and mantissa bits placed in
