@@ -57,14 +57,14 @@ struct AttArgs {
 
 // Barriers (arrival count; who arrives -> who waits).  [2]: by the parity of the key tile, so that a
 // waiter may be one key tile behind the arriver.
-//   q_full            1 + tx   producer -> MMA
+//   q_full[t]         1 + tx   producer -> MMA
 //   k_full, v_full[2] 1 + tx   producer -> MMA (values also -> softmax, which clears what lies behind the last key)
 //   s_full[t][2]      1        MMA commit of S of tile t -> its softmax warps, producer (the keys' slots)
 //   p_full[t][h][2]   4        softmax warps (P of keys 64 h .. 64 h + 63 stored) -> MMA
 //   pv_done[t][h][2]  1        MMA commit of PV of key half h -> producer (the values' slots), epilogue
 //   done              2        final commits of both MMA warps
 struct Aux {
-  uint64_t q_full, k_full[2], v_full[2], s_full[2][2], p_full[2][2][2], pv_done[2][2][2], done;
+  uint64_t q_full[2], k_full[2], v_full[2], s_full[2][2], p_full[2][2][2], pv_done[2][2][2], done;
   uint32_t tmem_base;
   int abort_flag;
   int b, pair;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (threadIdx.x == 0) {
-    ptx::mbar_init(&aux->q_full, 1);
+    for (int t = 0; t < 2; ++t) ptx::mbar_init(&aux->q_full[t], 1);
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&aux->k_full[s], 1);
       ptx::mbar_init(&aux->v_full[s], 1);
@@ -170,11 +170,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) {
       // ------------------------------------------------------------- TMA producer
       if (lane == 0 && ntk > 0) {
-        const int tiles = rq.n - q0 > 128 ? 2 : 1;
-        ptx::mbar_arrive_expect_tx(&aux->q_full, (uint32_t)(tiles * nqb * kBox));
-        for (int t = 0; t < tiles; ++t)
+        auto queries = [&](int t) {
+          ptx::mbar_arrive_expect_tx(&aux->q_full[t], (uint32_t)(nqb * kBox));
           for (int c = 0; c < nqb; ++c)
-            ptx::tma_load_3d(q_s + (t * nqb + c) * kBox, &tm_q, &aux->q_full, c * 64, head, rq.first + q0 + t * 128);
+            ptx::tma_load_3d(q_s + (t * nqb + c) * kBox, &tm_q, &aux->q_full[t], c * 64, head, rq.first + q0 + t * 128);
+        };
+        queries(0);                        // (the second tile's come behind the first keys)
+        const bool two = rq.n - q0 > 128;
         // Slots are taken and given back in one order, K0 V0 K1 V1 ..., so V_j goes where K_{j-1} was (free
         // early: its scores are done) and K_{j+1} partly where V_{j-1} was, half by half.
         bool ok = true;
@@ -211,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c < nkb - 1) ptx::tma_load_2d(dst, &tm_k, &aux->k_full[s], kvh * p.dn + c * 64, row);
             else ptx::tma_load_2d(dst, &tm_kr, &aux->k_full[s], 0, row);
           }
+          if (j == 0 && two) queries(1);
           for (int c = 0; c < nvb && ok; ++c) {
             uint8_t* dst = slot();
             if (!ok) break;
@@ -224,7 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // every copy this thread issued has landed before the CTA can exit
-        drain_wait(&aux->q_full, 0);
+        drain_wait(&aux->q_full[0], 0);
+        if (two) drain_wait(&aux->q_full[1], 0);
         for (int j = max(0, nk - 2); j < nk; ++j) drain_wait(&aux->k_full[j & 1], (j >> 1) & 1);
         for (int j = max(0, nv - 2); j < nv; ++j) drain_wait(&aux->v_full[j & 1], (j >> 1) & 1);
       }
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d_s = uniform(tmem + t * 128);
       int kp = 0;                                      // ring slot of key tile j
       uint64_t vb[2] = {vd, vd};                       // halves of value tile j - 1
-      bool ok = wait_w(&aux->q_full, 0, aux, p.err);
+      bool ok = ntt == 0 || wait_w(&aux->q_full[t], 0, aux, p.err);
 #pragma unroll 1
       for (int j = 0; j <= ntt && ok; ++j) {
         const int s = j & 1, ph = (j >> 1) & 1;

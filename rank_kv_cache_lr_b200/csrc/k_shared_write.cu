@@ -11,7 +11,7 @@
 // warp owns a token: its lanes hold 8 consecutive elements each (16 bytes in, 16 or 8 out), so
 // every access is a full coalesced run and a group's maximum is two shuffles within 4 lanes.  With
 // many tokens a warp owns two of them, all loads first (65536 tokens of r = 512 in 8 bits, written and
-// read back: 59 us with one token a warp, 53 with two, 55 with four or eight; 4.4 TB/s).
+// read back: 53 us with one token a warp, 50 with two, 56 with four; 4.8 TB/s).
 #include "shared_internal.cuh"
 
 #include <cuda_fp8.h>
