@@ -48,7 +48,7 @@ constexpr float kNoMax = -1e30f;
 struct AttArgs {
   unsigned long long wait_ns;
   const int32_t* cu_q; const int32_t* cu_k;
-  int nseq, total_q, total_k, Hq, g, dn, dv, dq, causal, slots, ring;   // slots: tile pairs a head; ring: 16 KB slots for keys and values
+  int nseq, total_q, total_k, Hq, g, dn, dv, dq, causal, stagger, slots, ring;   // slots: tile pairs a head; ring: 16 KB slots for keys and values
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
@@ -281,11 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (j == ntt) break;
         // S(j): the query boxes are dn, then the rotary columns (dn and dn + 64 are box borders).
-        // Over many key tiles, tile 1 starts when tile 0 is half through its softmax: in step, both would
-        // want the tensor pipe at one time and the exponentials at another (2 x 8192: 4% slower).  Over a
-        // few the later start costs more (seven prompts of up to 400 tokens: 28.8 us against 26.7).
+        // Where all CTAs run at once, over many key tiles, tile 1 starts when tile 0 is half through its
+        // softmax: in step, both would want the tensor pipe at one time and the exponentials at another
+        // (512 new tokens over 4096: 100 us against 116; over 32768: 637 against 675; 1280 over 16000: 320
+        // against 350).  In several waves the tiles drift apart by themselves and the wait costs (prompts of
+        // 4096: 158 us with it, 141 without; 16384: 2.2 and 2.1 ms), and so it does over a few key tiles
+        // (seven prompts of up to 400 tokens: 28.8 and 26.7 us).
         if (!k_in && !(ok = wait_w(&aux->k_full[s], ph, aux, p.err))) break;
-        if (t == 1 && ntk > 4 && j < nt[0] && !(ok = wait_w(&aux->p_full[0][0][s], ph, aux, p.err))) break;
+        if (t == 1 && p.stagger && ntk > 4 && j < nt[0] && !(ok = wait_w(&aux->p_full[0][0][s], ph, aux, p.err))) break;
         ptx::tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 3; ++c)
@@ -471,6 +474,7 @@ cudaError_t launch_shared_attn(lr_shared* c, const void* q, const void* k, const
   const long long slots = (long long)total_q / 256 + std::min(nseq, total_q);
   if (slots * a.Hq > 0x7FFFFFFF) return cudaErrorNotSupported;
   a.slots = (int)slots;
+  a.stagger = ((long long)total_q + 255) / 256 * a.Hq <= c->num_sms;
   CUtensorMap tq, tk, tkr, tv;
   if (total_k == 0) k = kr = v = q;      // no key tile is ever loaded; the maps need an address
   const cuuint64_t rows = std::max(total_k, 1);
