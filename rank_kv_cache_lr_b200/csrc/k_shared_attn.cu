@@ -354,9 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float mx[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        mx[c] = __uint_as_float(v[c][0]);
+        mx[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
 #pragma unroll
-        for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(v[c][e]));
+        for (int e = 2; e < 32; e += 2) mx[c] = ptx::max3(mx[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
       if (__any_sync(0xffffffffu, top > m + kLazy)) {
