@@ -17,9 +17,10 @@
 // (2560 clocks at 192 + 128) against 2048 clocks of exponentials on the same SM.  Measured: ~4300
 // clocks (per query tile: 1200 from the first MMA of S to its softmax, 1700 of softmax, 300 to
 // the last MMA of PV, and the keys of the next tile, which wait on values of the last).  Two
-// sequences of 8192 tokens, 28 heads, causal: 1.07 ms, 1.12 PFLOP/s at the card's power limit
-// (1.65 GHz); with two fixed stages for keys and one for values 1.22 ms; with a barrier per
-// 64-column box of keys 1.24 ms (a test between MMAs costs more than the earlier start gains).
+// sequences of 8192 tokens, 28 heads, causal: 1.07 ms, 1.12 PFLOP/s in a short burst, 1.27 ms run
+// continuously, at the card's power limit (1000 W, 1.65 GHz).  In bursts, with two fixed stages for
+// keys and one for values 1.22 ms; with a barrier per 64-column box of keys 1.24 ms (a test between
+// MMAs costs more than the earlier start gains).
 //
 // Roundings: P to bf16 (half a step, 2^-8 relative, at random over the keys, below the output's
 // own); sums of the unrounded weights in fp32; the output once.  A running max may be stale by

@@ -12,7 +12,8 @@
 // and each 64-rank part of the next is fetched as soon as the last block has used the old one.
 // Two TMEM accumulators let the epilogue of one block run under the MMAs of the next; it stores 32
 // bytes per lane, whole sectors.  32768 tokens of r = 512, 28 heads of 128 + 128: 206 us, 1.17
-// PFLOP/s at the card's power limit (1.6 GHz; 259 us with single CTAs on the same card).
+// PFLOP/s in a short burst (259 us with single CTAs), 246 us run continuously: the card's power limit
+// (1000 W, 1.6 GHz) then sets the pace, with 2 TB/s of writes beside the tensor pipe.
 //
 // 8-bit latents are expanded to bf16 (exactly) by eight warps straight from global memory into
 // the swizzled tile, once per tile; the MMAs then run as for bf16.
