@@ -94,17 +94,18 @@ __device__ __forceinline__ bool wait_x(uint64_t* bar, uint32_t parity, Aux* aux,
   return __all_sync(0xffffffffu, ok);
 }
 
-// Positions [lo, hi) of sequence b to expand, inside the cache; position t goes to row t + off.
+// Positions [lo, hi) of sequence b to expand, inside the cache and the results (so that there are no
+// more tiles than the host reckoned with, whatever cu holds); position t goes to row t + off.
 struct Span {
   int lo, hi;
   long long off;
 };
 __device__ __forceinline__ Span span_at(const ExpArgs& p, int b) {
-  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), st = p.start ? __ldg(p.start + b) : 0;
+  const long long c0 = __ldg(p.cu + b), c1 = min(__ldg(p.cu + b + 1), p.total), st = p.start ? __ldg(p.start + b) : 0;
   Span s;
-  s.lo = min(max(st, 0), p.cap);
-  s.hi = (int)min(max((long long)st + ((long long)c1 - c0), (long long)s.lo), (long long)p.cap);
-  s.off = (long long)c0 - st;
+  s.off = c0 - st;
+  s.lo = (int)min(max(max(c0, 0ll) - s.off, 0ll), (long long)p.cap);
+  s.hi = (int)min(max(c1 - s.off, (long long)s.lo), (long long)p.cap);
   return s;
 }
 __device__ __forceinline__ int span_tiles(const ExpArgs& p, int b) {

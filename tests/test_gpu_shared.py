@@ -467,6 +467,20 @@ def test_expand_outside_the_cache_writes_nothing(lib):
     assert np.array_equal(f64(kr)[3:7], m.kr64[[0, 1, 254, 255]])
 
 
+def test_expand_of_fewer_rows_than_the_parts_hold(lib):
+    """total bounds the rows, however many tokens cu speaks of (here 2 million, in a few zero pages)."""
+    import torch
+    d = lib.make_shared_desc(8, 1, 1, 64, 32, 64, 64, 1 << 18, n_pages=4)
+    cache = lib.lr_shared_create(d, bf16(np.ones((64, 64))), bf16(np.ones((64, 64))))
+    cu = i32(np.arange(9) << 18)
+    k, v, kr = (torch.full((n, *x), 55.0, dtype=torch.bfloat16, device="cuda") for n, x in
+                ((20001, (1, 64)), (20001, (1, 64)), (20001, (32,))))
+    lib.lr_shared_expand(cache, cu, k[:20000], v[:20000], kr[:20000])
+    assert lib.lr_shared_device_error(cache) == 0
+    for x in (k, v, kr):
+        assert not x[:20000].any() and (x[20000] == 55).all()
+
+
 @pytest.mark.parametrize("bits", [0, 8])
 def test_expand_captured_and_replayed_with_other_parts(lib, bits):
     import torch
