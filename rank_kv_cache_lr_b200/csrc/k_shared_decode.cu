@@ -65,13 +65,24 @@ struct DecArgs {
   int* err;
 };
 
+// A sequence's length and a page, read before the grid-dependency wait.  The kernel before (k_shared_qproj,
+// or k_shared_decode for the join) let this one in only after its own wait, so all work before the call,
+// whatever wrote lengths, pages and rows, is complete; only the query latents (the partials) are still on
+// their way.  The reads go to L2, past whatever an SM's L1 may hold from before.
+__device__ __forceinline__ int early_len(const int32_t* row_len, int b, int cap) {
+  return min(max(__ldcg(row_len + b), 0), cap);
+}
+__device__ __forceinline__ int early_page(const RowMap& m, int b, int t) {
+  return min(max(__ldcg(m.table + (long long)b * m.pps + (t >> 7)), 0), m.n_pages - 1);
+}
+
 // The next sequence part of a run: false at its end.  Every role walks its own copy.
 struct Seg {
   int b, t0, nt, len;
 };
 __device__ __forceinline__ bool next_seg(TileRun* run, const DecArgs& p, Seg* s) {
   while (run->left > 0 && run->b < p.B) {
-    const int len = shared_len(p.row_len, run->b, p.cap);
+    const int len = early_len(p.row_len, run->b, p.cap);
     const int nt = (len + kTok - 1) / kTok - run->tile;
     if (nt <= 0) {
       ++run->b;
@@ -250,23 +261,22 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     ptx::prefetch_tmap(&tm_c);
     ptx::prefetch_tmap(&tm_kr);
   }
-  pdl_wait();       // lengths, pages, rows and q~ may come from the work just before
-  // TMEM is taken after this wait, and dependents are let in once it is held: a CTA that held some
-  // while it waited for this grid could keep this grid from the rest
+  // TMEM: a CTA that held some while it waited for a grid could keep that grid from its own.  So a kernel
+  // here lets dependents in once it holds its TMEM, and takes it after its wait; or before, as here, where
+  // the grid to be waited for (k_shared_qproj) is known to hold its own by now.
   if (warp == 1) {
     ptx::tmem_alloc(&aux->tmem_base, 512);
     ptx::tmem_relinquish();
   }
   if (warp == 0) {
     int chunk;
-    const TileRun run = tile_run([&](int b) { return (shared_len(p.row_len, b, p.cap) + kTok - 1) / kTok; }, p.B,
+    const TileRun run = tile_run([&](int b) { return (early_len(p.row_len, b, p.cap) + kTok - 1) / kTok; }, p.B,
                                  p.X, x, &chunk);
     if (lane == 0) aux->run = run;
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  pdl_trigger();
   const uint32_t tmem = aux->tmem_base;
   TileRun run = aux->run;
   Seg sg;
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       while (ok && next_seg(&run, p, &sg)) {
         for (int i = 0; i < sg.nt; ++i) {
           const int tok = (sg.t0 + i) * kTok, half = tok & 64;
-          const long long page = p.map.page(sg.b, tok);
+          const long long page = early_page(p.map, sg.b, tok);
           uint8_t* dst = ring + w.slot * slot_bytes;
           const int row = (int)page * 128 + half;
           uint64_t* const full = aux->full[w.slot];
@@ -306,6 +316,8 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
           if (!ok) break;
           if (i > 0) continue;
           // the query latents, behind the first tile: it has further to come
+          pdl_wait();
+          pdl_trigger();
           if (nseg > 0 && !(ok = wait_b(&aux->q_empty, (nseg - 1) & 1, aux, p.err))) break;
           ptx::mbar_arrive_expect_tx(&aux->q_full, (uint32_t)(nsub * kQSub + NR * 128));
           for (int s = 0; s < nsub; ++s)
@@ -314,6 +326,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
           ++nseg;
         }
       }
+      pdl_wait();          // (a CTA without work too: this grid must not end before the one it waits for)
       // every copy this thread issued has landed before the CTA can exit
       if (nseg > 0) drain_wait(&aux->q_full, (nseg - 1) & 1);
       for (int k = min(gt, p.nslot); k > 0; --k) {
@@ -570,6 +583,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
     const uint32_t wide = code_place(tid, 3);
     const bool odd = (nsub & 1) != 0, swap = (lane & 4) != 0;
     // the next tile to fetch, its page's table entry, and the rows of the sequence in it
+    pdl_wait();                                        // (plain loads, unlike the producer's copies)
     int i = 0, page_n = 0, valid_n = 0;
     bool more = next_seg(&run, p, &sg);
     auto peek = [&]() { page_n = __ldg(p.map.table + (long long)sg.b * p.map.pps + ((sg.t0 + i) * kTok >> 7)); };
@@ -828,20 +842,11 @@ __global__ void __launch_bounds__(kOutThreads)
         ptx::tma_load_2d(w_s + v * p.r * 128 + k * 64 * 128, &tm_w, &aux->w_full, h * p.dv + v * 64, k * 64);
   }
   if (threadIdx.x < 32) aux->count[threadIdx.x] = 0;
-  pdl_wait();
-  if (warp == 1) {            // (after the wait, as in k_shared_decode)
-    ptx::tmem_alloc(&aux->tmem_base, 64);
-    ptx::tmem_relinquish();
-  }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  pdl_trigger();
-  const uint32_t tmem = aux->tmem_base;
+  __syncwarp();
   const int nrow = min(p.RB, p.rows - m0);               // rows m0 .. m0 + nrow - 1
   if (warp == 0) {
     // slots of the rows' sequences, from the same cut into runs as the decode's
-    auto tiles = [&](int b) { return (shared_len(p.row_len, b, p.cap) + kTok - 1) / kTok; };
+    auto tiles = [&](int b) { return (early_len(p.row_len, b, p.cap) + kTok - 1) / kTok; };
     const int chunk = max(1, (tile_total(tiles, p.B) + p.X - 1) / p.X);
     int run = 0;
     const int bk = (m0 + lane) / p.g / p.n_tok;          // the sequence of row m0 + lane
@@ -871,7 +876,16 @@ __global__ void __launch_bounds__(kOutThreads)
       aux->orow[lane] = (long long)(bs / p.n_tok) * p.n_tok * p.Hq + aux->row[lane];
     }
   }
+  pdl_wait();
+  if (warp == 1) {            // (after the wait, see k_shared_decode)
+    ptx::tmem_alloc(&aux->tmem_base, 64);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
   __syncthreads();
+  ptx::tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = aux->tmem_base;
   const size_t srow = (size_t)p.HB * p.NR;               // rows per slot
   for (int k = warp; k < nrow; k += kOutThreads / 32) {  // weights: a warp per row
     const int n = aux->count[k];
