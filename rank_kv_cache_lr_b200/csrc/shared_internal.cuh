@@ -105,9 +105,6 @@ __device__ __forceinline__ void shared_expand(const uint32_t (&in)[N], uint32_t 
 struct TileRun {
   int b, tile, left;   // first sequence, first tile in it, tiles in the run
 };
-__device__ __forceinline__ int shared_len(const int32_t* row_len, int b, int cap) {
-  return min(max(__ldg(row_len + b), 0), cap);
-}
 
 // By one whole warp: the sum of tiles(b) over the sequences.
 template <typename Tiles>

@@ -385,6 +385,35 @@ def test_waits_that_give_up_are_reported_and_the_cache_recovers(lib, r, bits):
     m.check_decode(q, *m.decode(q))
 
 
+@pytest.mark.parametrize("r,bits", [(64, 0), (512, 0), (512, 8)])
+def test_steps_without_a_pause(lib, r, bits):
+    """Appends, lengths and decodes follow one another on a stream with nothing between: each decode
+    reads what the calls before it wrote, as it does when the GPU is waited for after every call."""
+    import torch
+    B, hq, steps = 3, 16, 96
+    got = []
+    for pause in (False, True):
+        m = Layer(lib, [100, 1, 250], hq=hq, hkv=hq, r=r, bits=bits, cap=512)
+        rng = np.random.default_rng(5)
+        c, kr = bf16(rng.standard_normal((steps, B, r)) * 3), bf16(rng.standard_normal((steps, B, 64)))
+        q = bf16(rng.standard_normal((steps, B, 1, hq, 192)))
+        out = torch.zeros((steps, B, 1, hq, 128), dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros((steps, B, 1, hq), dtype=torch.float32, device="cuda")
+        seq, lens = i32(np.arange(B)), i32(m.lens)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            for call in (lambda: lib.lr_shared_append(m.cache, c[i], kr[i], seq, lens), lambda: lens.add_(1),
+                         lambda: lib.lr_shared_decode(m.cache, q[i], lens, out[i], lse[i])):
+                call()
+                if pause:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert lib.lr_shared_device_error(m.cache) == 0
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert got[0][0].abs().sum() > 0
+
+
 def test_decodes_of_two_caches_at_once(lib):
     """Caches own their scratch: decodes of two of them may overlap, on two streams."""
     import torch
