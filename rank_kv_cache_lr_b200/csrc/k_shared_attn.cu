@@ -41,7 +41,7 @@ constexpr int kVBox = kBox / 2;        // 64 rows x 64 columns x 2 B
 // (warp 9) and an idle warp.  Launched at 168 registers, rebalanced so that a softmax thread holds its
 // row of 128 scores (read from TMEM once).
 constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kCtlRegs = 88;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kCtlRegs = 104;
 static_assert(256 * kSoftmaxRegs + 128 * kCtlRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr int kAuxBytes = 1024;
 constexpr float kNoMax = -1e30f;
