@@ -701,6 +701,35 @@ def test_attn_captured_and_replayed_with_other_lengths(lib):
         check_attn(q, k, kr, v, nq, nk, True, 192 ** -0.5, out, lse)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,dn,dr,dv", [(1, 1, 128, 64, 128), (2, 2, 64, 32, 64), (3, 1, 64, 64, 128), (5, 5, 128, 32, 64)])
+@pytest.mark.parametrize("nq,nk", [([1], [4097]), ([50], [5000]), ([257], [2050]), ([300, 40], [3000, 129]),
+                                   ([130, 1], [1, 4000]), ([5, 0, 200], [0, 900, 3500]), ([400], [1100])])
+def test_attn_of_few_queries_over_many_keys(lib, nq, nk, causal, hq, hkv, dn, dr, dv):
+    """Few CTAs' worth of queries: the keys are split over a cluster, parts may be empty or see nothing."""
+    cache, q, k, kr, v, cu = attn_case(lib, nq, nk, hq=hq, hkv=hkv, dn=dn, dr=dr, dv=dv, seed=3)
+    check_attn(q, k, kr, v, nq, nk, causal, (dn + dr) ** -0.5, *run_attn(lib, cache, q, k, kr, v, cu, causal))
+
+
+@pytest.mark.parametrize("amp", [0.0, 30.0])
+def test_attn_split_with_equal_and_sharp_weights(lib, amp):
+    nq, nk = [70], [4500]
+    cache, q, k, kr, v, cu = attn_case(lib, nq, nk, amp=amp)
+    check_attn(q, k, kr, v, nq, nk, True, 192 ** -0.5, *run_attn(lib, cache, q, k, kr, v, cu, True))
+
+
+def test_attn_split_waits_that_give_up_are_reported(lib):
+    import torch
+    nq, nk = [300], [9000]
+    cache, q, k, kr, v, cu = attn_case(lib, nq, nk)
+    out = torch.zeros((q.shape[0], 4, 128), dtype=torch.bfloat16, device="cuda")
+    lib.lr_shared_set_wait_limit(cache, 4)
+    lib.lr_shared_attn(cache, q, k, kr, v, cu[0], cu[1], out)
+    assert lib.lr_shared_device_error(cache) == lib.LR_ERR_TIMEOUT
+    lib.lr_shared_set_wait_limit(cache, 0)
+    check_attn(q, k, kr, v, nq, nk, True, 192 ** -0.5, *run_attn(lib, cache, q, k, kr, v, cu, True))
+
+
 def test_attn_waits_that_give_up_are_reported(lib):
     nq, nk = [300, 40], [700, 129]
     cache, q, k, kr, v, cu = attn_case(lib, nq, nk)
