@@ -718,6 +718,29 @@ def test_attn_split_with_equal_and_sharp_weights(lib, amp):
     check_attn(q, k, kr, v, nq, nk, True, 192 ** -0.5, *run_attn(lib, cache, q, k, kr, v, cu, True))
 
 
+def test_attn_split_captured_and_replayed_with_other_lengths(lib):
+    import torch
+    nq, nk = [40, 20], [3000, 2000]
+    cache, q, k, kr, v, cu = attn_case(lib, nq, nk)
+    out = torch.zeros((q.shape[0], 4, 128), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((q.shape[0], 4), dtype=torch.float32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lib.lr_shared_attn(cache, q, k, kr, v, cu[0], cu[1], out, lse)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.lr_shared_attn(cache, q, k, kr, v, cu[0], cu[1], out, lse)
+    for nq, nk in (([40, 20], [3000, 2000]), ([1, 59], [5000, 0]), ([0, 60], [4, 4996]), ([30, 2], [129, 1])):
+        cu[0].copy_(i32(np.concatenate([[0], np.cumsum(nq)])))
+        cu[1].copy_(i32(np.concatenate([[0], np.cumsum(nk)])))
+        out.fill_(33.0), lse.fill_(33.0)
+        g.replay()
+        kk, rr, vv = (x[:sum(nk)] for x in (k, kr, v))
+        check_attn(q, kk, rr, vv, nq, nk, True, 192 ** -0.5, out, lse)
+
+
 def test_attn_split_waits_that_give_up_are_reported(lib):
     import torch
     nq, nk = [300], [9000]
