@@ -129,9 +129,12 @@ __device__ __forceinline__ uint32_t code_place(int tid, int sh) {
 
 // Barriers (arrival count; who arrives -> who waits); phase k is waited with parity k & 1.  NG =
 // NR / 16 groups of four softmax warps.
-//   full[s][h]      1 + tx   producer's boxes -> GEMM1 issuer; half h of the ranks, the rotary box with
-//                            the second (8 bits: 16 expansion warps, + 1 + tx with the rotary box)
-//   empty[s][h]     1        GEMM2's commit on half h -> producer, expansion warps
+//   full[s][h]      1 + tx   producer's boxes -> GEMM1 issuer; half h of the ranks (half_of_block), the
+//                            rotary box with the second (8 bits: 16 expansion warps, after their blocks
+//                            0 and 1 and after 2 and 3, + 1 + tx with the rotary box; at two blocks in all
+//                            the second one is there early, with full[s][0])
+//   empty[s][h]     1        GEMM2's commit on half h -> producer, expansion warps (each for the half of
+//                            the block it writes)
 //   q_full/q_empty  1 + tx / 2   per sequence of the run
 //   s_full[2]       2        GEMM1's commits (one a half) -> softmax warps
 //   s_empty[2]      4 NG     softmax warps (scores read) -> GEMM1 issuer
@@ -204,6 +207,13 @@ constexpr int dec_threads() {
   return 128 + NR * 8 + (kQuant ? 512 : 0);
 }
 __host__ __device__ constexpr int dec_slot(int r) { return (r / 64 + 1) * kSub; }   // a tile, its rotary box last
+// A tile's ranks in two halves that are filled and given back apart: the first (nch + 1) / 2 of its nch
+// blocks of 128 ranks, and the others (at 64 and 128 ranks there are none).  In 64-rank boxes:
+__host__ __device__ constexpr int first_boxes(int r) {
+  const int all = r / 64, half = ((r + 127) / 128 + 1) / 2 * 2;
+  return half < all ? half : all;
+}
+__host__ __device__ constexpr int half_of_block(int c, int r) { return 2 * c >= first_boxes(r); }
 
 // Shared memory: [aux][q~: r/64 blocks of (2 NR rows hi | lo) x 128 B][q_rope: NR rows x 128 B]
 // [P: 2 x 64 tokens x NR][slots].
@@ -219,7 +229,7 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
   }
   constexpr int NG = NR / 16, kQSub = 2 * NR * 128, kPBuf = kTok * NR * 2;
   const int nsub = p.r >> 6, nch = (p.r + 127) >> 7;
-  const int slot_bytes = dec_slot(p.r), nsub0 = min(nsub, (nch + 1) / 2 * 2);   // boxes of a tile's first half
+  const int slot_bytes = dec_slot(p.r), nsub0 = first_boxes(p.r);
   Aux* aux = reinterpret_cast<Aux*>(smem_raw);
   uint8_t* q_s = smem_raw + kAuxBytes;
   uint8_t* qr_s = q_s + nsub * kQSub;
@@ -631,8 +641,8 @@ __global__ void __launch_bounds__(dec_threads<NR, kQuant>(), 1)
       bool ok = true;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        if (gt >= p.nslot && !(ok = wait_w(&aux->empty[w.slot][k], w.ph ^ 1, aux, p.err))) break;
-        const int c = g + 2 * k;
+        const int c = g + 2 * k, h = c < nch ? half_of_block(c, p.r) : k;
+        if (gt >= p.nslot && !(ok = wait_w(&aux->empty[w.slot][h], w.ph ^ 1, aux, p.err))) break;
         if (c < nch) {
           const bool l = odd && c == nch - 1;
           const uint32_t box = dst + 2 * c * kSub + (l ? code_place(tid, 2) : wide);

@@ -257,6 +257,27 @@ def test_decode_long_context_over_many_splits(lib, r, bits):
     m.check_decode(q, *m.decode(q))
 
 
+@pytest.mark.parametrize("r,bits", [(r, 8) for r in range(64, 513, 64)] + [(192, 0), (512, 0)])
+def test_decode_runs_that_use_every_slot_again(lib, r, bits):
+    """Runs of 9 tiles over several sequences (1024 query rows leave 4 CTA columns), more than there are
+    slots at any rank, and tiles that differ in sign and size: latents of one tile under the weights of
+    another would show.  Twice the same."""
+    import torch
+    m = Layer(lib, [1500, 300, 129, 1, 100], hq=128, hkv=2, r=r, bits=bits, new=8, dn=64, dv=64)
+    pos = np.concatenate([np.arange(n) for n in m.lens])
+    tile = pos // 64
+    f = np.where(tile % 2, -1.0, 1.0) * 2.0 ** (tile % 3)      # exact in bf16, and in the codes' scales
+    m.c = m.c * bf16(f)[:, None]
+    m.c64 *= f[:, None]
+    lib.lr_shared_append(m.cache, m.c, m.kr, i32(np.repeat(np.arange(5), m.lens)), i32(pos))
+    q = m.query(8, 0.5)
+    a = m.decode(q)
+    m.check_decode(q, *a)
+    for _ in range(4):
+        b = m.decode(q)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_decode_of_rotated_keys_and_own_scale(lib):
     m = Layer(lib, [200, 129], r=128, theta=1e4, scale=0.21)
     m.rope_stored = True
