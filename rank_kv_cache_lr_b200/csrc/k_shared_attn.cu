@@ -194,8 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < nqb; ++c)
             ptx::tma_load_3d(q_s + (t * nqb + c) * kBox, &tm_q, &aux->q_full[t], c * 64, head, rq.first + q0 + t * 128);
         };
-        queries(0);                        // (the second tile's come behind the first keys)
-        const bool two = rq.n - q0 > 128;
+        // (a tile that sees no key here has no reader, and a part's sums take its place; the second tile's
+        // come behind the first keys)
+        if (nt[0] > 0) queries(0);
         // Slots are taken and given back in one order, K0 V0 K1 V1 ..., so V_j goes where K_{j-1} was (free
         // early: its scores are done) and K_{j+1} partly where V_{j-1} was, half by half.
         bool ok = true;
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c < nkb - 1) ptx::tma_load_2d(dst, &tm_k, &aux->k_full[s], kvh * p.dn + c * 64, row);
             else ptx::tma_load_2d(dst, &tm_kr, &aux->k_full[s], 0, row);
           }
-          if (j == 0 && two) queries(1);
+          if (j == 0 && nt[1] > 0) queries(1);
           for (int c = 0; c < nvb && ok; ++c) {
             uint8_t* dst = slot();
             if (!ok) break;
@@ -246,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // every copy this thread issued has landed before the CTA can exit
-        drain_wait(&aux->q_full[0], 0);
-        if (two) drain_wait(&aux->q_full[1], 0);
+        if (nt[0] > 0) drain_wait(&aux->q_full[0], 0);
+        if (nt[1] > 0) drain_wait(&aux->q_full[1], 0);
         for (int j = max(0, nk - 2); j < nk; ++j) drain_wait(&aux->k_full[j & 1], (j >> 1) & 1);
         for (int j = max(0, nv - 2); j < nv; ++j) drain_wait(&aux->v_full[j & 1], (j >> 1) & 1);
       }

@@ -739,6 +739,20 @@ def test_attn_split_with_equal_and_sharp_weights(lib, amp):
     check_attn(q, k, kr, v, nq, nk, True, 192 ** -0.5, *run_attn(lib, cache, q, k, kr, v, cu, True))
 
 
+@pytest.mark.parametrize("hq,dn,dr,dv", [(1, 128, 64, 128), (4, 64, 32, 64)])
+@pytest.mark.parametrize("nq,nk", [([256], [4608]), ([130], [2306]), ([130, 256], [1, 4608])])
+def test_attn_split_whose_last_part_is_the_second_query_tiles_alone(lib, nq, nk, hq, dn, dr, dv):
+    """36 (19) key tiles in 8 parts of 5 (3), causal: the last part holds a key tile that the first 128
+    queries do not see, so their tile is neither loaded nor read there."""
+    import torch
+    cache, q, k, kr, v, cu = attn_case(lib, nq, nk, hq=hq, hkv=hq, dn=dn, dr=dr, dv=dv, seed=4)
+    want = run_attn(lib, cache, q, k, kr, v, cu, True)
+    check_attn(q, k, kr, v, nq, nk, True, (dn + dr) ** -0.5, *want)
+    for _ in range(20):
+        got = run_attn(lib, cache, q, k, kr, v, cu, True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_attn_split_captured_and_replayed_with_other_lengths(lib):
     import torch
     nq, nk = [40, 20], [3000, 2000]
