@@ -47,7 +47,7 @@ constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kCtlRegs = 104;
 static_assert(256 * kSoftmaxRegs + 128 * kCtlRegs <= kThreads * kLaunchRegs, "register split exceeds the launch");
 constexpr int kAuxBytes = 1024;
-constexpr float kNoMax = -1e30f;
+constexpr float kNoMax = -3.402823466e38f;   // running max before any visible key: finite, and below every score
 constexpr int kMaxSplit = 8;
 constexpr int kPartMl = 256 * 8;       // (m, l) of a part's rows, then their sums (rows padded by 16 bytes)
 

@@ -48,7 +48,7 @@ constexpr int kSub = kTok * 128;       // 64 tokens x 64 ranks x 2 B (one TMA bo
 constexpr int kWSub = 128 * 128;       // 128 rows x 64 columns x 2 B (the projections' operands)
 constexpr int kAuxBytes = 2048;
 constexpr int kMaxSlots = 4;
-constexpr float kNoMax = -1e30f;       // running max before any visible token (finite: no inf - inf)
+constexpr float kNoMax = -3.402823466e38f;   // running max before any visible token: finite (no inf - inf), and below every score
 constexpr int kSCol = 0;               // TMEM: S of tile t and rank half h in columns [128 (t % 2) + 64 h, + 2 NR)
 constexpr int kOCol = 256;             // TMEM: O~ of 128-rank block k in columns [256 + k NR, + NR)
 

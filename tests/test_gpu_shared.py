@@ -454,6 +454,42 @@ def test_decodes_of_two_caches_at_once(lib):
         assert all(torch.equal(o, w[0]) and torch.equal(e, w[1]) for o, e in g)
 
 
+# Scores from the rotary part alone, 8 bits times a power of two and so exact in fp32: far from zero on
+# either side.  (sign, power): sign 2^power or, where its product with log2(e) rounds, 165/128 of it.
+FAR = [(s * f, p) for f in (1.0, 165 / 128) for s, p in ((-1, 110), (-1, 60), (-1, 35), (1, 35), (1, 110))]
+
+
+def far_scores(n, sign, power):
+    """Scores of n keys and which of them carry all the weight: half of the keys, in no order, stand at
+    sign 2^power; the others at twice (half) that where that is less."""
+    pick = np.random.default_rng(n).random(n) < 0.5
+    pick[0] = True
+    low = sign * 2.0 ** (power + (1 if sign < 0 else -1))
+    return np.where(pick, sign * 2.0 ** power, low), pick
+
+
+@pytest.mark.parametrize("sign,power", FAR)
+@pytest.mark.parametrize("hq,r,bits,n", [(4, 128, 0, 700), (28, 512, 0, 129), (28, 512, 8, 129), (6, 256, 8, 3000)])
+def test_decode_of_scores_far_from_zero(lib, hq, r, bits, n, sign, power):
+    """A maximum of -2^110 is a maximum as any other: equal scores weigh the same, lower ones nothing."""
+    m = Layer(lib, [n], hq=hq, hkv=hq, r=r, bits=bits, dn=64, dv=64, scale=1.0)
+    s, pick = far_scores(n, sign, power)
+    m.kr.zero_()
+    m.kr[:, 3] = bf16(s / 2.0 ** 60)
+    lib.lr_shared_append(m.cache, m.c, m.kr, i32(np.zeros(n)), i32(np.arange(n)))
+    q = m.query(1, 0.0)
+    q[..., 64 + 3] = 2.0 ** 60
+    out, lse = map(f64, m.decode(q))
+    # the lse: scale log2(e) and its product each round once, as do log2(e) itself and the factor back
+    want = sign * 2.0 ** power + np.log(pick.sum())
+    assert np.all(np.abs(lse - want) <= 8 * F * abs(want) + 2.0 ** -20)
+    # equal weights 2^x of one rounding (u), in the numerator; sums of n + r fp32 steps, two halves; the output
+    rows = S.expand(m.c64[pick], m.Bv64, hq)
+    A = (np.abs(m.c64[pick]).mean(axis=0) @ np.abs(m.Bv64)).reshape(hq, 64)
+    tol = U * np.abs(rows.mean(axis=0)) + U * np.abs(rows).mean(axis=0) + (U * U + (n + r + 64) * F) * A
+    assert np.all(np.abs(out[0, 0] - rows.mean(axis=0)) <= tol)
+
+
 # ---------------------------------------------------------------------------
 # expansion
 # ---------------------------------------------------------------------------
@@ -674,6 +710,24 @@ def test_attn_rising_scores_raise_the_maximum_often(lib):
     q[:, :, 0], k[:, :, 0] = 1.0, ramp[:, None].to(torch.bfloat16)
     out, lse = run_attn(lib, cache, q, k, kr, v, cu, True)
     check_attn(q, k, kr, v, nq, nk, True, 1.0, out, lse)
+
+
+@pytest.mark.parametrize("sign,power", FAR[:5])
+@pytest.mark.parametrize("hq,hkv,nq,nk", [(4, 4, 300, 700), (28, 28, 260, 260), (2, 1, 5, 5000)])
+def test_attn_of_scores_far_from_zero(lib, hq, hkv, nq, nk, sign, power):
+    """As for the decode: plain, causal and split over a cluster."""
+    cache, q, k, kr, v, cu = attn_case(lib, [nq], [nk], hq, hkv, 64, 64, 64, behind=0, scale=1.0)
+    s, pick = far_scores(nk, sign, power)
+    q.zero_(), kr.zero_()
+    q[:, :, 64 + 3], kr[:, 3] = 2.0 ** 60, bf16(s / 2.0 ** 60)
+    out, lse = map(f64, run_attn(lib, cache, q, k, kr, v, cu, True))
+    seen = pick & (np.arange(nk) <= np.arange(nq)[:, None] + nk - nq)
+    n = seen.sum(axis=1, keepdims=True)
+    want = sign * 2.0 ** power + np.log(n)
+    assert np.all(np.abs(lse[:nq] - want) <= 8 * F * np.abs(want) + 2.0 ** -20)
+    v64 = np.repeat(f64(v), hq // hkv, axis=1)
+    ro, mix = (np.einsum("ij,jhd->ihd", seen / n, x) for x in (v64, np.abs(v64)))
+    assert np.all(np.abs(out[:nq] - ro) <= U * np.abs(ro) + (U + (nk + 64) * F) * mix)
 
 
 def test_attn_without_keys_or_queries(lib):
