@@ -322,6 +322,11 @@ lr_status lr_attn_decode_noalloc(const lr_cache_desc* desc, int32_t len, const v
  * included, must not run at the same time.  Calls run on the device the cache was created on,
  * whichever is current.
  *
+ * Both attentions hold scores in fp32, times scale and log2(e): a finite one counts however far from
+ * zero it is, one beyond fp32's range is infinite.  Scores that are +infinity or NaN make NaN of their
+ * query's out and lse; scores of -infinity weigh nothing, and a query that has no others is one that
+ * sees no token.
+ *
  * 8 bits (quant_bits = 8): per group of 32 ranks the smallest power of two 2^e, e >= -100, with
  * max|c| <= 448 * 2^e, and per element the nearest e4m3 value (ties to even) of c / 2^e.  What
  * a code stands for is a bf16 value.  A group that holds a NaN or an infinity reads back as

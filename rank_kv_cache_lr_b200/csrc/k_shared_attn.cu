@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int last = p.causal ? min(rk.n - 1, i + shift) : rk.n - 1;   // last key this query sees
     const int wlast = __shfl_sync(0xffffffffu, last, 0);                     // the warp's smallest
     float m = kNoMax, l = 0.f;
-    bool ok = true;
+    bool ok = true, far = false;                   // far: some row of the warp has |m| > 2^24
     for (int j = 0; j < nt[t]; ++j) {
       if (!(ok = wait_w(&aux->s_full[t][j & 1], (j >> 1) & 1, aux, p.err))) break;
       ptx::tc_fence_after();
@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mn = fmaxf(m, top), a = ptx::ex2_approx(m - mn);
         m = mn;
         l *= a;
+        far = __any_sync(0xffffffffu, fabsf(m) > 16777216.f && m > kNoMax);
         if (j > 0) {                               // (PV(j - 1) came before S(j), which is complete)
           for (int c = 0; c < p.dv; c += 16) {
             uint32_t o[16];
@@ -394,17 +395,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const float2 sc = make_float2(p.scale_log2, p.scale_log2), nm = make_float2(-m, -m);
-      float2 sum[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      // Weights 2^(v c - m), by one fma a score.  m is a rounded product, so beyond 2^24 the exact v c of an
+      // fma is off from it by whole units, alike for a row's scores (at 2^35 by up to 2^11: every weight 0 or
+      // infinite).  There the products round first, as m did (from TMEM again and in a loop of its own: as a
+      // choice within the usual one it cost 2% of long prompts).
+      auto weights = [&](int c, const uint32_t (&x)[32], float2 sc) {
+        const float2 nm = make_float2(-m, -m);
         uint32_t w[16];
-        sum[c] = make_float2(0.f, 0.f);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float2 x = ptx::fma2(make_float2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), sc, nm);
-          const float2 y = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
-          sum[c] = ptx::add2(sum[c], y);
+          const float2 z = ptx::fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc, nm);
+          const float2 y = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
+          sum = ptx::add2(sum, y);
           const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
           w[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
@@ -415,6 +418,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&aux->p_full[t][c >> 1][j & 1]);
         }
+        return sum;
+      };
+      float2 sum[4];
+      if (far) {
+        sum[1] = sum[2] = sum[3] = make_float2(0.f, 0.f);
+        sum[0] = sum[1];
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[32];
+          ptx::tmem_ld32(s_col + 32 * c, x);       // (the weights so far lie below these columns)
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            x[e] = 32 * c + e <= lim ? __float_as_uint(__uint_as_float(x[e]) * p.scale_log2) : 0xFF800000u;
+          sum[0] = ptx::add2(sum[0], weights(c, x, make_float2(1.f, 1.f)));
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum[c] = weights(c, v[c], make_float2(p.scale_log2, p.scale_log2));
       }
       const float2 l2 = ptx::add2(ptx::add2(sum[0], sum[1]), ptx::add2(sum[2], sum[3]));
       l += l2.x + l2.y;
