@@ -325,7 +325,8 @@ lr_status lr_attn_decode_noalloc(const lr_cache_desc* desc, int32_t len, const v
  * Both attentions hold scores in fp32, times scale and log2(e): a finite one counts however far from
  * zero it is, one beyond fp32's range is infinite.  Scores that are +infinity or NaN make NaN of their
  * query's out and lse; scores of -infinity weigh nothing, and a query that has no others is one that
- * sees no token.
+ * sees no token.  Weights are rounded to bf16 for the value mix, their sum is taken before: that
+ * moves an output by at most 2^-8 of the weighted mean of |v|, and equal weights all alike.
  *
  * 8 bits (quant_bits = 8): per group of 32 ranks the smallest power of two 2^e, e >= -100, with
  * max|c| <= 448 * 2^e, and per element the nearest e4m3 value (ties to even) of c / 2^e.  What

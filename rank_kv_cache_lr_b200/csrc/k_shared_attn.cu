@@ -25,8 +25,10 @@
 // keys and one for values 1.22 ms; with a barrier per 64-column box of keys 1.24 ms (a test between
 // MMAs costs more than the earlier start gains).
 //
-// Roundings: P to bf16 (half a step, 2^-8 relative, at random over the keys, below the output's
-// own); sums of the unrounded weights in fp32; the output once.  A running max may be stale by
+// Roundings: P to bf16 (half a step, 2^-8 relative at most: at random over the keys, but alike for equal
+// weights that are no powers of two, and then 2^-8 of the output before its own rounding); sums of the
+// unrounded weights in fp32 (a second sum, of the rounded ones, would take three more instructions
+// for every two weights); the output once.  A running max may be stale by
 // 2^8 before it is raised (fp32 sums hold that easily), which saves most rescales of O.
 #include "shared_internal.cuh"
 #include "tc_common.cuh"

@@ -293,6 +293,33 @@ def test_decode_equal_and_sharp_weights(lib, amp, r):
     m.check_decode(q, *m.decode(q))
 
 
+@pytest.mark.parametrize("hq,r,bits,new", [(4, 128, 0, 1), (28, 512, 0, 1), (28, 512, 8, 1), (128, 256, 8, 2)])
+def test_decode_of_equal_weights_other_than_one(lib, hq, r, bits, new):
+    """Every 64th token has weight 1, the others all the same weight, which bf16 rounds by nearly half a
+    step.  One latent throughout: the common rounding of the weights (u at most, their sum is of the
+    unrounded ones), then that of the output, u of a value itself up to u larger; sums, the halves."""
+    w = 0.5 * (1 + 2.0 ** -8 - 2.0 ** -13)
+    m = Layer(lib, [640, 64, 1], hq=hq, hkv=hq, r=r, bits=bits, new=new, dn=64, dv=64, scale=-float(np.log(w)))
+    pos = np.concatenate([np.arange(n) for n in m.lens])
+    m.c[:] = m.c[:1].clone()
+    m.kr.zero_()
+    m.kr[:, 3] = bf16(np.where(pos % 64 == 0, 0.0, -1.0))
+    lib.lr_shared_append(m.cache, m.c, m.kr, i32(np.repeat([0, 1, 2], m.lens)), i32(pos))
+    q = m.query(new, 0.0)
+    q[..., 64 + 3] = 1.0
+    out, lse = map(f64, m.decode(q))
+    want = (m.c64[0] @ m.Bv64).reshape(hq, 64)
+    A = (np.abs(m.c64[0]) @ np.abs(m.Bv64)).reshape(hq, 64)
+    for b, n in enumerate(m.lens):
+        for s in range(new):
+            seen = n - (new - 1 - s)
+            if seen <= 0:
+                continue
+            high = (seen + 63) // 64
+            assert np.all(np.abs(lse[b, s] - np.log(high + (seen - high) * w)) <= 2.0 ** -18)
+            assert np.all(np.abs(out[b, s] - want) <= U * (2 + U) * np.abs(want) + (U * U + (n + r + 64) * F) * A)
+
+
 def test_decode_shorter_lengths_and_clamping(lib):
     """row_len picks a prefix; values outside 0..capacity are clamped."""
     import torch
@@ -698,6 +725,22 @@ def test_attn_equal_and_sharp_weights(lib, amp):
     case = attn_case(lib, nq, nk, amp=amp)
     out, lse = run_attn(lib, *case, True)
     check_attn(*case[1:5], nq, nk, True, 192 ** -0.5, out, lse)
+
+
+@pytest.mark.parametrize("hq,nq,nk", [(4, 300, 700), (2, 5, 5000)])
+def test_attn_of_equal_weights_other_than_one(lib, hq, nq, nk):
+    """As for the decode: every 64th key has weight 1, the others one that rounds by nearly half a step."""
+    w = 0.5 * (1 + 2.0 ** -8 - 2.0 ** -13)
+    cache, q, k, kr, v, cu = attn_case(lib, [nq], [nk], hq, hq, 64, 64, 64, behind=0, scale=-float(np.log(w)))
+    q.zero_(), kr.zero_()
+    q[:, :, 64 + 3], kr[:, 3] = 1.0, bf16(np.where(np.arange(nk) % 64 == 0, 0.0, -1.0))
+    v[:] = v[:1].clone()
+    out, lse = map(f64, run_attn(lib, cache, q, k, kr, v, cu, True))
+    seen = np.arange(nq) + nk - nq + 1
+    high = (seen + 63) // 64
+    assert np.all(np.abs(lse[:nq] - np.log(high + (seen - high) * w)[:, None]) <= 2.0 ** -18)
+    want = f64(v)[0]
+    assert np.all(np.abs(out[:nq] - want) <= (U * (2 + U) + (nk + 64) * F) * np.abs(want))
 
 
 def test_attn_rising_scores_raise_the_maximum_often(lib):
