@@ -412,8 +412,9 @@ __global__ void __launch_bounds__(exp_threads<kQuant>(), 1)
   ptx::tc_fence_before();
   __syncthreads();
   // neither CTA leaves while the other's MMAs, copies or arrivals may still reach it (after an abort,
-  // those that nobody waited for have time to land)
-  if (aux->abort_flag) __nanosleep(1000000);
+  // those that nobody waited for have a millisecond to land, by the clock: a sleep may end at once)
+  if (aux->abort_flag)
+    for (const uint64_t t0 = ptx::globaltimer(); ptx::globaltimer() - t0 < 1000000;) __nanosleep(10000);
   ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
