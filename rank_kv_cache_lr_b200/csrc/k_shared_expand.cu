@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(exp_threads<kQuant>(), 1)
   // those that nobody waited for have a millisecond to land, by the clock: a sleep may end at once)
   if (aux->abort_flag)
     for (const uint64_t t0 = ptx::globaltimer(); ptx::globaltimer() - t0 < 1000000;) __nanosleep(10000);
+  __syncwarp();
   ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
