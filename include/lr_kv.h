@@ -400,7 +400,9 @@ lr_status lr_shared_decode(lr_shared* cache, const void* q, int32_t n_tokens, co
 /* lr_shared_expand — stored tokens as per-head keys and values, for prompts (many queries):
  *   row cu[b] + i of k [total][Hkv][dn], v [total][Hkv][dv] (32-byte) and kr [total][dr] (bf16, 16-byte
  *   aligned) is token start[b] + i of sequence b: k_h = c B_k,h, v_h = c B_v,h in fp32,
- *   rounded once.  cu, start, total as for lr_shared_read.
+ *   rounded once.  cu, start, total as for lr_shared_read.  With a cu that does not ascend, parts
+ *   may be left out; where it asks for so many that a block cannot hold its list of them,
+ *   lr_shared_device_error reports LR_ERR_INVALID_ARG.
  * lr_shared_attn — attention of ragged queries over expanded keys and values: sequence b's
  *   queries are rows cu_q[b]..cu_q[b+1]-1 of q [total_q][Hq][dn + dr], its keys and values rows
  *   cu_k[b]..cu_k[b+1]-1 of k, v, kr (as lr_shared_expand writes them; n_seq sequences, 0..1024,

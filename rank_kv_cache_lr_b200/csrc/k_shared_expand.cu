@@ -94,8 +94,9 @@ __device__ __forceinline__ bool wait_x(uint64_t* bar, uint32_t parity, Aux* aux,
   return __all_sync(0xffffffffu, ok);
 }
 
-// Positions [lo, hi) of sequence b to expand, inside the cache and the results (so that there are no
-// more tiles than the host reckoned with, whatever cu holds); position t goes to row t + off.
+// Positions [lo, hi) of sequence b to expand, inside the cache and the results; position t goes to row
+// t + off.  With an ascending cu there are then no more tiles than the host reckoned with, however many
+// rows it speaks of; with another one there may be, and runs that do not fit are cut and reported.
 struct Span {
   int lo, hi;
   long long off;
@@ -188,7 +189,10 @@ __global__ void __launch_bounds__(exp_threads<kQuant>(), 1)
     int n = 0, blk0 = 0;
     if (first < units) {
       n = (int)min(chunk, units - first);
-      n = min(n, (kMaxTiles - 1) * p.NB);      // (the host's grid never reaches this)
+      if (n > (kMaxTiles - 1) * p.NB) {        // more than the tile table holds: cu does not ascend
+        n = (kMaxTiles - 1) * p.NB;
+        if (lane == 0) atomicExch(p.err, (int)LR_ERR_INVALID_ARG);
+      }
       blk0 = (int)(first % (unsigned)p.NB);
       const int t0 = (int)(first / (unsigned)p.NB), nt = (blk0 + n + p.NB - 1) / p.NB;
       for (int k = 0; k < nt; ++k) {

@@ -595,6 +595,21 @@ def test_expand_of_fewer_rows_than_the_parts_hold(lib):
 
 
 @pytest.mark.parametrize("bits", [0, 8])
+def test_expand_of_parts_that_do_not_ascend_is_bounded_and_reported(lib, bits):
+    """64 parts that all claim the same 20000 rows: far more tiles than those rows can have."""
+    import torch
+    d = lib.make_shared_desc(128, 1, 1, 64, 32, 64, 64, 1 << 15, n_pages=4, quant_bits=bits)
+    cache = lib.lr_shared_create(d, bf16(np.ones((64, 64))), bf16(np.ones((64, 64))))
+    k, v, kr = (torch.full((20001, *x), 55.0, dtype=torch.bfloat16, device="cuda") for x in ((1, 64), (1, 64), (32,)))
+    lib.lr_shared_expand(cache, i32([0, 20000] * 64 + [0]), k[:20000], v[:20000], kr[:20000])
+    assert lib.lr_shared_device_error(cache) == lib.LR_ERR_INVALID_ARG
+    assert all((x[20000] == 55).all() for x in (k, v, kr))
+    lib.lr_shared_expand(cache, i32([0] + [20000] * 128), k[:20000], v[:20000], kr[:20000])
+    assert lib.lr_shared_device_error(cache) == 0
+    assert not any(x[:20000].any() for x in (k, v, kr)) and all((x[20000] == 55).all() for x in (k, v, kr))
+
+
+@pytest.mark.parametrize("bits", [0, 8])
 def test_expand_captured_and_replayed_with_other_parts(lib, bits):
     import torch
     m = Layer(lib, [300, 513, 40], hq=3, hkv=3, r=192, bits=bits)
