@@ -320,6 +320,50 @@ def test_decode_of_equal_weights_other_than_one(lib, hq, r, bits, new):
             assert np.all(np.abs(out[b, s] - want) <= U * (2 + U) * np.abs(want) + (U * U + (n + r + 64) * F) * A)
 
 
+@pytest.mark.parametrize("hq,r,bits,new", [(4, 128, 0, 1), (28, 512, 8, 2), (6, 192, 8, 1), (28, 512, 0, 2)])
+def test_decode_over_visible_infinities_and_nans(lib, hq, r, bits, new):
+    """A score of -infinity weighs nothing; one of +infinity, and a NaN, make NaN of the queries that see
+    them; other sequences, before and behind in the same run or not, are as without."""
+    import torch
+    m = Layer(lib, [200, 700, 130, 64], hq=hq, hkv=hq, r=r, bits=bits, new=new, dn=64, dv=64)
+    q = m.query(new)
+    q[..., 64:] = 0.0
+    q[..., 64 + 5] = 1.0
+    want, wl = m.decode(q)
+
+    def put(b, t, c=None, kr=None):
+        """Token t of sequence b once more, some of its elements replaced."""
+        i = int(m.cu[b]) + t
+        x, y = m.c[i:i + 1].clone(), m.kr[i:i + 1].clone()
+        if c is not None:
+            x[0, r - 3] = c
+        if kr is not None:
+            y[0, 5] = kr
+        lib.lr_shared_append(m.cache, x, y, i32([b]), i32([t]))
+
+    # tokens of a very low score, then of none at all
+    for t in (0, 63, 64, 699 - new):
+        put(1, t, kr=-3e38)
+    low, ll = m.decode(q)
+    assert torch.isfinite(low.float()).all() and torch.isfinite(ll).all() and not torch.equal(low[1], want[1])
+    for t in (0, 63, 64, 699 - new):
+        put(1, t, kr=-np.inf)
+    out, lse = m.decode(q)
+    assert torch.equal(out, low) and torch.equal(lse, ll)
+    for kw in (dict(kr=np.inf), dict(kr=np.nan), dict(c=np.nan), dict(c=np.inf), dict(c=-np.inf)):
+        put(1, 300, **kw)
+        out, lse = m.decode(q)
+        assert torch.isnan(out[1].float()).all(), kw
+        # (an infinite latent's score may be -infinity: no weight, but 0 times its value is NaN still)
+        assert torch.isnan(lse[1]).all() or kw.get("c") in (np.inf, -np.inf), kw
+        for b in (0, 2, 3):
+            assert torch.equal(out[b], want[b]) and torch.equal(lse[b], wl[b]), kw
+    for t in (0, 63, 64, 300, 699 - new):
+        put(1, t)
+    out, lse = m.decode(q)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
 def test_decode_shorter_lengths_and_clamping(lib):
     """row_len picks a prefix; values outside 0..capacity are clamped."""
     import torch
@@ -786,6 +830,50 @@ def test_attn_of_scores_far_from_zero(lib, hq, hkv, nq, nk, sign, power):
     v64 = np.repeat(f64(v), hq // hkv, axis=1)
     ro, mix = (np.einsum("ij,jhd->ihd", seen / n, x) for x in (v64, np.abs(v64)))
     assert np.all(np.abs(out[:nq] - ro) <= U * np.abs(ro) + (U + (nk + 64) * F) * mix)
+
+
+@pytest.mark.parametrize("hq,hkv,nq,nk", [(4, 4, [100, 300, 40], [100, 600, 40]), (28, 7, [5, 260, 3], [70, 260, 3]),
+                                          (2, 1, [3, 9, 7], [130, 5000, 900])])
+def test_attn_over_visible_infinities_and_nans(lib, hq, hkv, nq, nk):
+    """A score of -infinity weighs nothing; one of +infinity, or NaN, makes NaN of the queries that see it and
+    of no other (those of its sequence may be rescaled along with them: both results are within u |out| + u of
+    the mean of |v|, and a little, of the truth); an infinite value is infinite in its column for the queries that see it; other sequences
+    are as without."""
+    import torch
+    cache, q, k, kr, v, cu = attn_case(lib, nq, nk, hq, hkv, 64, 32, 64)
+    q[..., 64:] = 0.0
+    q[..., 64 + 5] = 1.0
+    want, wl = run_attn(lib, cache, q, k, kr, v, cu, True)
+    a, b = nq[0], nk[0]
+    t = nk[1] - nq[1] // 2                                     # a key of the second sequence
+    mine = np.arange(a, a + nq[1])
+    sees = torch.tensor(mine[np.arange(nq[1]) + nk[1] - nq[1] >= t]).cuda()
+    not_ = torch.tensor(np.setdiff1d(np.arange(q.shape[0]), sees.cpu().numpy())).cuda()
+    other = torch.tensor(np.setdiff1d(np.arange(q.shape[0]), mine)).cuda()
+    low = kr.clone()
+    low[b + t, 5] = -3e38
+    none = kr.clone()
+    none[b + t, 5] = -np.inf
+    x, y = run_attn(lib, cache, q, k, low, v, cu, True), run_attn(lib, cache, q, k, none, v, cu, True)
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1]) and not torch.equal(x[0][sees], want[sees])
+    for bad in (np.inf, np.nan):
+        z = kr.clone()
+        z[b + t, 5] = bad
+        out, lse = run_attn(lib, cache, q, k, z, v, cu, True)
+        assert torch.isnan(out[sees].float()).all() and torch.isnan(lse[sees]).all()
+        assert torch.equal(out[other], want[other]) and torch.equal(lse[other], wl[other])
+        assert (out[not_].float() - want[not_].float()).abs().max() <= 4.1 * U * v[:sum(nk)].abs().max()
+        assert torch.allclose(lse[not_], wl[not_], rtol=2.0 ** -18, atol=2.0 ** -18)
+    for bad in (np.inf, -np.inf, np.nan):
+        z = v.clone()
+        z[b + t, hkv - 1, 7] = bad
+        out, lse = run_attn(lib, cache, q, k, kr, z, cu, True)
+        g = hq // hkv
+        hit = out[sees][:, hq - g:, 7].float()
+        assert torch.isnan(hit).all() if np.isnan(bad) else (hit == bad).all()
+        assert torch.equal(lse, wl) and torch.equal(out[other], want[other])
+        rest = [c for c in range(64) if c != 7]
+        assert torch.equal(out[..., rest], want[..., rest]) and torch.equal(out[:, :hq - g], want[:, :hq - g])
 
 
 def test_attn_without_keys_or_queries(lib):
