@@ -1052,6 +1052,131 @@ def test_prompts_then_steps(lib, bits):
         assert err.max() <= 0.25 * mix.max()
 
 
+@pytest.mark.parametrize("bits", [0, 8])
+def test_pools_past_32_bits(lib, bits):
+    """Pages whose first element (code) lies past 2^32 give what pages at the pool's start give."""
+    import torch
+    r, hq, lens = 512, 4, [200, 256]
+    rng = np.random.default_rng(8)
+    c, kr, q = bf16(rng.standard_normal((456, r))), bf16(rng.standard_normal((456, 64))), bf16(
+        rng.standard_normal((2, 1, hq, 192)))
+    B = bf16(rng.standard_normal((r, hq * 128)) / r ** 0.5)
+    seq, pos = i32(np.repeat([0, 1], lens)), i32(np.concatenate([np.arange(n) for n in lens]))
+    got = []
+    for n in (4, (1 << 16) + 4):                               # 2^16 pages of 128 x 512
+        cache = lib.lr_shared_create(lib.make_shared_desc(2, hq, hq, 128, 64, 128, r, 256, n_pages=n, quant_bits=bits), B, B)
+        lib.lr_shared_set_block_table(cache, np.array([[n - 1, n - 3], [n - 4, n - 2]]))
+        lib.lr_shared_append(cache, c, kr, seq, pos)
+        x, y, out = torch.zeros_like(c), torch.zeros_like(kr), torch.zeros((2, 1, hq, 128), dtype=torch.bfloat16, device="cuda")
+        k, v, z = torch.zeros((456, hq, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros(
+            (456, hq, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros_like(kr)
+        cu = i32([0, 200, 456])
+        lib.lr_shared_read(cache, cu, x, y)
+        lib.lr_shared_decode(cache, q, i32(lens), out)
+        lib.lr_shared_expand(cache, cu, k, v, z)
+        assert lib.lr_shared_device_error(cache) == 0
+        got.append((x, y, out, k, v, z))
+        lib.lr_shared_destroy(cache)
+    assert all(torch.equal(a, b) and a.any() for a, b in zip(*got))
+    assert np.array_equal(f64(got[1][0]), S.quantize_e4m3(f64(c)) if bits else f64(c))
+
+
+def test_results_past_32_bits(lib):
+    """Expanded rows, queries and outputs past element 2^31."""
+    import torch
+    H, n, parts = 128, 16900, 8
+    d = lib.make_shared_desc(parts, H, H, 128, 64, 128, 64, 17024, n_pages=133)        # all sequences share the pages
+    rng = np.random.default_rng(9)
+    Bk, Bv = bf16(rng.standard_normal((64, H * 128)) / 8), bf16(rng.standard_normal((64, H * 128)) / 8)
+    cache = lib.lr_shared_create(d, Bk, Bv)
+    c, kr = bf16(rng.standard_normal((n, 64))), bf16(rng.standard_normal((n, 64)))
+    lib.lr_shared_append(cache, c, kr, i32(np.zeros(n)), i32(np.arange(n)))
+    T = n * parts
+    k, v = (torch.zeros((T, H, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x = torch.zeros((T, 64), dtype=torch.bfloat16, device="cuda")
+    lib.lr_shared_expand(cache, i32(np.arange(parts + 1) * n), k, v, x)
+    assert lib.lr_shared_device_error(cache) == 0 and k.numel() > 1 << 31
+    c64 = f64(c[-70:])
+    for got, B in ((k, Bk), (v, Bv)):
+        assert all(torch.equal(got[i * n:(i + 1) * n], got[:n]) for i in range(1, parts))
+        want, mag = c64 @ f64(B), np.abs(c64) @ np.abs(f64(B))
+        assert np.all(np.abs(f64(got[-70:]).reshape(70, -1) - want) <= U * np.abs(want) + (64 + 8) * F * mag)
+    assert torch.equal(x, kr.repeat(parts, 1))
+    k, v, x = k[:340].clone(), v[:340].clone(), x[:340].clone()
+    nq = [131100, 100]
+    q = torch.randn((sum(nq), H, 192), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((sum(nq), H, 128), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((sum(nq), H), dtype=torch.float32, device="cuda")
+    lib.lr_shared_attn(cache, q, k, x, v, i32([0, nq[0], sum(nq)]), i32([0, 40, 340]), out, lse, causal=False)
+    assert lib.lr_shared_device_error(cache) == 0 and out.numel() > 1 << 31
+    for rows, keys in ((slice(0, 30), slice(0, 40)), (slice(131050, 131100), slice(0, 40)), (slice(131100, 131200), slice(40, 340))):
+        check_attn(q[rows], k[keys], x[keys], v[keys], [rows.stop - rows.start], [keys.stop - keys.start], False,
+                   192 ** -0.5, out[rows], lse[rows])
+
+
+@pytest.mark.parametrize("bits", [0, 8])
+def test_the_largest_batch(lib, bits):
+    """1024 sequences, most of them empty or of a few tokens."""
+    rng = np.random.default_rng(10)
+    lens = rng.integers(0, 4, 1024)
+    lens[[0, 31, 32, 500, 1023]] = 129, 0, 200, 256, 65
+    m = Layer(lib, [int(n) for n in lens], hq=2, hkv=1, r=64, dn=64, dr=32, dv=64, bits=bits, new=2, stale=False)
+    q = m.query(2)
+    m.check_decode(q, *m.decode(q))
+    k, v, kr, _ = run_expand(m, None, m.lens)
+    check_expand(m, [0] * 1024, m.lens, k, v, kr)
+    nq, nk = [int(n) for n in rng.integers(0, 3, 1024)], [int(n) for n in rng.integers(0, 4, 1024)]
+    nq[7], nk[7], nk[900] = 300, 400, 1000
+    case = attn_case(lib, nq, nk, 2, 2, 64, 32, 64)
+    check_attn(*case[1:5], nq, nk, True, 96 ** -0.5, *run_attn(lib, *case, True))
+
+
+@pytest.mark.parametrize("hq,r,bits", [(1, 64, 8), (7, 192, 8), (5, 512, 0)])
+def test_decode_of_fewer_tokens_than_the_cache_allows(lib, hq, r, bits):
+    m = Layer(lib, [300, 7, 64, 1], hq=hq, hkv=hq, r=r, dn=64, dv=64, bits=bits, new=8)
+    for n in range(1, 9):
+        q = m.query(n)
+        m.check_decode(q, *m.decode(q))
+
+
+@pytest.mark.parametrize("r,bits", [(192, 8), (512, 0), (512, 8)])
+def test_steps_captured_and_replayed(lib, r, bits):
+    """Two steps (append, lengths, decode) in one graph, replayed, against the same steps one by one."""
+    import torch
+    B, hq, reps = 3, 16, 20
+    rng = np.random.default_rng(6)
+    c, kr = bf16(rng.standard_normal((reps, 2, B, r)) * 3), bf16(rng.standard_normal((reps, 2, B, 64)))
+    q = bf16(rng.standard_normal((reps, 2, B, 1, hq, 192)))
+    got = []
+    for graph in (False, True):
+        m = Layer(lib, [100, 1, 250], hq=hq, hkv=hq, r=r, bits=bits, cap=512)
+        seq, lens = i32(np.arange(B)), i32(m.lens)
+        x, y, w = c[0].clone(), kr[0].clone(), q[0].clone()
+        out = torch.zeros((2, B, 1, hq, 128), dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros((2, B, 1, hq), dtype=torch.float32, device="cuda")
+
+        def steps():
+            for i in range(2):
+                lib.lr_shared_append(m.cache, x[i], y[i], seq, lens)
+                lens.add_(1)
+                lib.lr_shared_decode(m.cache, w[i], lens, out[i], lse[i])
+
+        m.decode(m.query(1))                                   # first launches outside the capture
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                steps()
+        res = []
+        for i in range(reps):
+            x.copy_(c[i]), y.copy_(kr[i]), w.copy_(q[i])
+            g.replay() if graph else steps()
+            res += [out.clone(), lse.clone()]
+        torch.cuda.synchronize()
+        assert lib.lr_shared_device_error(m.cache) == 0
+        got.append(res)
+    assert all(torch.equal(a, b) and a.any() for a, b in zip(*got))
+
+
 # ---------------------------------------------------------------------------
 # refusals
 # ---------------------------------------------------------------------------
