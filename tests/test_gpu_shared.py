@@ -1139,6 +1139,38 @@ def test_decode_of_fewer_tokens_than_the_cache_allows(lib, hq, r, bits):
         m.check_decode(q, *m.decode(q))
 
 
+def test_all_operators_at_once(lib):
+    """Decode, expansion, attention with split keys and without, each on a stream of its own, again and
+    again: they share SMs, shared memory and tensor memory, and wait for nobody but themselves."""
+    import torch
+    dec = Layer(lib, [900, 31, 400], hq=28, hkv=28, r=64, bits=8, dn=64, dr=32, dv=64)
+    exp = Layer(lib, [700, 1200], hq=4, hkv=4, r=64, dn=64, dr=32, dv=64, seed=1)
+    few = attn_case(lib, [200], [5000], 2, 2, 64, 32, 64)
+    many = attn_case(lib, [300, 700], [300, 700], 28, 28, 64, 32, 64)
+    q, lens, cu, main = dec.query(1), i32(dec.lens), i32(exp.cu), torch.cuda.current_stream()
+
+    def calls(s):
+        o = torch.zeros((3, 1, 28, 64), dtype=torch.bfloat16, device="cuda")
+        e = [torch.zeros((1900, *x), dtype=torch.bfloat16, device="cuda") for x in ((4, 64), (4, 64), (32,))]
+        a, b = (torch.zeros((c[1].shape[0], c[1].shape[1], 64), dtype=torch.bfloat16, device="cuda") for c in (few, many))
+        for t in s:
+            t.wait_stream(main)
+        lib.lr_shared_decode(dec.cache, q, lens, o, stream=s[0])
+        lib.lr_shared_expand(exp.cache, cu, *e, stream=s[1])
+        for c, y, t in ((few, a, s[2]), (many, b, s[3])):
+            lib.lr_shared_attn(*c[:5], *c[5], y, stream=t)
+        return [o, *e, a, b]
+
+    want = calls([main] * 4)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = [calls(streams) for _ in range(20)]
+    torch.cuda.synchronize()
+    for c in (dec.cache, exp.cache, few[0], many[0]):
+        assert lib.lr_shared_device_error(c) == 0
+    assert all(torch.equal(x, y) and y.any() for g in got for x, y in zip(g, want))
+
+
 @pytest.mark.parametrize("r,bits", [(192, 8), (512, 0), (512, 8)])
 def test_steps_captured_and_replayed(lib, r, bits):
     """Two steps (append, lengths, decode) in one graph, replayed, against the same steps one by one."""
