@@ -34,6 +34,7 @@
 #include "tc_common.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 namespace {
 
@@ -58,7 +59,7 @@ struct AttArgs {
   const int32_t* cu_q; const int32_t* cu_k;
   int nseq, total_q, total_k, Hq, g, dn, dv, dq, causal, stagger, slots, ring, split;   // slots: tile pairs a head; ring: 16 KB slots for keys and values;
                                                                                 // split: CTAs a tile pair
-  float scale_log2;
+  float scale_log2, scale_pow2;   // softmax scale times log2 e, and the largest power of two that is no larger
   __nv_bfloat16* out;
   float* lse;
   int* err;
@@ -339,8 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col = tmem + ((uint32_t)(qd * 32) << 16) + t * 128, o_col = s_col + 256;
     const int last = p.causal ? min(rk.n - 1, i + shift) : rk.n - 1;   // last key this query sees
     const int wlast = __shfl_sync(0xffffffffu, last, 0);                     // the warp's smallest
-    float m = kNoMax, l = 0.f;
-    bool ok = true, far = false;                   // far: some row of the warp has |m| > 2^24
+    // Weights are 2^(v cf + neg), by one fma a score v: with c = scale log2 e usually cf = c and neg = -m, m
+    // the rounded product of c and the largest v.  The fma's product is exact, so all weights of a row share a
+    // factor 2^x, |x| at most half a step of m, which their sum and so out and lse take part in.  From
+    // |m| = 2^31 on it could leave fp32; there scores that differ do so by 2^7 or more, so weights are 1 or
+    // nothing with any factor near c, and cf is a power of two, whose products are exact.
+    float m = kNoMax, neg = -kNoMax, cf = p.scale_log2, l = 0.f;
+    bool ok = true;
     for (int j = 0; j < nt[t]; ++j) {
       if (!(ok = wait_w(&aux->s_full[t][j & 1], (j >> 1) & 1, aux, p.err))) break;
       ptx::tc_fence_after();
@@ -380,12 +386,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 2; e < 32; e += 2) mx[c] = ptx::max3(mx[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
       }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      const float vmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), top = vmax * p.scale_log2;
       if (__any_sync(0xffffffffu, top > m + kLazy)) {
         const float mn = fmaxf(m, top), a = ptx::ex2_approx(m - mn);
+        if (top > m) {
+          cf = fabsf(top) < 2147483648.f ? p.scale_log2 : p.scale_pow2;
+          neg = -(vmax * cf);
+        }
         m = mn;
         l *= a;
-        far = __any_sync(0xffffffffu, fabsf(m) > 16777216.f && m > kNoMax);
         if (j > 0) {                               // (PV(j - 1) came before S(j), which is complete)
           for (int c = 0; c < p.dv; c += 16) {
             uint32_t o[16];
@@ -397,19 +406,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // Weights 2^(v c - m), by one fma a score.  m is a rounded product, so beyond 2^24 the exact v c of an
-      // fma is off from it by whole units, alike for a row's scores (at 2^35 by up to 2^11: every weight 0 or
-      // infinite).  There the products round first, as m did (from TMEM again and in a loop of its own: as a
-      // choice within the usual one it cost 2% of long prompts).
-      auto weights = [&](int c, const uint32_t (&x)[32], float2 sc) {
-        const float2 nm = make_float2(-m, -m);
+      const float2 sc = make_float2(cf, cf), nm = make_float2(neg, neg);
+      float2 sum[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
         uint32_t w[16];
-        float2 sum = make_float2(0.f, 0.f);
+        sum[c] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float2 z = ptx::fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc, nm);
-          const float2 y = make_float2(ptx::ex2_approx(z.x), ptx::ex2_approx(z.y));
-          sum = ptx::add2(sum, y);
+          const float2 x = ptx::fma2(make_float2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), sc, nm);
+          const float2 y = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
+          sum[c] = ptx::add2(sum[c], y);
           const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
           w[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
@@ -420,25 +427,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&aux->p_full[t][c >> 1][j & 1]);
         }
-        return sum;
-      };
-      float2 sum[4];
-      if (far) {
-        sum[1] = sum[2] = sum[3] = make_float2(0.f, 0.f);
-        sum[0] = sum[1];
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[32];
-          ptx::tmem_ld32(s_col + 32 * c, x);       // (the weights so far lie below these columns)
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            x[e] = 32 * c + e <= lim ? __float_as_uint(__uint_as_float(x[e]) * p.scale_log2) : 0xFF800000u;
-          sum[0] = ptx::add2(sum[0], weights(c, x, make_float2(1.f, 1.f)));
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sum[c] = weights(c, v[c], make_float2(p.scale_log2, p.scale_log2));
       }
       const float2 l2 = ptx::add2(ptx::add2(sum[0], sum[1]), ptx::add2(sum[2], sum[3]));
       l += l2.x + l2.y;
@@ -585,6 +573,7 @@ cudaError_t launch_shared_attn(lr_shared* c, const void* q, const void* k, const
   a.dq = d.dim_nope + d.dim_rope;
   a.causal = causal;
   a.scale_log2 = c->scale_log2;
+  a.scale_pow2 = std::scalbn(1.f, std::ilogb(a.scale_log2));
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.err = c->dev_err;

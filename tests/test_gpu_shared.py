@@ -527,7 +527,8 @@ def test_decodes_of_two_caches_at_once(lib):
 
 # Scores from the rotary part alone, 8 bits times a power of two and so exact in fp32: far from zero on
 # either side.  (sign, power): sign 2^power or, where its product with log2(e) rounds, 165/128 of it.
-FAR = [(s * f, p) for f in (1.0, 165 / 128) for s, p in ((-1, 110), (-1, 60), (-1, 35), (1, 35), (1, 110))]
+FAR = [(s * f, p) for f in (1.0, 165 / 128) for s, p in ((-1, 110), (-1, 60), (-1, 35), (1, 35), (1, 110))] + [
+    (s * 165 / 128, p) for s, p in ((-1, 32), (-1, 30), (1, 29), (-1, 25))]
 
 
 def far_scores(n, sign, power):
