@@ -355,7 +355,9 @@ typedef struct lr_shared lr_shared;   /* opaque */
 
 /* lr_shared_create — allocate a cache (zeroed pages; page (b * capacity/128 + j) % n_pages for
  *   span j of sequence b) and copy the bases B_k [r][Hkv * dn], B_v [r][Hkv * dv] (bf16, device).
- *   Errors as for lr_cache_create.  The decode's scratch is part of the cache: at most
+ *   Errors as for lr_cache_create.  The bases are kept twice, as they are and transposed (for
+ *   lr_shared_expand), 2 r Hkv (dn + dv) elements in all; rope_theta > 0 adds a table of
+ *   capacity * dr floats.  The decode's scratch is part of the cache: at most
  *   (148 / k + batch) * Hq * max_queries rows (padded to 16 or 32 k) of r floats, k being the
  *   blocks of 32 query rows of a sequence.  Blocks until the copies end.
  * lr_shared_destroy — synchronise the device and free all memory.  NULL is a no-op. */

@@ -20,8 +20,8 @@
 // (2560 clocks at 192 + 128) against 2048 clocks of exponentials on the same SM.  Measured: ~4300
 // clocks (per query tile: 1200 from the first MMA of S to its softmax, 1700 of softmax, 300 to
 // the last MMA of PV, and the keys of the next tile, which wait on values of the last).  Two
-// sequences of 8192 tokens, 28 heads, causal: 1.07 ms, 1.12 PFLOP/s in a short burst, 1.27 ms run
-// continuously, at the card's power limit (1000 W, 1.65 GHz).  In bursts, with two fixed stages for
+// sequences of 8192 tokens, 28 heads, causal: 1.02 ms, 1.18 PFLOP/s in a short burst, 1.19 ms run
+// continuously, at the card's power limit (1000 W).  In bursts, with two fixed stages for
 // keys and one for values 1.22 ms; with a barrier per 64-column box of keys 1.24 ms (a test between
 // MMAs costs more than the earlier start gains).
 //
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (512 new tokens over 4096: 100 us against 116; over 32768: 637 against 675; 1280 over 16000: 320
         // against 350).  In several waves the tiles drift apart by themselves and the wait costs (prompts of
         // 4096: 158 us with it, 141 without; 16384: 2.2 and 2.1 ms), and so it does over a few key tiles
-        // (seven prompts of up to 400 tokens: 28.8 and 26.7 us).
+        // (seven prompts of up to 400 tokens: 28.8 and 26.7 us; the border of four is from these and the above).
         if (!k_in && !(ok = wait_w(&aux->k_full[s], ph, aux, p.err))) break;
         if (t == 1 && p.stagger && ntk > 4 && j < nt[0] && !(ok = wait_w(&aux->p_full[0][0][s], ph, aux, p.err))) break;
         ptx::tc_fence_after();
@@ -591,8 +591,10 @@ cudaError_t launch_shared_attn(lr_shared* c, const void* q, const void* k, const
   const int nqb = (a.dq + 63) / 64, unit = a.dn / 64 + 1 + a.dv / 64;
   a.ring = std::min(2 * unit, (int)((tc::kSmemLimit - kAuxBytes) / kBox) - 2 * nqb);
   const size_t smem = kAuxBytes + (size_t)(2 * nqb + a.ring) * kBox;
-  // Split the keys while the CTAs still are one wave and keep two key tiles each (by the average).  4 heads,
-  // 512 new tokens over 8192: 158 us without, 38 with a split of 8; 28 heads, 256 over 30000: 597 and 341.
+  // Split the keys while there are SMs for all parts and each keeps two key tiles (by the average).  Timed
+  // alone, in short bursts: 4 heads, 512 new tokens over 8192: 158 us without, 38 with a split of 8; 28 heads,
+  // 256 over 30000: 597 without, 325 in two parts.  (A cluster lies in one GPC: 15 of 8 CTAs run at once, so
+  // 16 to 18 take two waves, and as long as in fours: 200 over 30000 with 15 heads 96 us, 16 to 18 187, 19 179.)
   a.split = 1;
   while (a.split < kMaxSplit && 2 * a.split * slots * a.Hq <= c->num_sms && total_k / (256 * nseq) >= 2 * a.split) a.split *= 2;
   return a.split > 1 ? launch<true>(a, smem, s, tq, tk, tkr, tv) : launch<false>(a, smem, s, tq, tk, tkr, tv);
